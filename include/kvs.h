@@ -343,6 +343,110 @@ kvs_status kvs_select_blocks_noalloc(const kvs_config* cfg, const void* d_score_
  * Errors: KVS_ERR_INVALID_ARG. */
 kvs_status kvs_quantize_e4m3(const void* d_src_bf16, void* d_dst, size_t n, float scale, kvs_stream_t stream);
 
+/* ------------------------------------------------------------------ caches resident in device memory
+ * A kvs_pool is a paged KV cache that stays whole in device memory (no host history): the layers,
+ * requests or prompt prefixes whose K/V need no offloading.  It lives beside a kvs_ctx in a model
+ * whose other layers decode sparsely from host memory, and shares its terms: blocks of block_size
+ * tokens, slots that hold a block, and block2slot tables.
+ *
+ * Layouts (row-major):
+ *   K pool, V pool [n_layer][n_slots][H_kv][block_size][d]  bf16 or E4M3 codes, caller-owned
+ *   q              [n_tok] tokens of [H_q][d] bf16, q_stride elements apart
+ *   out            [n_tok][H_q][d] bf16;  lse [n_tok][H_q] fp32 (natural log; -inf for an empty row)
+ *   cu_q           [n_req + 1] int32: request r's query tokens are rows [cu_q[r], cu_q[r + 1])
+ *   ctx_len        [n_req] int32: tokens request r has in the pool, its query tokens included
+ *   block2slot     [n_req][nb_max] int32, nb_max = ceil(max_ctx / block_size): the slot of each block
+ *   weight         [n_req][H_kv][max_ctx] fp32: softmax weight each key has received
+ * All counts, lengths and tables are read on the device, so a captured graph replays with new ones.
+ *
+ * Query token i of request r, with q_r = cu_q[r + 1] - cu_q[r], stands at position
+ * p = ctx_len[r] - q_r + i: the request's query tokens are the last of its context (kvs_pool_append
+ * puts their K/V there).  A row that sees no key (p < 0, an empty context) gives zeros and lse -inf.
+ * Rows of `out` and `lse` that belong to no request are left as they are.  K/V of keys that no row of the
+ * call sees (past the context end, outside every window, in blocks whose table entry is -1) are
+ * never used and may hold anything; keys that some row sees must be finite.
+ *
+ * Supported: head dim 64 or 128; block_size 16, 32, 64 or 128; 1 to 128 query heads per kv head;
+ * max_req <= 4096 with max_req * n_kv_head <= 65535.
+ * Calls are asynchronous on `stream` and capturable; the workspace is scratch of one call at a time,
+ * so calls on one kvs_pool must not overlap on the GPU, captured graphs that hold them included
+ * (a second kvs_pool over the same K/V memory, with a workspace of its own, may run beside it).
+ * The current device must be the one the pool was created on (else KVS_ERR_INVALID_ARG).  Errors found on
+ * the device set a sticky word that kvs_pool_poll_error reads: KVS_ERR_BAD_INDEX for offsets that
+ * are not ascending within [0, n_tok], a length outside [0, max_ctx], or a slot outside
+ * [0, n_slots) of a block that is needed (nothing outside the pool is read or written; the results
+ * of that request are unspecified), KVS_ERR_TIMEOUT for a device wait that ran out. */
+typedef struct {
+  int n_layer, n_slots;
+  int n_q_head, n_kv_head, head_dim, block_size;
+  int max_ctx;                /* tokens per request (the tables' and weights' extent) */
+  int max_req, max_tokens;    /* largest n_req and n_tok of a call */
+  int max_prefix_tokens;      /* largest n_tok of kvs_pool_prefix_attn; 0: it is not called */
+  int kv_dtype;               /* KVS_KV_BF16 or KVS_KV_FP8_E4M3 */
+  float k_scale, v_scale;     /* E4M3: as in kvs_config (0 -> 1) */
+  float softmax_scale;        /* 0 -> 1/sqrt(head_dim) */
+  unsigned wait_timeout_us;   /* bound on device waits (0 -> 2000000 us) */
+} kvs_pool_config;
+
+typedef struct kvs_pool kvs_pool;
+
+/* Device bytes the workspace of `cfg` needs (0 when cfg is invalid or not supported). */
+size_t kvs_pool_workspace_bytes(const kvs_pool_config* cfg);
+
+/* Bind a pool to its K/V memory (256-byte aligned device pointers, both of n_layer * n_slots * H_kv *
+ * block_size * head_dim elements; never written but by kvs_pool_append and kvs_pool_evict) and to a
+ * workspace (>= kvs_pool_workspace_bytes, 256-byte aligned).  Synchronous; on the current device. */
+kvs_status kvs_pool_create(const kvs_pool_config* cfg, void* d_k, void* d_v, void* d_workspace,
+                           size_t workspace_bytes, kvs_pool** out);
+kvs_status kvs_pool_destroy(kvs_pool* pool);
+
+/* Read and clear the sticky device status word, as kvs_poll_error. */
+kvs_status kvs_pool_poll_error(kvs_pool* pool, kvs_status* device_status);
+
+/* Number of kernels this pool has launched (or captured into graphs) so far. */
+unsigned long long kvs_pool_launch_count(kvs_pool* pool);
+
+/* Write the K/V rows of every request's query tokens to their positions in the pool: k_new, v_new
+ * [n_tok] tokens of [H_kv][d] bf16, kv_stride elements apart (a multiple of 8, 16-byte aligned);
+ * E4M3 pools quantise them with the rule of kvs_quantize_e4m3. */
+kvs_status kvs_pool_append(kvs_pool* pool, int layer, const void* d_k_new, const void* d_v_new, long long kv_stride,
+                           const int* d_cu_q, const int* d_ctx_len, const int* d_block2slot, int n_req, int n_tok,
+                           kvs_stream_t stream);
+
+/* Causal attention, optionally with a sliding window: the row at position p attends to the keys t <= p
+ * with p - t < window (window 0: no limit) or t < n_sink (the first tokens, which stay visible).
+ *   out = sum_t softmax_t(scale * q . k_t) v_t,  lse = ln sum_t exp(scale * q . k_t)
+ * d_lse may be NULL.  d_weight (may be NULL) accumulates the softmax weight of each key over the rows
+ * and heads of the call: weight[r][h][t] of a key before the request's query tokens is added to, that
+ * of the query tokens themselves (positions ctx_len - q_r and up) is set; entries >= ctx_len are left.
+ * q_stride: a multiple of 8, >= H_q * d; d_q and d_out 16-byte aligned. */
+kvs_status kvs_pool_attn(kvs_pool* pool, int layer, const void* d_q, long long q_stride, const int* d_cu_q,
+                         const int* d_ctx_len, const int* d_block2slot, int n_req, int n_tok, int window, int n_sink,
+                         void* d_out, float* d_lse, float* d_weight, kvs_stream_t stream);
+
+/* Attention of a batch whose requests share prefixes: the requests [prefix_req[i], prefix_req[i + 1])
+ * see all prefix_len[i] tokens of prefix i (its blocks in prefix2slot [n_prefix][nb_max], once in
+ * the pool), then their own context causally as kvs_pool_attn without a window (ctx_len and positions
+ * count a request's own tokens only).  Requests before prefix_req[0] or from prefix_req[n_prefix] on
+ * have no prefix.  prefix_req [n_prefix + 1], ascending within [0, n_req]; n_prefix <= max_req; n_tok <=
+ * max_prefix_tokens.  A prefix's K/V is read once for all its requests. */
+kvs_status kvs_pool_prefix_attn(kvs_pool* pool, int layer, const void* d_q, long long q_stride, const int* d_cu_q,
+                                const int* d_ctx_len, const int* d_block2slot, int n_req, int n_tok,
+                                const int* d_prefix_req, const int* d_prefix_len, const int* d_prefix2slot, int n_prefix,
+                                void* d_out, float* d_lse, kvs_stream_t stream);
+
+/* Cut caches down to the tokens that matter: per request and kv head keep the first n_sink and the last
+ * n_recent tokens and, of the others, those with the largest weight, min(keep, ctx_len) in all (ties:
+ * the earlier token; NaN lowest), in their order, and gather their K/V rows into the blocks of
+ * dst2slot [n_req][nb_max], which must be disjoint from every block the call reads.
+ *   kept [n_req][H_kv][keep]   the kept tokens' indices, ascending (entries past n_kept are left)
+ *   n_kept [n_req]             min(keep, ctx_len): the new context length
+ *   weight_out [n_req][H_kv][max_ctx], another buffer than weight: the kept tokens' weights, in order
+ * n_sink + n_recent <= keep <= max_ctx. */
+kvs_status kvs_pool_evict(kvs_pool* pool, int layer, const float* d_weight, const int* d_ctx_len,
+                          const int* d_block2slot, int n_req, int keep, int n_sink, int n_recent, const int* d_dst2slot,
+                          int* d_kept, int* d_n_kept, float* d_weight_out, kvs_stream_t stream);
+
 /* Library version string. */
 const char* kvs_version(void);
 

@@ -27,6 +27,8 @@ What it computes, written plainly (numpy, fp64 where the arithmetic is floating 
                restore for speculative rollback (KV-cache overview, section 6.1).
   attention    exact softmax attention over the selected tokens (OasisKV page, key module 1;
                HiSparse page, insight 1: outputs identical to full KV in HBM).
+  pool         attention over one request's cached tokens (window, first tokens, shared prefix, summed
+               weights) and the eviction rule of the device-resident pools.
   step         one decode step over all layers: append, score, select, update, prefetch,
                attend -- sync mode and lookahead-draft mode.
 
@@ -42,11 +44,12 @@ from .select import forced_blocks, select_blocks
 from .cache import (UnitCache, UpdateResult, PrefetchResult, cache_restore, cache_update, importance_key,
                     layer_prefetch)
 from .attention import attend
+from .pool import pool_attend, pool_kept
 from .step import OracleDecoder, UnitRecord
 
 __all__ = [
     "bf16_to_f32", "bf16_to_f64", "f32_to_bf16_rne", "kv_cache_bytes", "kv_cache_bytes_variant",
     "index_keys", "index_key_block", "index_minmax", "index_minmax_block", "block_scores", "block_scores_bound", "forced_blocks", "select_blocks", "UnitCache",
     "UpdateResult", "PrefetchResult", "cache_update", "cache_restore", "importance_key", "layer_prefetch", "attend", "OracleDecoder",
-    "UnitRecord",
+    "UnitRecord", "pool_attend", "pool_kept",
 ]

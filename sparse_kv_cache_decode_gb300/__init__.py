@@ -45,12 +45,21 @@ class KvsStats(ctypes.Structure):
                 ("hits", "misses", "evictions", "prefetched", "prefetch_hits", "pin_fallbacks", "bytes_fetched")]
 
 
+
+class KvsPoolConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in
+                ("n_layer", "n_slots", "n_q_head", "n_kv_head", "head_dim", "block_size", "max_ctx", "max_req",
+                 "max_tokens", "max_prefix_tokens", "kv_dtype")] + \
+               [("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float), ("softmax_scale", ctypes.c_float),
+                ("wait_timeout_us", ctypes.c_uint)]
+
+
 STATS_FIELDS = [f[0] for f in KvsStats._fields_]
 
 _lib = None
 
 # name -> (restype, argtypes)
-_P, _I, _U = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint
+_P, _I, _U, _LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_longlong
 _SIGS = {
     "kvs_version": (ctypes.c_char_p, []),
     "kvs_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(KvsConfig)]),
@@ -79,6 +88,15 @@ _SIGS = {
     "kvs_select_blocks_noalloc": (_I, [ctypes.POINTER(KvsConfig), _P, _I, _P, _P, _P, _P, _P, _P]),
     "kvs_probe_host_read": (_I, [_P, ctypes.c_size_t, _P, _I, _I, _I, _I, _P, _P]),
     "kvs_quantize_e4m3": (_I, [_P, _P, ctypes.c_size_t, ctypes.c_float, _P]),
+    "kvs_pool_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(KvsPoolConfig)]),
+    "kvs_pool_create": (_I, [ctypes.POINTER(KvsPoolConfig), _P, _P, _P, ctypes.c_size_t, ctypes.POINTER(_P)]),
+    "kvs_pool_destroy": (_I, [_P]),
+    "kvs_pool_poll_error": (_I, [_P, ctypes.POINTER(_I)]),
+    "kvs_pool_launch_count": (ctypes.c_ulonglong, [_P]),
+    "kvs_pool_append": (_I, [_P, _I, _P, _P, _LL, _P, _P, _P, _I, _I, _P]),
+    "kvs_pool_attn": (_I, [_P, _I, _P, _LL, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "kvs_pool_prefix_attn": (_I, [_P, _I, _P, _LL, _P, _P, _P, _I, _I, _P, _P, _P, _I, _P, _P, _P]),
+    "kvs_pool_evict": (_I, [_P, _I, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
 }
 
 KERNEL_IDS = {"score": 1, "topk": 2, "update": 3, "fetch": 4, "attn": 5, "prefetch": 6, "append": 7, "index": 8}
@@ -464,3 +482,10 @@ def quantize_history_e4m3(src_host, dst_host, scale: float, chunk: int = 1 << 28
 
 def version() -> str:
     return lib().kvs_version().decode()
+
+
+def __getattr__(name):   # the pool binding imports torch: on first use
+    if name in ("Pool", "make_pool_config"):
+        from . import pool
+        return getattr(pool, name)
+    raise AttributeError(name)

@@ -1,0 +1,276 @@
+// Device-resident KV pools, host side: configuration checks, workspace carving and the C-ABI entry points.
+#include <math.h>
+
+#include <new>
+
+#include "kvs_pool.cuh"
+
+using namespace kvs;
+
+struct kvs_pool {
+  PoolDims d;
+  unsigned char *k, *v;     // [n_layer][n_slots][H_kv][bs][d]
+  size_t layer_bytes;
+  int device;
+  unsigned* err;
+  float *lse2, *prev_lse2, *prev_out;
+  void* scratch;
+  CUtensorMap* maps;        // per layer: K, V
+  unsigned long long launches;
+};
+
+namespace {
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool pool_dims(const kvs_pool_config* c, PoolDims* d) {
+  if (!c) return false;
+  if (c->n_layer < 1 || c->n_layer > 1024 || c->n_slots < 1) return false;
+  if (c->n_q_head < 1 || c->n_kv_head < 1 || c->n_kv_head > 1024 || c->n_q_head % c->n_kv_head) return false;
+  if (c->n_q_head / c->n_kv_head > 128) return false;
+  if (c->head_dim != 64 && c->head_dim != 128) return false;
+  if (c->block_size != 16 && c->block_size != 32 && c->block_size != 64 && c->block_size != 128) return false;
+  if (c->max_ctx < 1 || c->max_ctx > (1 << 30) || c->max_req < 1 || c->max_req > 4096) return false;
+  if ((long long)c->max_req * c->n_kv_head > 65535) return false;   // (request, kv head) pairs are a grid dimension
+  if (c->max_tokens < 1 || c->max_tokens > (1 << 24)) return false;
+  if (c->max_prefix_tokens < 0 || c->max_prefix_tokens > c->max_tokens) return false;
+  if (c->kv_dtype != KVS_KV_BF16 && c->kv_dtype != KVS_KV_FP8_E4M3) return false;
+  if (!(c->softmax_scale >= 0.f) || isinf(c->softmax_scale)) return false;
+  if (!(c->k_scale >= 0.f) || !(c->v_scale >= 0.f) || isinf(c->k_scale) || isinf(c->v_scale)) return false;
+  // rows of a layer are tensor-load coordinates (32 bits), and row tiles are counted in 32 bits
+  if ((long long)c->n_slots * c->n_kv_head * c->block_size > 0x7fff0000ll) return false;
+  if ((long long)c->max_tokens * (c->n_q_head / c->n_kv_head) > 0x7fff0000ll) return false;
+  d->NL = c->n_layer;
+  d->n_slots = c->n_slots;
+  d->Hq = c->n_q_head;
+  d->Hkv = c->n_kv_head;
+  d->G = c->n_q_head / c->n_kv_head;
+  d->d = c->head_dim;
+  d->bs = c->block_size;
+  d->log2bs = 0;
+  while ((1 << d->log2bs) < d->bs) ++d->log2bs;
+  d->max_ctx = c->max_ctx;
+  d->nb_max = (c->max_ctx + c->block_size - 1) / c->block_size;
+  d->max_req = c->max_req;
+  d->max_tokens = c->max_tokens;
+  d->max_prefix_tokens = c->max_prefix_tokens;
+  d->fp8 = c->kv_dtype == KVS_KV_FP8_E4M3;
+  d->ebytes = d->fp8 ? 1 : 2;
+  d->scale = c->softmax_scale > 0.f ? c->softmax_scale : (float)(1.0 / sqrt((double)c->head_dim));
+  d->k_scale = d->fp8 && c->k_scale > 0.f ? c->k_scale : 1.f;
+  d->v_scale = d->fp8 && c->v_scale > 0.f ? c->v_scale : 1.f;
+  d->timeout_us = c->wait_timeout_us ? c->wait_timeout_us : 2000000u;
+  return true;
+}
+
+struct PoolPlan {
+  size_t err, lse2, prev_lse2, prev_out, scratch, total;
+};
+PoolPlan pool_plan(const PoolDims& d) {
+  PoolPlan p;
+  p.err = align_up(16);
+  p.lse2 = align_up((size_t)d.max_tokens * d.Hq * 4);
+  p.prev_lse2 = align_up((size_t)d.max_prefix_tokens * d.Hq * 4);
+  p.prev_out = align_up((size_t)d.max_prefix_tokens * d.Hq * d.d * 4);
+  p.scratch = align_up(pool_attn_scratch_bytes(d));
+  p.total = p.err + p.lse2 + p.prev_lse2 + p.prev_out + p.scratch;
+  return p;
+}
+
+inline cudaStream_t S(kvs_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+inline kvs_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KVS_OK : KVS_ERR_CUDA; }
+
+// Arguments every call on a layer shares.
+bool call_ok(const kvs_pool* p, int layer, int n_req) {
+  if (!p || layer < 0 || layer >= p->d.NL || n_req < 0 || n_req > p->d.max_req) return false;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return dev == p->device;
+}
+
+bool query_ok(const kvs_pool* p, const void* q, long long q_stride, const int* cu_q, const int* ctx_len,
+              const int* table, const void* out) {
+  if (!q || !cu_q || !ctx_len || !table || !out) return false;
+  return aligned16(q) && aligned16(out) && q_stride % 8 == 0 && q_stride >= (long long)p->d.Hq * p->d.d;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kvs_pool_workspace_bytes(const kvs_pool_config* cfg) {
+  PoolDims d;
+  if (!pool_dims(cfg, &d)) return 0;
+  return pool_plan(d).total;
+}
+
+kvs_status kvs_pool_create(const kvs_pool_config* cfg, void* d_k, void* d_v, void* d_workspace,
+                           size_t workspace_bytes, kvs_pool** out) {
+  if (!out) return KVS_ERR_INVALID_ARG;
+  *out = nullptr;
+  PoolDims d;
+  if (!pool_dims(cfg, &d)) return KVS_ERR_INVALID_ARG;
+  const PoolPlan p = pool_plan(d);
+  if (!d_k || !d_v || !d_workspace || workspace_bytes < p.total) return KVS_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return KVS_ERR_CUDA;
+  }
+  for (void* x : {d_k, d_v, d_workspace}) {
+    cudaPointerAttributes a;
+    if (reinterpret_cast<uintptr_t>(x) % kAlign) return KVS_ERR_INVALID_ARG;
+    if (cudaPointerGetAttributes(&a, x) != cudaSuccess || a.type != cudaMemoryTypeDevice || a.device != dev) {
+      cudaGetLastError();
+      return KVS_ERR_INVALID_ARG;
+    }
+  }
+  kvs_pool* c = new (std::nothrow) kvs_pool();
+  if (!c) return KVS_ERR_INVALID_ARG;
+  c->maps = new (std::nothrow) CUtensorMap[2 * (size_t)d.NL];
+  if (!c->maps) {
+    delete c;
+    return KVS_ERR_INVALID_ARG;
+  }
+  c->d = d;
+  c->k = static_cast<unsigned char*>(d_k);
+  c->v = static_cast<unsigned char*>(d_v);
+  c->layer_bytes = (size_t)d.n_slots * d.Hkv * d.bs * d.d * d.ebytes;
+  c->device = dev;
+  c->launches = 0;
+  unsigned char* b = static_cast<unsigned char*>(d_workspace);
+  c->err = reinterpret_cast<unsigned*>(b); b += p.err;
+  c->lse2 = reinterpret_cast<float*>(b); b += p.lse2;
+  c->prev_lse2 = reinterpret_cast<float*>(b); b += p.prev_lse2;
+  c->prev_out = reinterpret_cast<float*>(b); b += p.prev_out;
+  c->scratch = b;
+  // each layer's rows [n_slots * H_kv * bs][d]; a load brings up to one block's rows of 128 bytes
+  const uint64_t rows = (uint64_t)d.n_slots * d.Hkv * d.bs;
+  const uint32_t inner = (uint32_t)(d.d < 128 / d.ebytes ? d.d : 128 / d.ebytes);
+  for (int l = 0; l < d.NL; ++l)
+    for (int x = 0; x < 2; ++x)
+      if (!make_tmap_2d(&c->maps[2 * l + x], (x ? c->v : c->k) + l * c->layer_bytes, (uint64_t)d.d, rows, inner,
+                        (uint32_t)d.bs, d.ebytes)) {
+        kvs_pool_destroy(c);
+        return KVS_ERR_CUDA;
+      }
+  if (cudaMemset(c->err, 0, p.err) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+    kvs_pool_destroy(c);
+    return KVS_ERR_CUDA;
+  }
+  *out = c;
+  return KVS_OK;
+}
+
+kvs_status kvs_pool_destroy(kvs_pool* c) {
+  if (!c) return KVS_ERR_INVALID_ARG;
+  delete[] c->maps;
+  delete c;
+  return KVS_OK;
+}
+
+kvs_status kvs_pool_poll_error(kvs_pool* c, kvs_status* device_status) {
+  if (!c || !device_status || !call_ok(c, 0, 0)) return KVS_ERR_INVALID_ARG;
+  unsigned v = 0;
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpy(&v, c->err, sizeof(v), cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess) e = cudaMemset(c->err, 0, sizeof(v));
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  *device_status = static_cast<kvs_status>(v);
+  return cuda_status(e);
+}
+
+unsigned long long kvs_pool_launch_count(kvs_pool* c) { return c ? c->launches : 0ull; }
+
+kvs_status kvs_pool_append(kvs_pool* c, int layer, const void* d_k_new, const void* d_v_new, long long kv_stride,
+                           const int* d_cu_q, const int* d_ctx_len, const int* d_block2slot, int n_req, int n_tok,
+                           kvs_stream_t stream) {
+  if (!call_ok(c, layer, n_req) || n_tok < 0 || n_tok > c->d.max_tokens) return KVS_ERR_INVALID_ARG;
+  const PoolDims& d = c->d;
+  if (n_req == 0 || n_tok == 0) return KVS_OK;
+  if (!d_k_new || !d_v_new || !d_cu_q || !d_ctx_len || !d_block2slot) return KVS_ERR_INVALID_ARG;
+  if (kv_stride % 8 || kv_stride < (long long)d.Hkv * d.d) return KVS_ERR_INVALID_ARG;
+  if (!aligned16(d_k_new) || !aligned16(d_v_new)) return KVS_ERR_INVALID_ARG;
+  const PoolSeqs q = {d_cu_q, nullptr, d_ctx_len, d_block2slot, n_req, n_req, n_tok, 1, 0, 0};
+  c->launches += 1;
+  return cuda_status(launch_pool_append(d, c->k + layer * c->layer_bytes, c->v + layer * c->layer_bytes,
+                                        static_cast<const __nv_bfloat16*>(d_k_new),
+                                        static_cast<const __nv_bfloat16*>(d_v_new), kv_stride, q, c->err, S(stream)));
+}
+
+kvs_status kvs_pool_attn(kvs_pool* c, int layer, const void* d_q, long long q_stride, const int* d_cu_q,
+                         const int* d_ctx_len, const int* d_block2slot, int n_req, int n_tok, int window, int n_sink,
+                         void* d_out, float* d_lse, float* d_weight, kvs_stream_t stream) {
+  if (!call_ok(c, layer, n_req) || window < 0 || n_sink < 0) return KVS_ERR_INVALID_ARG;
+  const PoolDims& d = c->d;
+  if (n_tok < 0 || n_tok > d.max_tokens) return KVS_ERR_INVALID_ARG;
+  if (n_req == 0 || n_tok == 0) return KVS_OK;
+  if (!query_ok(c, d_q, q_stride, d_cu_q, d_ctx_len, d_block2slot, d_out)) return KVS_ERR_INVALID_ARG;
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(d_q);
+  const unsigned char* k = c->k + layer * c->layer_bytes;
+  const PoolSeqs seqs = {d_cu_q, nullptr, d_ctx_len, d_block2slot, n_req, n_req, n_tok, 1, window, n_sink};
+  const PoolAttnOut o = {static_cast<__nv_bfloat16*>(d_out), d_lse, d_weight ? c->lse2 : nullptr, nullptr, nullptr, nullptr,
+                         nullptr, 0};
+  int n = 0;
+  cudaError_t e = launch_pool_attn(d, k, c->v + layer * c->layer_bytes, &c->maps[2 * layer], q, q_stride, seqs, o,
+                                   c->scratch, c->err, S(stream), &n);
+  c->launches += n;
+  if (e == cudaSuccess && d_weight) {
+    e = launch_pool_weight(d, k, &c->maps[2 * layer], q, q_stride, seqs, c->lse2, d_weight, c->err, S(stream));
+    c->launches += 1;
+  }
+  return cuda_status(e);
+}
+
+kvs_status kvs_pool_prefix_attn(kvs_pool* c, int layer, const void* d_q, long long q_stride, const int* d_cu_q,
+                                const int* d_ctx_len, const int* d_block2slot, int n_req, int n_tok,
+                                const int* d_prefix_req, const int* d_prefix_len, const int* d_prefix2slot, int n_prefix,
+                                void* d_out, float* d_lse, kvs_stream_t stream) {
+  if (!call_ok(c, layer, n_req) || n_prefix < 0 || n_prefix > c->d.max_req) return KVS_ERR_INVALID_ARG;
+  const PoolDims& d = c->d;
+  if (n_tok < 0 || n_tok > d.max_prefix_tokens) return KVS_ERR_INVALID_ARG;
+  if (n_req == 0 || n_tok == 0) return KVS_OK;
+  if (!query_ok(c, d_q, q_stride, d_cu_q, d_ctx_len, d_block2slot, d_out)) return KVS_ERR_INVALID_ARG;
+  if (n_prefix > 0 && (!d_prefix_req || !d_prefix_len || !d_prefix2slot)) return KVS_ERR_INVALID_ARG;
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(d_q);
+  const unsigned char *k = c->k + layer * c->layer_bytes, *v = c->v + layer * c->layer_bytes;
+  cudaError_t e = cudaSuccess;
+  int n = 0;
+  if (n_prefix > 0) {
+    const PoolSeqs pre = {d_cu_q, d_prefix_req, d_prefix_len, d_prefix2slot, n_prefix, n_req, n_tok, 0, 0, 0};
+    const PoolAttnOut o = {nullptr, nullptr, c->prev_lse2, c->prev_out, nullptr, nullptr, nullptr, 0};
+    e = launch_pool_attn(d, k, v, &c->maps[2 * layer], q, q_stride, pre, o, c->scratch, c->err, S(stream), &n);
+    c->launches += n;
+  }
+  if (e == cudaSuccess) {
+    const PoolSeqs own = {d_cu_q, nullptr, d_ctx_len, d_block2slot, n_req, n_req, n_tok, 1, 0, 0};
+    const PoolAttnOut o = {static_cast<__nv_bfloat16*>(d_out), d_lse, nullptr, nullptr, c->prev_out, c->prev_lse2,
+                           d_prefix_req, n_prefix};
+    e = launch_pool_attn(d, k, v, &c->maps[2 * layer], q, q_stride, own, o, c->scratch, c->err, S(stream), &n);
+    c->launches += n;
+  }
+  return cuda_status(e);
+}
+
+kvs_status kvs_pool_evict(kvs_pool* c, int layer, const float* d_weight, const int* d_ctx_len,
+                          const int* d_block2slot, int n_req, int keep, int n_sink, int n_recent, const int* d_dst2slot,
+                          int* d_kept, int* d_n_kept, float* d_weight_out, kvs_stream_t stream) {
+  if (!call_ok(c, layer, n_req)) return KVS_ERR_INVALID_ARG;
+  const PoolDims& d = c->d;
+  if (keep < 1 || keep > d.max_ctx || n_sink < 0 || n_recent < 0 || n_sink > keep || n_recent > keep - n_sink)
+    return KVS_ERR_INVALID_ARG;
+  if (n_req == 0) return KVS_OK;
+  if (!d_weight || !d_ctx_len || !d_block2slot || !d_dst2slot || !d_kept || !d_n_kept || !d_weight_out) return KVS_ERR_INVALID_ARG;
+  if (d_weight == d_weight_out) return KVS_ERR_INVALID_ARG;
+  c->launches += 2;
+  return cuda_status(launch_pool_evict(d, c->k + layer * c->layer_bytes, c->v + layer * c->layer_bytes, d_weight, d_ctx_len,
+                                       d_block2slot, n_req, keep, n_sink, n_recent, d_dst2slot, d_kept, d_n_kept,
+                                       d_weight_out, c->err, S(stream)));
+}
+
+}  // extern "C"
