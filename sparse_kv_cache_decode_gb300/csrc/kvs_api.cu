@@ -248,9 +248,9 @@ inline cudaStream_t S(kvs_stream_t s) { return reinterpret_cast<cudaStream_t>(s)
 
 namespace kvs {
 // 2D tensor map over a row-major matrix [rows][inner] of bf16 (elem_bytes 2) or bytes (1), boxes of
-// box_inner x box_rows with the 128-byte swizzle (box_inner * elem_bytes must be 128).
+// box_inner x box_rows with the 128-byte swizzle (box_inner * elem_bytes must be 128), or none.
 bool make_tmap_2d(CUtensorMap* m, void* base, uint64_t inner, uint64_t rows, uint32_t box_inner, uint32_t box_rows,
-                  int elem_bytes) {
+                  int elem_bytes, bool swizzle) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if (!encode) {
     void* fn = nullptr;
@@ -268,7 +268,7 @@ bool make_tmap_2d(CUtensorMap* m, void* base, uint64_t inner, uint64_t rows, uin
   cuuint32_t estr[2] = {1, 1};
   CUresult r = encode(m, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base,
                       dims, strides, box, estr,
-                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }

@@ -32,7 +32,7 @@ bool pool_dims(const kvs_pool_config* c, PoolDims* d) {
   if (c->n_q_head / c->n_kv_head > 128) return false;
   if (c->head_dim != 64 && c->head_dim != 128) return false;
   if (c->block_size != 16 && c->block_size != 32 && c->block_size != 64 && c->block_size != 128) return false;
-  if (c->max_ctx < 1 || c->max_ctx > (1 << 30) || c->max_req < 1 || c->max_req > 4096) return false;
+  if (c->max_ctx < 1 || c->max_ctx > (1 << 30) || c->max_req < 1 || c->max_req > kPoolMaxReq) return false;
   if ((long long)c->max_req * c->n_kv_head > 65535) return false;   // (request, kv head) pairs are a grid dimension
   if (c->max_tokens < 1 || c->max_tokens > (1 << 24)) return false;
   if (c->max_prefix_tokens < 0 || c->max_prefix_tokens > c->max_tokens) return false;
@@ -149,13 +149,14 @@ kvs_status kvs_pool_create(const kvs_pool_config* cfg, void* d_k, void* d_v, voi
   c->prev_lse2 = reinterpret_cast<float*>(b); b += p.prev_lse2;
   c->prev_out = reinterpret_cast<float*>(b); b += p.prev_out;
   c->scratch = b;
-  // each layer's rows [n_slots * H_kv * bs][d]; a load brings up to one block's rows of 128 bytes
+  // each layer's rows [n_slots * H_kv * bs][d]; a load brings one block's rows: 64 dims of bf16 (128 bytes,
+  // swizzled as the products read them), or all dims of E4M3 codes, as they are
   const uint64_t rows = (uint64_t)d.n_slots * d.Hkv * d.bs;
-  const uint32_t inner = (uint32_t)(d.d < 128 / d.ebytes ? d.d : 128 / d.ebytes);
+  const uint32_t inner = (uint32_t)(d.fp8 ? d.d : 64);
   for (int l = 0; l < d.NL; ++l)
     for (int x = 0; x < 2; ++x)
       if (!make_tmap_2d(&c->maps[2 * l + x], (x ? c->v : c->k) + l * c->layer_bytes, (uint64_t)d.d, rows, inner,
-                        (uint32_t)d.bs, d.ebytes)) {
+                        (uint32_t)d.bs, d.ebytes, !d.fp8)) {
         kvs_pool_destroy(c);
         return KVS_ERR_CUDA;
       }

@@ -4,6 +4,8 @@
 
 namespace kvs {
 
+constexpr int kPoolMaxReq = 2048;   // requests (or prefixes) per call
+
 // Shape of one pool, as the kernels see it (passed by value).
 struct PoolDims {
   int NL, n_slots;
