@@ -42,6 +42,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMaxGrowth = 8.f;
 constexpr int TOK = 128;                      // tokens per tile
 constexpr int MAX_SMEM = 227 * 1024;
+constexpr int kPieces = 64;                   // pieces planned at a time
 
 struct Split {
   int n_cta;
@@ -71,21 +72,30 @@ __host__ __device__ inline Scratch scratch_of(void* p, int n_cta) {
 template <int D, bool FP8, int QT>
 struct Cfg {
   static constexpr int CHUNKS = D / 64;                       // 64-dim (128-byte) chunks of a bf16 row
-  static constexpr int QTILE = TOK * D * 2;                   // one 128-row tile of Q
+  // Q: QT tiles of 128 rows; with one tile half a tile more, so that the next item's Q (at most 64 rows) can
+  // be brought to the half the current one leaves free (rows past an item's last are never used)
+  static constexpr int QROWS = QT == 1 ? 192 : 256;
+  static constexpr int QHALF = QT == 1 ? 64 : 128;
+  static constexpr int QCHUNK = QROWS * 128;
+  static constexpr int QBYTES = CHUNKS * QCHUNK;
   static constexpr int TILE = TOK * D * 2;                    // one bf16 K or V tile
   static constexpr int CODES = TOK * D;                       // one tile of E4M3 codes
   static constexpr int THREADS = FP8 ? 512 : 384;
   static constexpr int FIXED = 2048 + 512 + 1024;             // group states, barriers, alignment
-  static constexpr int ROOM = MAX_SMEM - FIXED - 4 * (kPoolMaxReq + 1) - QT * QTILE;
+  static constexpr int ROOM = MAX_SMEM - FIXED - 4 * (kPoolMaxReq + 1) - kPieces * 64 - QBYTES;
   static constexpr int STAGING = FP8 ? (D == 128 ? 3 : 4) : 0;         // code tiles in flight
   static constexpr int S_BF = (ROOM - STAGING * CODES) / TILE;
   static constexpr int STAGES = S_BF > 8 ? 8 : S_BF;
+  // registers of the helper and the softmax warps (the groups of 128 threads share the launch's registers)
+  static constexpr int REGS_LOW = 72, REGS_HIGH = FP8 ? 184 : 216;
+  static_assert(FP8 ? 2 * REGS_LOW + 2 * REGS_HIGH <= 4 * 128 : REGS_LOW + 2 * REGS_HIGH <= 3 * 168, "register plan");
   static constexpr int RB = TOK * QT;
-  static constexpr int OFF_RING = QT * QTILE;
+  static constexpr int OFF_RING = QBYTES;
   static constexpr int OFF_STG = OFF_RING + STAGES * TILE;
   static constexpr int OFF_ML = OFF_STG + STAGING * CODES;
   static constexpr int OFF_BAR = OFF_ML + 2048;
-  static constexpr int OFF_TAB = OFF_BAR + 512;
+  static constexpr int OFF_PIECES = OFF_BAR + 512;
+  static constexpr int OFF_TAB = OFF_PIECES + kPieces * 64;
   static_assert(STAGES >= 3, "shared memory plan");
   static_assert(OFF_TAB + 4 * (kPoolMaxReq + 1) + 1024 <= MAX_SMEM, "shared memory plan");
 };
@@ -96,16 +106,47 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// An item: rows [row0, row0 + nrows) of head h of sequence s, and the keys it sees: [0, first) and [lo, hi).
-struct Item {
-  int s, h, t0, row0, nrows, R;
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// pairs of fp32 in one 64-bit register
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// the lowest n bits (n < 0: none, n > 32: all)
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// A CTA's piece of an item: rows [row0, row0 + nrows) of head h of sequence s against n of the item's nt tiles,
+// from tile j0 on.  The item's rows see the keys [0, first) and [lo, hi).
+struct __align__(16) Piece {
+  int s, h, t0, row0, nrows;
   int p0;                 // position of the sequence's first query token
   int len;
-  int first, lo, hi;      // keys some row of the item sees
+  int first, lo, hi;
   int ns, lo_tile, nt;    // tiles of the first tokens, first tile of the span, tiles in all
+  int j0, n;
+  int pad;
 };
+static_assert(sizeof(Piece) == 64, "smem plan");
 
-__device__ __forceinline__ void item_span(const PoolSeqs& q, int G, Item& it) {
+__device__ __forceinline__ void item_span(const PoolSeqs& q, int G, Piece& it) {
   if (!q.causal) {
     it.first = 0;
     it.lo = 0;
@@ -121,6 +162,17 @@ __device__ __forceinline__ void item_span(const PoolSeqs& q, int G, Item& it) {
   it.nt = max(1, it.ns + (it.hi + TOK - 1) / TOK - it.lo_tile);
 }
 
+// Row block rb of a sequence: its rows and span.
+template <int RB>
+__device__ __forceinline__ void item_rows(const PoolSeqs& q, int G, const SeqInfo& r, int rb, Piece& it) {
+  it.t0 = r.t0;
+  it.len = r.len;
+  it.p0 = r.len - (r.t1 - r.t0);
+  it.row0 = rb * RB;
+  it.nrows = max(0, min(RB, (r.t1 - r.t0) * G - it.row0));
+  item_span(q, G, it);
+}
+
 // Item number `pos` of the dealt-out order: position p = c * K + k is item k * n + c (the first n_items % n
 // columns are one longer).
 __device__ __forceinline__ int dealt(int p, int n_items, int n) {
@@ -131,55 +183,67 @@ __device__ __forceinline__ int dealt(int p, int n_items, int n) {
   return (p % K) * n + r + p / K;
 }
 
+// Item i: the sequences' items follow one another, row block by row block, head by head.
 template <int RB>
-__device__ __forceinline__ Item item_at(const PoolDims& d, const PoolSeqs& q, const int* tab, int i, unsigned* err) {
+__device__ __forceinline__ Piece item_at(const PoolDims& d, const PoolSeqs& q, const int* tab, int i, unsigned* err) {
   // the last sequence with tab[s] <= i (empty sequences hold no items, so it is the one that does)
   int lo = 0, hi = q.n_seq;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (tab[mid] <= i) lo = mid; else hi = mid;
   }
-  Item it;
+  Piece it;
   it.s = lo;
   const SeqInfo r = pool_seq(d, q, lo, err);
   const int local = i - tab[lo], rb = local / d.Hkv;
   it.h = local - rb * d.Hkv;
-  it.t0 = r.t0;
-  it.len = r.len;
-  it.p0 = r.len - (r.t1 - r.t0);
-  it.R = (r.t1 - r.t0) * d.G;
-  it.row0 = rb * RB;
-  it.nrows = max(0, min(RB, it.R - it.row0));
-  item_span(q, d.G, it);
+  item_rows<RB>(q, d.G, r, rb, it);
   return it;
 }
 
-__device__ __forceinline__ int tile_base(const Item& it, int j) { return (j < it.ns ? j : it.lo_tile + j - it.ns) * TOK; }
-__device__ __forceinline__ bool key_seen(const Item& it, int t) { return t < it.first || (t >= it.lo && t < it.hi); }
+__device__ __forceinline__ int tile_base(const Piece& it, int j) { return (j < it.ns ? j : it.lo_tile + j - it.ns) * TOK; }
+__device__ __forceinline__ bool key_seen(const Piece& it, int t) { return t < it.first || (t >= it.lo && t < it.hi); }
 // every key of the tile at `base` is seen by some row
-__device__ __forceinline__ bool tile_whole(const Item& it, int base) {
+__device__ __forceinline__ bool tile_whole(const Piece& it, int base) {
   return (base >= it.lo && base + TOK <= it.hi) || base + TOK <= it.first;
 }
 
-// Exclusive scan over the CTA's threads (64-bit); ws: 33 words of shared memory.
-__device__ __forceinline__ long long block_scan(long long v, long long* ws, int nw, long long* total) {
+// Exclusive scans of a count and a sum over the CTA's threads in one; ws: 64 words of shared memory.
+struct Scan {
+  int n, n_all;
+  long long v, v_all;
+};
+__device__ __forceinline__ Scan block_scan(int n, long long v, long long* ws, int nw) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
+  int xn = n;
+  long long xv = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const int yn = __shfl_up_sync(0xffffffffu, xn, o);
+    const long long yv = __shfl_up_sync(0xffffffffu, xv, o);
+    if (lane >= o) {
+      xn += yn;
+      xv += yv;
+    }
   }
   __syncthreads();
-  if (lane == 31) ws[warp] = x;
+  if (lane == 31) {
+    ws[2 * warp] = xn;
+    ws[2 * warp + 1] = xv;
+  }
   __syncthreads();
-  long long before = x - v, all = 0;
+  Scan r = {xn - n, 0, xv - v, 0};
   for (int w = 0; w < nw; ++w) {
-    if (w < warp) before += ws[w];
-    all += ws[w];
+    const int a = (int)ws[2 * w];
+    const long long b = ws[2 * w + 1];
+    if (w < warp) {
+      r.n += a;
+      r.v += b;
+    }
+    r.n_all += a;
+    r.v_all += b;
   }
-  *total = all;
-  return before;
+  return r;
 }
 
 // out / lse of one row from its joined state: D columns by the caller.
@@ -213,6 +277,26 @@ __device__ __forceinline__ void row_store4(const PoolAttnOut& o, size_t e, float
   else *reinterpret_cast<uint2*>(o.out + e) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
 }
 
+// The rest of a bounded wait on a barrier that was not ready at once.
+__device__ __forceinline__ bool slow_wait(uint64_t* bar, unsigned parity, uint64_t timeout_ns, volatile int* abort_flag,
+                                       unsigned* err) {
+  const uint64_t t = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t > timeout_ns) {
+      set_error(err, KVS_ERR_TIMEOUT);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
+
 template <int D, bool FP8, int QT>
 __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
     pool_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, PoolDims d,
@@ -233,12 +317,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
   uint64_t* s_full = bars + 24;         // [2]
   uint64_t* p_full = bars + 26;         // [2]
   uint64_t* o_full = bars + 28;         // [2]
-  uint64_t* q_full = bars + 30;
-  uint64_t* q_free = bars + 31;
-  uint64_t* drained = bars + 32;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 33);
+  uint64_t* q_full = bars + 30;         // [2] by piece parity
+  uint64_t* q_free = bars + 32;
+  uint64_t* drained = bars + 33;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 34);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* start = reinterpret_cast<int*>(tmem_slot + 2);                 // first position, its first tile, tiles, items
+  // position and first tile of the CTA's next piece, its tiles still to plan, pieces planned, items, tiles per CTA
+  volatile int* plan = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  const Piece* pieces = reinterpret_cast<const Piece*>(smem + C::OFF_PIECES);
   int* tab = reinterpret_cast<int*>(smem + C::OFF_TAB);               // [n_seq + 1] items before each sequence
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x;
@@ -258,11 +344,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
       mbar_init(&p_full[g], 4);
       mbar_init(&o_full[g], 1);
     }
-    mbar_init(q_full, 2);
+    mbar_init(&q_full[0], 2);
+    mbar_init(&q_full[1], 2);
     mbar_init(q_free, 1);
     mbar_init(drained, 1);
     *abort_flag = 0;
-    start[2] = 0;
+    plan[0] = plan[1] = plan[2] = 0;
     mbar_fence_init();
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
@@ -275,76 +362,154 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
   {
     long long* ws = reinterpret_cast<long long*>(ml);
     const int per_s = (seqs.n_seq + C::THREADS - 1) / C::THREADS;
-    int mine = 0;
-    for (int s = tid * per_s; s < min(seqs.n_seq, (tid + 1) * per_s); ++s) {
+    const int s0 = min(seqs.n_seq, tid * per_s), s1 = min(seqs.n_seq, s0 + per_s);
+    // items and, in the order of sequences, tiles of this thread's sequences
+    auto seq_work = [&](int s, int* items) {
       const SeqInfo r = pool_seq(d, seqs, s, err);
-      mine += (int)(((long long)(r.t1 - r.t0) * d.G + RB - 1) / RB) * d.Hkv;
-    }
-    long long n_all;
-    int at = (int)block_scan(mine, ws, NW, &n_all);
-    for (int s = tid * per_s; s < min(seqs.n_seq, (tid + 1) * per_s); ++s) {
-      const SeqInfo r = pool_seq(d, seqs, s, err);
-      tab[s] = at;
-      at += (int)(((long long)(r.t1 - r.t0) * d.G + RB - 1) / RB) * d.Hkv;
-    }
-    const int n_items = (int)n_all;
-    if (tid == 0) tab[seqs.n_seq] = n_items;
-    __syncthreads();
-    const int per_i = (n_items + C::THREADS - 1) / C::THREADS;
-    const int i0 = min(n_items, tid * per_i), i1 = min(n_items, i0 + per_i);
-    long long tiles = 0, total;
-    for (int p = i0; p < i1; ++p) tiles += item_at<RB>(d, seqs, tab, dealt(p, n_items, sp.n_cta), err).nt;
-    long long f = block_scan(tiles, ws, NW, &total);
-    const long long per = max((long long)sp.min_per, (total + sp.n_cta - 1) / sp.n_cta);
-    const long long f0 = per * c, f1 = min(total, f0 + per);
-    if (f0 < f1 && f0 >= f && f0 < f + tiles) {
-      for (int p = i0; p < i1; ++p) {
-        const int nt = item_at<RB>(d, seqs, tab, dealt(p, n_items, sp.n_cta), err).nt;
-        if (f0 < f + nt) {
-          start[0] = p;
-          start[1] = (int)(f0 - f);
-          start[2] = (int)(f1 - f0);
-          break;
+      const int n_rb = (int)(((long long)(r.t1 - r.t0) * d.G + RB - 1) / RB);
+      *items = n_rb * d.Hkv;
+      long long v = 0;
+      if (QT == 1)
+        for (int rb = 0; rb < n_rb; ++rb) {
+          Piece it;
+          item_rows<RB>(seqs, d.G, r, rb, it);
+          v += (long long)it.nt * d.Hkv;
         }
-        f += nt;
+      return v;
+    };
+    int mine = 0, n1 = 0;
+    long long tiles = 0, v1 = 0;
+    for (int s = s0; s < s1; ++s) {
+      v1 = seq_work(s, &n1);
+      mine += n1;
+      tiles += v1;
+    }
+    Scan r = block_scan(mine, tiles, ws, NW);
+    const int n_items = r.n_all;
+    {
+      int at = r.n;
+      for (int s = s0; s < s1; ++s) {
+        tab[s] = at;
+        if (s + 1 < s1) {      // the last one's count is not needed
+          seq_work(s, &n1);
+          at += n1;
+        }
       }
+      if (tid == 0) tab[seqs.n_seq] = n_items;
+    }
+    // with two row tiles the items are dealt out: the tiles in that order
+    int i0 = 0, i1 = 0;
+    if (QT == 2) {
+      __syncthreads();
+      const int per_i = (n_items + C::THREADS - 1) / C::THREADS;
+      i0 = min(n_items, tid * per_i);
+      i1 = min(n_items, i0 + per_i);
+      tiles = 0;
+      for (int p = i0; p < i1; ++p) tiles += item_at<RB>(d, seqs, tab, dealt(p, n_items, sp.n_cta), err).nt;
+      r = block_scan(0, tiles, ws, NW);
+    }
+    const long long per = max((long long)sp.min_per, (r.v_all + sp.n_cta - 1) / sp.n_cta);
+    const long long f0 = per * c, f1 = min(r.v_all, f0 + per);
+    if (f0 < f1 && f0 >= r.v && f0 < r.v + tiles) {
+      long long f = r.v;
+      int p = -1, j = 0;
+      if (QT == 2) {
+        for (p = i0; p < i1; ++p) {
+          const int nt = item_at<RB>(d, seqs, tab, dealt(p, n_items, sp.n_cta), err).nt;
+          if (f0 < f + nt) break;
+          f += nt;
+        }
+        j = (int)(f0 - f);
+      } else {
+        for (int s = s0; s < s1 && p < 0; ++s) {
+          const long long v = s1 - s0 == 1 ? v1 : seq_work(s, &n1);
+          if (f0 >= f + v) {
+            f += v;
+            continue;
+          }
+          const SeqInfo q1 = pool_seq(d, seqs, s, err);
+          for (int rb = 0; p < 0; ++rb) {
+            Piece it;
+            item_rows<RB>(seqs, d.G, q1, rb, it);
+            const long long w = (long long)it.nt * d.Hkv;
+            if (f0 < f + w) {
+              const int h = (int)((f0 - f) / it.nt);
+              p = tab[s] + rb * d.Hkv + h;
+              j = (int)(f0 - f - (long long)h * it.nt);
+            }
+            f += w;
+          }
+        }
+      }
+      plan[0] = p;
+      plan[1] = j;
+      plan[2] = (int)(f1 - f0);
     }
     if (tid == 0) {
-      start[3] = n_items;
-      start[4] = (int)per;
+      plan[4] = n_items;
+      plan[5] = (int)per;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int n_items = start[3], per = start[4];
   const uint64_t timeout_ns = (uint64_t)d.timeout_us * 1000ull;
+  const int total = plan[2];            // the CTA's tiles
   auto wait = [&](uint64_t* bar, unsigned parity) {
     if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t = global_timer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-      if (*abort_flag) return false;
-      if (global_timer_ns() - t > timeout_ns) {
-        set_error(err, KVS_ERR_TIMEOUT);
-        *abort_flag = 1;
-        return false;
-      }
-    }
-    return true;
+    return slow_wait(bar, parity, timeout_ns, abort_flag, err);
   };
-  // the pieces of this CTA in order: (item, first tile, tiles)
-  int pos = start[0], j0 = start[1], left = start[2];
-  auto next_item = [&]() { return item_at<RB>(d, seqs, tab, dealt(pos, n_items, sp.n_cta), err); };
-  auto advance = [&](int n) {
-    left -= n;
-    ++pos;
-    j0 = 0;
+  // Plans the CTA's next kPieces pieces (warp 0, a lane per piece).
+  auto plan_pieces = [&]() {
+    int pos = plan[0], j0 = plan[1], left = plan[2], cnt = 0;
+    const int n_items = plan[4];
+    for (int x = 0; x < kPieces && left > 0; x += 32) {
+      Piece it;
+      it.nt = 0;
+      if (pos + lane < n_items)
+        it = item_at<RB>(d, seqs, tab, QT == 2 ? dealt(pos + lane, n_items, sp.n_cta) : pos + lane, err);
+      it.j0 = lane == 0 ? j0 : 0;
+      const long long w = it.nt - it.j0;
+      long long incl = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      it.n = (int)max(0ll, min(w, left - (incl - w)));
+      if (it.n > 0) const_cast<Piece*>(pieces)[x + lane] = it;
+      const int got = __popc(__ballot_sync(0xffffffffu, it.n > 0));
+      const long long all = __shfl_sync(0xffffffffu, incl, 31);
+      left = (int)max(0ll, left - all);
+      pos += got;
+      cnt += got;
+      j0 = 0;
+    }
+    __syncwarp();
+    if (lane == 0) {
+      plan[0] = pos;
+      plan[1] = 0;
+      plan[2] = left;
+      plan[3] = cnt;
+    }
+  };
+  if (warp == 0) plan_pieces();
+  __syncthreads();
+  // Between two lists of pieces (long calls only): every role is done with the old one.
+  auto more = [&]() {
+    const int l = plan[2];
+    __syncthreads();
+    if (l <= 0) return false;
+    if (warp == 0) plan_pieces();
+    __syncthreads();
+    return true;
   };
 
   if (warp == 0) {
     // ------------------------------------------------------------------ K/V tiles
-    // a lane per (block, chunk) of a tile: K first, then V, each into the next slot of the ring
+    // a lane per block of a tile: K first, then V, each into the next slot of the ring
+    regs_dec<C::REGS_LOW>();
     constexpr int BOXES = FP8 ? 1 : C::CHUNKS;
     constexpr int SLOTS = FP8 ? C::STAGING : S;
     uint64_t* full = FP8 ? raw_full : kv_full;
@@ -353,355 +518,404 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
     const int box_bytes = d.bs * (FP8 ? D : 128);
     int k = 0;
     bool ok = true;
-    while (left > 0 && ok) {
-      const Item it = next_item();
-      const int n = min(left, it.nt - j0);
-      const int* table = seqs.table + (size_t)it.s * d.nb_max;
-      for (int j = j0; j < j0 + n && ok; ++j) {
-        const int base = tile_base(it, j);
-        // lane p: block p of the tile, its slot if some row sees one of its tokens
-        int row = -1;
-        if (lane < pages) {
-          const int b0 = base + (lane << d.log2bs), b1 = b0 + d.bs;
-          if ((b0 < it.first) || (b0 < it.hi && b1 > it.lo)) {
-            const int slot = table[b0 >> d.log2bs];
-            if (slot < 0 || slot >= d.n_slots) set_error(err, KVS_ERR_BAD_INDEX);
-            else row = (slot * d.Hkv + it.h) * d.bs;
+    do {
+      const int cnt = plan[3];
+      for (int i = 0; i < cnt && ok; ++i) {
+        const Piece it = pieces[i];
+        const int* table = seqs.table + (size_t)it.s * d.nb_max;
+        for (int j = it.j0; j < it.j0 + it.n && ok; ++j) {
+          const int base = tile_base(it, j);
+          // lane p: block p of the tile, its slot if some row sees one of its tokens
+          int row = -1;
+          if (lane < pages) {
+            const int b0 = base + (lane << d.log2bs), b1 = b0 + d.bs;
+            if ((b0 < it.first) || (b0 < it.hi && b1 > it.lo)) {
+              const int slot = table[b0 >> d.log2bs];
+              if (slot < 0 || slot >= d.n_slots) set_error(err, KVS_ERR_BAD_INDEX);
+              else row = (slot * d.Hkv + it.h) * d.bs;
+            }
           }
-        }
-        const int n_load = __popc(__ballot_sync(0xffffffffu, row >= 0));
-        for (int x = 0; x < 2; ++x, ++k) {
-          const int s = k % SLOTS;
-          ok = k < SLOTS || __all_sync(0xffffffffu, wait(&empty[s], ((k / SLOTS) & 1) ^ 1));
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&full[s], (unsigned)(n_load * BOXES * box_bytes));
-          __syncwarp();
-          if (row >= 0) {
-            unsigned char* dst = FP8 ? stg + s * C::CODES + lane * box_bytes : ring + s * C::TILE + lane * box_bytes;
-            for (int b = 0; b < BOXES; ++b)
-              tma_load_2d(dst + b * (TOK * 128), x ? &tmV : &tmK, b * 64, row, &full[s]);
+          const int n_load = __popc(__ballot_sync(0xffffffffu, row >= 0));
+          for (int x = 0; x < 2; ++x, ++k) {
+            const int s = k % SLOTS;
+            ok = k < SLOTS || __all_sync(0xffffffffu, wait(&empty[s], ((k / SLOTS) & 1) ^ 1));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], (unsigned)(n_load * BOXES * box_bytes));
+            __syncwarp();
+            if (row >= 0) {
+              unsigned char* dst = FP8 ? stg + s * C::CODES + lane * box_bytes : ring + s * C::TILE + lane * box_bytes;
+#pragma unroll
+              for (int b = 0; b < BOXES; ++b)
+                tma_load_2d(dst + b * (TOK * 128), x ? &tmV : &tmK, b * 64, row, &full[s]);
+            }
           }
         }
       }
-      advance(n);
-    }
+    } while (more());
     __syncwarp();
     // no tensor load may still be writing this CTA's shared memory when it exits
     for (int i = max(0, k - SLOTS); i < k; ++i) mbar_wait(&full[i % SLOTS], (i / SLOTS) & 1, kDrainTimeoutNs);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ products
-    if (lane == 0) {
-      const uint32_t id_qk = idesc_bf16_f32(128, TOK);
-      const uint32_t id_pv = idesc_bf16_f32(128, D) | (1u << 16);     // V is read MN-major
-      const uint64_t dq = smem_desc_sw128(smem_u32(smem));
-      int N = 0, piece = 0;           // tiles before this piece; pieces
-      int ops[2] = {0, 0};            // products S of each group so far
-      bool ok = true;
-      while (left > 0 && ok) {
-        const Item it = next_item();
-        const int n = min(left, it.nt - j0);
-        const bool pair = it.nrows > 128;
-        if (!wait(q_full, piece & 1)) break;
-        const int n_ops = pair ? 2 * n : n;
-        // operation x: tile x / 2 (pair) or x of the piece, group x % 2; its PV follows when the group's next
-        // operation comes up
-        auto pv = [&](int x) {
-          const int g = x & 1, tile = N + (pair ? x >> 1 : x);
-          const int first = x < 2, s = (2 * tile + 1) % S;
-          if (!wait(&p_full[g], (ops[g] - 1) & 1) || !wait(&kv_full[s], ((2 * tile + 1) / S) & 1)) return false;
-          tc_fence_after();
-          const uint32_t v0 = smem_u32(ring + s * C::TILE);
-#pragma unroll
-          for (int kk = 0; kk < TOK / 16; ++kk)
-            tc_mma_f16_ts(tmem + 256 + g * D, tmem + g * 128 + kk * 8, smem_desc_sw128_mn(v0 + kk * 2048, TOK * 128, 1024),
-                          id_pv, !(first && kk == 0));
-          if (!pair || g) tc_commit(&kv_empty[s]);
-          if (x + 2 >= n_ops) tc_commit(&o_full[g]);
-          return true;
-        };
-        for (int x = 0; x < n_ops && ok; ++x) {
-          if (x >= 2) ok = pv(x - 2);
-          if (!ok) break;
-          const int g = x & 1, tile = N + (pair ? x >> 1 : x), s = (2 * tile) % S;
-          if (!wait(&kv_full[s], ((2 * tile) / S) & 1)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t dk = smem_desc_sw128(smem_u32(ring + s * C::TILE));
-          const uint64_t da = dq + (uint64_t)((pair ? g * C::QTILE : 0) >> 4);
-#pragma unroll
-          for (int k16 = 0; k16 < D / 16; ++k16) {
-            const uint64_t off = (uint64_t)(((k16 >> 2) * (TOK * 128) + (k16 & 3) * 32) >> 4);
-            tc_mma_f16(tmem + g * 128, da + off, dk + off, id_qk, k16 != 0);
-          }
-          tc_commit(&s_full[g]);
-          ++ops[g];
-          if (!pair || g) tc_commit(&kv_empty[s]);
-          if (x == n_ops - 1) tc_commit(q_free);
-        }
-        for (int x = max(0, n_ops - 2); x < n_ops && ok; ++x) ok = pv(x);
-        N += n;
-        ++piece;
-        advance(n);
+    // Operation x of a piece: S of tile x / 2 for group x % 2 (two row tiles), or of tile x for group x % 2 (one
+    // row tile).  Its PV is issued before the group's next S, which overwrites P, oldest first.
+    regs_dec<C::REGS_LOW>();
+    const uint32_t id_qk = idesc_bf16_f32(128, TOK);
+    const uint32_t id_pv = idesc_bf16_f32(128, D) | (1u << 16);     // V is read MN-major
+    const uint64_t dq0 = smem_desc_sw128(smem_u32(smem));
+    const uint64_t dr0 = smem_desc_sw128(smem_u32(ring));
+    const uint64_t dv0 = smem_desc_sw128_mn(smem_u32(ring), TOK * 128, 1024);
+    int N = 0, piece = 0, qb = 0;   // tiles and pieces before this one, the half that holds its Q
+    int pend0 = -1, pend1 = -1;     // the groups' operations whose PV is due: tile * 8 + pair * 4 + last * 2 + first
+    int older = 0, pv_par = 0;      // the group whose operation came first; parity of each group's next P
+    bool ok = true;
+    auto pv = [&](int g) {
+      const int info = g ? pend1 : pend0;
+      if (g) pend1 = -1; else pend0 = -1;
+      older = g ^ 1;
+      const int slot = 2 * (info >> 3) + 1, s = slot % S;
+      if (!wait(&p_full[g], (pv_par >> g) & 1) || !wait(&kv_full[s], (slot / S) & 1)) {
+        ok = false;
+        return;
       }
+      pv_par ^= 1 << g;
+      tc_fence_after();
+      const uint64_t dv = dv0 + (uint64_t)((s * C::TILE) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < TOK / 16; ++kk)
+        tc_mma_f16_ts(tmem + 256 + g * D, tmem + g * 128 + kk * 8, dv + (uint64_t)(kk * 2048 >> 4), id_pv,
+                      kk > 0 || !(info & 1));
+      if (!(info & 4) || g) tc_commit(&kv_empty[s]);
+      if (info & 2) tc_commit(&o_full[g]);
+    };
+    do {
+      const int cnt = plan[3];
+      if (lane == 0) {
+        for (int i = 0; i < cnt && ok; ++i, ++piece) {
+          const int nrows = pieces[i].nrows, n = pieces[i].n;
+          const bool pair = nrows > 128;
+          qb = nrows <= C::QHALF ? qb ^ 1 : 0;
+          const int n_ops = pair ? 2 * n : n;
+          if (!mbar_try_wait(&q_full[piece & 1], (piece >> 1) & 1)) {
+            // while Q is on its way: what is due
+            for (int y = 0; y < 2 && ok; ++y)
+              if ((older ? pend1 : pend0) >= 0) pv(older);
+              else if ((older ? pend0 : pend1) >= 0) pv(older ^ 1);
+            if (!ok || !wait(&q_full[piece & 1], (piece >> 1) & 1)) { ok = false; break; }
+          }
+          for (int x = 0; x < n_ops && ok; ++x) {
+            const int g = x & 1, tile = N + (pair ? x >> 1 : x), s = (2 * tile) % S;
+            while ((g ? pend1 : pend0) >= 0 && ok) pv((older ? pend1 : pend0) >= 0 ? older : g);
+            if (!ok || !wait(&kv_full[s], ((2 * tile) / S) & 1)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t dk = dr0 + (uint64_t)((s * C::TILE) >> 4);
+            const uint64_t da = dq0 + (uint64_t)((pair ? g * 128 : qb * C::QHALF) * 128 >> 4);
+#pragma unroll
+            for (int k16 = 0; k16 < D / 16; ++k16)
+              tc_mma_f16(tmem + g * 128, da + (uint64_t)(((k16 >> 2) * C::QCHUNK + (k16 & 3) * 32) >> 4),
+                         dk + (uint64_t)(((k16 >> 2) * (TOK * 128) + (k16 & 3) * 32) >> 4), id_qk, k16 != 0);
+            tc_commit(&s_full[g]);
+            if (!pair || g) tc_commit(&kv_empty[s]);
+            if (x == n_ops - 1) tc_commit(q_free);
+            const int info = tile * 8 + (pair ? 4 : 0) + (x + 2 >= n_ops ? 2 : 0) + (x < 2 ? 1 : 0);
+            if (g) pend1 = info; else pend0 = info;
+            if ((g ? pend0 : pend1) < 0) older = g;
+          }
+          N += n;
+        }
+        for (int y = 0; y < 2 && ok; ++y)
+          if ((older ? pend1 : pend0) >= 0) pv(older);
+          else if ((older ? pend0 : pend1) >= 0) pv(older ^ 1);
+      }
+      __syncwarp();
+    } while (more());
+    if (lane == 0) {
       // every product issued by this thread has finished before the tensor memory is released
       tc_commit(drained);
       mbar_wait(drained, 0, kDrainTimeoutNs);
     }
     __syncwarp();
   } else if (warp < 4) {
-    // ------------------------------------------------------------------ Q, once the last piece's products have read it
-    int piece = 0;
-    while (left > 0) {
-      const Item it = next_item();
-      const int n = min(left, it.nt - j0);
-      if (piece > 0 && !__all_sync(0xffffffffu, wait(q_free, (piece - 1) & 1))) break;
-      constexpr int VEC = D / 8;       // 16-byte vectors of a row
-      for (int i = tid - 64; i < it.nrows * VEC; i += 64) {
-        const int r = i / VEC, v = i - r * VEC, row = it.row0 + r;
-        const int tok = row / d.G, g = row - tok * d.G;
-        const __nv_bfloat16* src = q + (it.t0 + tok) * q_stride + (it.h * d.G + g) * D + v * 8;
-        unsigned char* dst = smem + (r >> 7) * C::QTILE + (v >> 3) * (TOK * 128) + (r & 127) * 128 + (((v & 7) ^ (r & 7)) << 4);
-        cp_async16(dst, src, 16);
+    // ------------------------------------------------------------------ Q
+    // Two items of at most QHALF rows each use the two halves; otherwise Q waits for the last item's products.
+    regs_dec<C::REGS_LOW>();
+    int piece = 0, qb = 0, last_small = 1;
+    bool ok = true;
+    do {
+      const int cnt = plan[3];
+      for (int i = 0; i < cnt && ok; ++i, ++piece) {
+        const Piece it = pieces[i];
+        const int small = it.nrows <= C::QHALF;
+        qb = small ? qb ^ 1 : 0;
+        const int behind = small && last_small ? piece - 2 : piece - 1;    // the piece that must be through
+        last_small = small;
+        ok = behind < 0 || __all_sync(0xffffffffu, wait(q_free, behind & 1));
+        if (!ok) break;
+        constexpr int VEC = D / 8;       // 16-byte vectors of a row
+        for (int x = tid - 64; x < it.nrows * VEC; x += 64) {
+          const int r = x / VEC, v = x - r * VEC, row = it.row0 + r;
+          const int tok = row / d.G, g = row - tok * d.G, at = r + qb * C::QHALF;
+          const __nv_bfloat16* src = q + (it.t0 + tok) * q_stride + (it.h * d.G + g) * D + v * 8;
+          unsigned char* dst = smem + (v >> 3) * C::QCHUNK + at * 128 + (((v & 7) ^ (at & 7)) << 4);
+          cp_async16(dst, src, 16);
+        }
+        cp_async_commit();
+        cp_async_wait_all();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[piece & 1]);
       }
-      cp_async_commit();
-      cp_async_wait_all();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-      ++piece;
-      advance(n);
-    }
+    } while (more());
     cp_async_wait_all();
   } else if (warp < 12) {
     // ------------------------------------------------------------------ softmax and output
+    regs_inc<C::REGS_HIGH>();
     const int g = (warp - 4) >> 2, lr = (warp & 3) * 32 + lane;      // group; row of its 128
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tS = trow + g * 128, tO = trow + 256 + g * D;
     const float sl2 = d.scale * d.k_scale * kLog2e;
-    int N = 0, n_ops = 0, n_out[2] = {0, 0};
-    while (left > 0) {
-      const Item it = next_item();
-      const int n = min(left, it.nt - j0);
-      const bool pair = it.nrows > 128;
-      const int r = pair ? g * 128 + lr : lr;                          // row of the item
-      const bool live = r < it.nrows;
-      const int row = it.row0 + r;
-      // the keys this row sees, and those every row of this group sees
-      int hi = live ? it.len : 0, lo = 0, first = 0, hi_all = it.len, lo_all = 0, first_all = 0;
-      if (seqs.causal) {
-        const int ra = it.row0 + (pair ? g * 128 : 0), rb = min(ra + 127, it.row0 + it.nrows - 1);
-        const int p = it.p0 + row / d.G, pa = it.p0 + ra / d.G, pb = it.p0 + rb / d.G;
-        hi = live ? max(0, p + 1) : 0;
-        lo = seqs.window ? max(0, p - seqs.window + 1) : 0;
-        first = min(seqs.n_sink, lo);
-        hi_all = max(0, pa + 1);
-        lo_all = seqs.window ? max(0, pb - seqs.window + 1) : 0;
-        first_all = seqs.window ? min(seqs.n_sink, max(0, pa - seqs.window + 1)) : 0;
-      }
-      float m = -INFINITY, l = 0.f;
-      const int step = pair ? 1 : 2;
-      for (int j = pair ? 0 : g; j < n; j += step) {
-        const int base = tile_base(it, j0 + j);
-        wait(&s_full[g], n_ops & 1);
-        tc_fence_after();
-        float s[128];
-        tmem_ld128(tS, s);
-        const bool whole = (base + TOK <= hi_all && base >= lo_all) || base + TOK <= first_all;
-        if (!whole) {
-          const int h = hi - base, a = lo - base, f = first - base;
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (!(i < h && (i >= a || i < f))) s[i] = -INFINITY;
+    int N = 0, n_ops = 0, n_out0 = 0, n_out1 = 0;
+    if (warp == 4 && lane == 0) sc.meta[c].nrows = 0;
+    do {
+      const int cnt = plan[3];
+      for (int i = 0; i < cnt; ++i) {
+        const Piece& it = pieces[i];
+        const int n = it.n, nrows = it.nrows, j0 = it.j0;
+        const bool pair = nrows > 128;
+        const int r = pair ? g * 128 + lr : lr;                          // row of the item
+        const bool live = r < nrows;
+        const int row = it.row0 + r;
+        // the keys this row sees, and those every row of this group sees
+        int hi = live ? it.len : 0, lo = 0, first = 0, hi_all = it.len, lo_all = 0, first_all = 0;
+        if (seqs.causal) {
+          const int ra = it.row0 + (pair ? g * 128 : 0), rb = min(ra + 127, it.row0 + nrows - 1);
+          const int p = it.p0 + row / d.G, pa = it.p0 + ra / d.G, pb = it.p0 + rb / d.G;
+          hi = live ? max(0, p + 1) : 0;
+          hi_all = max(0, pa + 1);
+          if (seqs.window) {
+            lo = max(0, p - seqs.window + 1);
+            first = min(seqs.n_sink, lo);
+            lo_all = max(0, pb - seqs.window + 1);
+            first_all = min(seqs.n_sink, max(0, pa - seqs.window + 1));
+          }
         }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
+        float m = -INFINITY, l = 0.f;
+        for (int j = pair ? 0 : g; j < n; j += pair ? 1 : 2) {
+          const int base = tile_base(it, j0 + j);
+          wait(&s_full[g], n_ops & 1);
+          tc_fence_after();
+          float s[128];
+          tmem_ld128(tS, s);
+          if (!((base + TOK <= hi_all && base >= lo_all) || base + TOK <= first_all)) {
 #pragma unroll
-        for (int i = 4; i < 128; i += 4) {
-          mx[0] = fmaxf(mx[0], s[i]);
-          mx[1] = fmaxf(mx[1], s[i + 1]);
-          mx[2] = fmaxf(mx[2], s[i + 2]);
-          mx[3] = fmaxf(mx[3], s[i + 3]);
-        }
-        const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-        const bool grow = tmax > m + kMaxGrowth || (m == -INFINITY && tmax != -INFINITY);
-        const float m_new = grow ? tmax : m;
-        // O holds earlier tiles' products (all finished: S of this tile was issued behind them)
-        if (__any_sync(0xffffffffu, grow && l > 0.f)) {
-          const float f = grow && l > 0.f ? ex2(m - m_new) : 1.f;
+            for (int w = 0; w < 4; ++w) {
+              const int off = base + 32 * w;
+              const uint32_t vis = bits_below(hi - off) & (~bits_below(lo - off) | bits_below(first - off));
+#pragma unroll
+              for (int i2 = 0; i2 < 32; ++i2)
+                if (!(vis & (1u << i2))) s[32 * w + i2] = -INFINITY;
+            }
+          }
+          float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int i2 = 4; i2 < 124; i2 += 8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i2 + 2 * e], s[i2 + 2 * e + 1]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[124 + e]);
+          const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+          const bool grow = tmax > m + kMaxGrowth || (m == -INFINITY && tmax != -INFINITY);
+          const float m_new = grow ? tmax : m;
+          // O holds earlier tiles' products (all finished: S of this tile was issued behind them)
+          if (__any_sync(0xffffffffu, grow && l > 0.f)) {
+            const float f = grow && l > 0.f ? ex2(m - m_new) : 1.f;
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            float ov[32];
-            tmem_ld32(tO + c0, ov);
+            for (int c0 = 0; c0 < D; c0 += 16) {
+              float ov[16];
+              uint32_t ow[16];
+              tmem_ld16(tO + c0, ov);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) ov[i] *= f;
-            tmem_st32(tO + c0, ov);
+              for (int i2 = 0; i2 < 16; ++i2) ow[i2] = __float_as_uint(ov[i2] * f);
+              tmem_st16(tO + c0, ow);
+            }
+            l *= f;
           }
-          l *= f;
+          m = m_new;
+          const float neg = m == -INFINITY ? 0.f : -m;
+          const uint64_t sl22 = pack2(sl2, sl2), neg2 = pack2(neg, neg);
+          uint64_t ps0 = 0, ps1 = 0;
+#pragma unroll
+          for (int c0 = 0; c0 < 128; c0 += 32) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i2 = 0; i2 < 32; i2 += 2) {
+              float a, b;
+              unpack2(fma2(pack2(s[c0 + i2], s[c0 + i2 + 1]), sl22, neg2), a, b);
+              a = ex2(a);
+              b = ex2(b);
+              if (i2 & 2) ps1 = add2(ps1, pack2(a, b));
+              else ps0 = add2(ps0, pack2(a, b));
+              pk[i2 / 2] = pack_bf16x2(a, b);
+            }
+            tmem_st16(tS + c0 / 2, pk);
+          }
+          {
+            float a, b;
+            unpack2(add2(ps0, ps1), a, b);
+            l += a + b;
+          }
+          tmem_wait_st();
+          if (!FP8 && !tile_whole(it, base)) {
+            // value rows that no row of the item sees (a row per thread)
+            const int slot = 2 * (N + j) + 1;
+            wait(&kv_full[slot % S], (slot / S) & 1);
+            if (!key_seen(it, base + lr)) {
+              unsigned char* vr = ring + (slot % S) * C::TILE + lr * 128;
+#pragma unroll
+              for (int b = 0; b < C::CHUNKS; ++b)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(vr + b * (TOK * 128) + e * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[g]);
+          ++n_ops;
         }
-        m = m_new;
-        const float neg = m == -INFINITY ? 0.f : -m;
-        float ps[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float a = ex2(fmaf(s[c0 + i], sl2, neg)), b = ex2(fmaf(s[c0 + i + 1], sl2, neg));
-            ps[i & 2] += a;
-            ps[(i & 2) + 1] += b;
-            pk[i / 2] = pack_bf16x2(a, b);
-          }
-          tmem_st16(tS + c0 / 2, pk);
+        // -------------------------------------------------------------- the piece's end
+        const bool begun = j0 == 0, done = j0 + n == it.nt, whole = begun && done;
+        const int tok = it.t0 + row / d.G, head = it.h * d.G + row % d.G;
+        const size_t orow = (size_t)tok * d.Hq + head;
+        const size_t prow = ((size_t)c * 2 + (begun ? 1 : 0)) * 256 + r;      // partial state's place
+        const bool has_prev = o.prev_out && it.s >= o.prev_req[0] && it.s < o.prev_req[o.n_prev];
+        float w0 = 1.f, w1 = 0.f;          // weights of the two groups' O
+        int ca = 0, cb = D;                // columns this thread writes
+        uint32_t tA = tO, tB = tO;
+        const bool one = pair || n < 2;    // a single O
+        if (pair) {
+          wait(&o_full[g], (g ? n_out1 : n_out0) & 1);
+          ++n_out0;
+          ++n_out1;
+        } else {
+          wait(&o_full[0], n_out0++ & 1);
+          if (!one) wait(&o_full[1], n_out1++ & 1);
+          ml[g * 128 + lr] = make_float2(m, l);
+          named_bar_sync(1, 256);
+          const float2 a = ml[lr], b = ml[128 + lr];
+          const float M = fmaxf(a.x, b.x);
+          w0 = a.x == -INFINITY ? 0.f : ex2(a.x - M);
+          w1 = b.x == -INFINITY ? 0.f : ex2(b.x - M);
+          l = w0 * a.y + w1 * b.y;
+          m = M;
+          ca = g * (D / 2);
+          cb = ca + D / 2;
+          tA = trow + 256;
+          tB = trow + 256 + D;
         }
-        l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-        tmem_wait_st();
-        if (!FP8 && !tile_whole(it, base)) {
-          // value rows that no row of the item sees (a row per thread)
-          const int slot = 2 * (N + j) + 1;
-          wait(&kv_full[slot % S], (slot / S) & 1);
-          if (!key_seen(it, base + lr)) {
-            unsigned char* vr = ring + (slot % S) * C::TILE + lr * 128;
-            for (int b = 0; b < C::CHUNKS; ++b)
+        tc_fence_after();
+        if (__any_sync(0xffffffffu, live)) {
+          RowOut ro = {0.f, 1.f, 0.f};
+          if (whole && live) ro = row_out(o, has_prev, orow, m, l, d.v_scale);
+          const bool has = l > 0.f;
+#pragma unroll 1
+          for (int c0 = ca; c0 < cb; c0 += 32) {
+            float x[32];
+            tmem_ld32(tA + c0, x);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(vr + b * (TOK * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+            for (int i2 = 0; i2 < 32; ++i2) x[i2] = w0 > 0.f ? x[i2] * w0 : 0.f;
+            if (!one) {
+              float y[32];
+              tmem_ld32(tB + c0, y);
+#pragma unroll
+              for (int i2 = 0; i2 < 32; ++i2) x[i2] += w1 > 0.f ? y[i2] * w1 : 0.f;
+            }
+            if (!live) continue;
+            if (whole) {
+#pragma unroll
+              for (int i2 = 0; i2 < 32; i2 += 4) {
+                float4 y = has ? make_float4(x[i2] * ro.w_new, x[i2 + 1] * ro.w_new, x[i2 + 2] * ro.w_new, x[i2 + 3] * ro.w_new)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+                if (has_prev && ro.w_prev > 0.f) {
+                  const float4 z = *reinterpret_cast<const float4*>(o.prev_out + orow * D + c0 + i2);
+                  y = make_float4(y.x + ro.w_prev * z.x, y.y + ro.w_prev * z.y, y.z + ro.w_prev * z.z, y.w + ro.w_prev * z.w);
+                }
+                row_store4(o, orow * D + c0 + i2, y);
+              }
+            } else {
+#pragma unroll
+              for (int i2 = 0; i2 < 32; i2 += 4)
+                *reinterpret_cast<float4*>(sc.o + prow * D + c0 + i2) =
+                    has ? make_float4(x[i2], x[i2 + 1], x[i2 + 2], x[i2 + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
           }
-          fence_proxy_async_smem();
+          if (live && (pair || g == 0)) {
+            if (whole) row_lse(o, orow, ro.lse2);
+            else sc.ml[prow] = make_float2(m, l);
+          }
+        }
+        if (begun && !done && warp == 4 && lane == 0) {
+          // the item goes on in the next CTAs: up to the one that holds its last tile
+          const int per = plan[5];
+          const long long f_end = (long long)per * c + N + it.nt;
+          sc.meta[c] = {it.t0, it.row0, nrows, it.h * d.G, (int)((f_end - 1) / per), it.s, 0, 0};
         }
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[g]);
-        ++n_ops;
+        if (!pair) named_bar_sync(1, 256);     // both groups have read the states and both O
+        N += n;
       }
-      // ---------------------------------------------------------------- the piece's end
-      const bool begun = j0 == 0, done = j0 + n == it.nt;
-      const int tok = it.t0 + row / d.G, head = it.h * d.G + row % d.G;
-      const size_t orow = (size_t)tok * d.Hq + head;
-      const bool whole = begun && done;
-      const size_t prow = ((size_t)c * 2 + (begun ? 1 : 0)) * 256 + r;      // partial state's place
-      const bool has_prev = o.prev_out && it.s >= o.prev_req[0] && it.s < o.prev_req[o.n_prev];
-      float w0 = 1.f, w1 = 0.f;          // weights of the two groups' O
-      int ca = 0, cb = D;                // columns this thread writes
-      uint32_t tA = tO, tB = tO;
-      if (pair) {
-        wait(&o_full[g], n_out[g] & 1);
-        ++n_out[0];
-        ++n_out[1];
-      } else {
-        const int both = min(n, 2);       // groups with a tile
-        wait(&o_full[0], n_out[0]++ & 1);
-        if (both == 2) wait(&o_full[1], n_out[1]++ & 1);
-        ml[g * 128 + lr] = make_float2(m, l);
-        named_bar_sync(1, 256);
-        const float2 a = ml[lr], b = ml[128 + lr];
-        const float M = fmaxf(a.x, b.x);
-        w0 = a.x == -INFINITY ? 0.f : ex2(a.x - M);
-        w1 = b.x == -INFINITY ? 0.f : ex2(b.x - M);
-        l = w0 * a.y + w1 * b.y;
-        m = M;
-        ca = g * (D / 2);
-        cb = ca + D / 2;
-        tA = trow + 256;
-        tB = trow + 256 + D;
-      }
-      tc_fence_after();
-      const bool one = pair || n < 2;    // a single O
-      if (__any_sync(0xffffffffu, live)) {
-        RowOut ro = {0.f, 1.f, 0.f};
-        if (whole && live) ro = row_out(o, has_prev, orow, m, l, d.v_scale);
-        const bool has = l > 0.f;
-#pragma unroll 1
-        for (int c0 = ca; c0 < cb; c0 += 32) {
-          float x[32];
-          tmem_ld32(tA + c0, x);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = w0 > 0.f ? x[i] * w0 : 0.f;
-          if (!one) {
-            float y[32];
-            tmem_ld32(tB + c0, y);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] += w1 > 0.f ? y[i] * w1 : 0.f;
-          }
-          if (!live) continue;
-          if (whole) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              float4 y = has ? make_float4(x[i] * ro.w_new, x[i + 1] * ro.w_new, x[i + 2] * ro.w_new, x[i + 3] * ro.w_new)
-                             : make_float4(0.f, 0.f, 0.f, 0.f);
-              if (has_prev && ro.w_prev > 0.f) {
-                const float4 z = *reinterpret_cast<const float4*>(o.prev_out + orow * D + c0 + i);
-                y = make_float4(y.x + ro.w_prev * z.x, y.y + ro.w_prev * z.y, y.z + ro.w_prev * z.z, y.w + ro.w_prev * z.w);
-              }
-              row_store4(o, orow * D + c0 + i, y);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(sc.o + prow * D + c0 + i) =
-                  has ? make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-          }
-        }
-        if (live && (pair || g == 0)) {
-          if (whole) row_lse(o, orow, ro.lse2);
-          else sc.ml[prow] = make_float2(m, l);
-        }
-      }
-      if (begun && !done && warp == 4 && lane == 0) {
-        // the item goes on in the next CTAs: up to the one that holds its last tile
-        const long long f_end = (long long)per * c + (start[2] - left) + it.nt;
-        sc.meta[c] = {it.t0, it.row0, it.nrows, it.h * d.G, (int)((f_end - 1) / per), it.s, 0, 0};
-      }
-      tc_fence_before();
-      if (!pair) named_bar_sync(1, 256);     // both groups have read the states and both O
-      N += n;
-      advance(n);
-      if (left <= 0 && warp == 4 && lane == 0 && !(begun && !done)) sc.meta[c].nrows = 0;
-    }
-    if (start[2] == 0 && warp == 4 && lane == 0) sc.meta[c].nrows = 0;
+    } while (more());
   } else if constexpr (FP8) {
     // ------------------------------------------------------------------ E4M3 codes -> bf16 tiles
+    regs_dec<C::REGS_LOW>();
     int k = 0;
     bool ok = true;
-    while (left > 0 && ok) {
-      const Item it = next_item();
-      const int n = min(left, it.nt - j0);
-      for (int j = j0; j < j0 + n && ok; ++j) {
-        const int base = tile_base(it, j);
-        const bool part = !tile_whole(it, base);
-        for (int x = 0; x < 2; ++x, ++k) {
-          const int s = k % S, rs = k % C::STAGING;
-          ok = __all_sync(0xffffffffu, wait(&raw_full[rs], (k / C::STAGING) & 1) &&
-                                           (k < S || wait(&kv_empty[s], ((k / S) & 1) ^ 1)));
-          if (!ok) break;
-          const unsigned char* src = stg + rs * C::CODES;
-          unsigned char* dst = ring + s * C::TILE;
-          constexpr int VEC = D / 16;              // 16-code vectors of a row
+    do {
+      const int cnt = plan[3];
+      for (int i = 0; i < cnt && ok; ++i) {
+        const Piece& it = pieces[i];
+        const int j1 = it.j0 + it.n;
+        for (int j = it.j0; j < j1 && ok; ++j) {
+          const int base = tile_base(it, j);
+          const bool part = !tile_whole(it, base);
+          for (int x = 0; x < 2; ++x, ++k) {
+            const int s = k % S, rs = k % C::STAGING;
+            ok = __all_sync(0xffffffffu, wait(&raw_full[rs], (k / C::STAGING) & 1) &&
+                                             (k < S || wait(&kv_empty[s], ((k / S) & 1) ^ 1)));
+            if (!ok) break;
+            const unsigned char* src = stg + rs * C::CODES;
+            unsigned char* dst = ring + s * C::TILE;
+            constexpr int VEC = D / 16;              // 16-code vectors of a row
 #pragma unroll 4
-          for (int i = tid - 384; i < TOK * VEC; i += 128) {
-            const int row = i / VEC, v = i - row * VEC;
-            uint4 w = *reinterpret_cast<const uint4*>(src + row * D + v * 16);
-            if (x && part && !key_seen(it, base + row)) w = make_uint4(0, 0, 0, 0);
-            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-            uint32_t out[8];
+            for (int y = tid - 384; y < TOK * VEC; y += 128) {
+              const int row = y / VEC, v = y - row * VEC;
+              uint4 w = *reinterpret_cast<const uint4*>(src + row * D + v * 16);
+              if (x && part && !key_seen(it, base + row)) w = make_uint4(0, 0, 0, 0);
+              const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+              uint32_t out[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              uint32_t h2;
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(in[e >> 1] >> ((e & 1) * 16))));
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-              out[e] = pack_bf16x2(f.x, f.y);
+              for (int e = 0; e < 8; ++e) {
+                uint32_t h2;
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(in[e >> 1] >> ((e & 1) * 16))));
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                out[e] = pack_bf16x2(f.x, f.y);
+              }
+              unsigned char* p = dst + (v >> 2) * (TOK * 128) + row * 128;
+              const int c16 = (v & 3) * 2;
+              *reinterpret_cast<uint4*>(p + ((c16 ^ (row & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
+              *reinterpret_cast<uint4*>(p + (((c16 + 1) ^ (row & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
             }
-            unsigned char* p = dst + (v >> 2) * (TOK * 128) + row * 128;
-            const int c16 = (v & 3) * 2;
-            *reinterpret_cast<uint4*>(p + ((c16 ^ (row & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
-            *reinterpret_cast<uint4*>(p + (((c16 + 1) ^ (row & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&raw_empty[rs]);
-            mbar_arrive(&kv_full[s]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&raw_empty[rs]);
+              mbar_arrive(&kv_full[s]);
+            }
           }
         }
       }
-      advance(n);
-    }
+    } while (more());
   }
   tc_fence_before();
   __syncthreads();
