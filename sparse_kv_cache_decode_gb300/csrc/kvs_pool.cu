@@ -1,6 +1,7 @@
 // Device-resident KV pools, host side: configuration checks, workspace carving and the C-ABI entry points.
 #include <math.h>
 
+#include <algorithm>
 #include <new>
 
 #include "kvs_pool.cuh"
@@ -74,7 +75,7 @@ PoolPlan pool_plan(const PoolDims& d) {
   p.lse2 = align_up((size_t)d.max_tokens * d.Hq * 4);
   p.prev_lse2 = align_up((size_t)d.max_prefix_tokens * d.Hq * 4);
   p.prev_out = align_up((size_t)d.max_prefix_tokens * d.Hq * d.d * 4);
-  p.scratch = align_up(pool_attn_scratch_bytes(d));
+  p.scratch = align_up(std::max(pool_attn_scratch_bytes(d), pool_weight_scratch_bytes()));
   p.total = p.err + p.lse2 + p.prev_lse2 + p.prev_out + p.scratch;
   return p;
 }
@@ -222,8 +223,8 @@ kvs_status kvs_pool_attn(kvs_pool* c, int layer, const void* d_q, long long q_st
                                    c->scratch, c->err, S(stream), &n);
   c->launches += n;
   if (e == cudaSuccess && d_weight) {
-    e = launch_pool_weight(d, k, &c->maps[2 * layer], q, q_stride, seqs, c->lse2, d_weight, c->err, S(stream));
-    c->launches += 1;
+    e = launch_pool_weight(d, &c->maps[2 * layer], q, q_stride, seqs, c->lse2, d_weight, c->scratch, c->err, S(stream), &n);
+    c->launches += n;
   }
   return cuda_status(e);
 }

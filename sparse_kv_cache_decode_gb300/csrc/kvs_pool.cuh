@@ -90,9 +90,10 @@ size_t pool_attn_scratch_bytes(const PoolDims& d);
 cudaError_t launch_pool_attn(const PoolDims& d, const unsigned char* k, const unsigned char* v, const CUtensorMap* tm,
                              const __nv_bfloat16* q, long long q_stride, const PoolSeqs& seqs, const PoolAttnOut& o,
                              void* scratch, unsigned* err, cudaStream_t s, int* n_launched);
-cudaError_t launch_pool_weight(const PoolDims& d, const unsigned char* k, const CUtensorMap* tm, const __nv_bfloat16* q,
-                               long long q_stride, const PoolSeqs& seqs, const float* lse2, float* weight,
-                               unsigned* err, cudaStream_t s);
+size_t pool_weight_scratch_bytes();
+cudaError_t launch_pool_weight(const PoolDims& d, const CUtensorMap* tm, const __nv_bfloat16* q, long long q_stride,
+                               const PoolSeqs& seqs, const float* lse2, float* weight, void* scratch, unsigned* err,
+                               cudaStream_t s, int* n_launched);
 cudaError_t launch_pool_evict(const PoolDims& d, unsigned char* k, unsigned char* v, const float* weight,
                               const int* ctx_len, const int* table, int n_req, int keep, int n_sink, int n_recent,
                               const int* dst, int* kept, int* n_kept, float* weight_out, unsigned* err, cudaStream_t s);

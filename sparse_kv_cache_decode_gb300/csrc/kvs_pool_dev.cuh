@@ -1,0 +1,116 @@
+// Device helpers of the pool kernels that run on the tensor cores.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "kvs_pool.cuh"
+#include "kvs_ptx.cuh"
+
+namespace kvs {
+namespace pdev {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int TOK = 128;                      // tokens per K/V tile
+constexpr int MAX_SMEM = 227 * 1024;
+constexpr int kPieces = 64;                   // pieces of work a CTA plans at a time
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// pairs of fp32 in one 64-bit register
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// the lowest n bits (n < 0: none, n > 32: all)
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// Exclusive scans of a count and a sum over the CTA's threads in one; ws: 64 words of shared memory.
+struct Scan {
+  int n, n_all;
+  long long v, v_all;
+};
+__device__ __forceinline__ Scan block_scan(int n, long long v, long long* ws, int nw) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int xn = n;
+  long long xv = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int yn = __shfl_up_sync(0xffffffffu, xn, o);
+    const long long yv = __shfl_up_sync(0xffffffffu, xv, o);
+    if (lane >= o) {
+      xn += yn;
+      xv += yv;
+    }
+  }
+  __syncthreads();
+  if (lane == 31) {
+    ws[2 * warp] = xn;
+    ws[2 * warp + 1] = xv;
+  }
+  __syncthreads();
+  Scan r = {xn - n, 0, xv - v, 0};
+  for (int w = 0; w < nw; ++w) {
+    const int a = (int)ws[2 * w];
+    const long long b = ws[2 * w + 1];
+    if (w < warp) {
+      r.n += a;
+      r.v += b;
+    }
+    r.n_all += a;
+    r.v_all += b;
+  }
+  return r;
+}
+
+// The rest of a bounded wait on a barrier that was not ready at once.
+__device__ __forceinline__ bool slow_wait(uint64_t* bar, unsigned parity, uint64_t timeout_ns, volatile int* abort_flag,
+                                       unsigned* err) {
+  const uint64_t t = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t > timeout_ns) {
+      set_error(err, KVS_ERR_TIMEOUT);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+// 16 E4M3 codes (vector v of a row) as bf16, exactly (through f16, which holds every E4M3 value), into the row of a
+// K-major 128-byte-swizzled tile: `p` the row in its first 64-dim chunk, chunks `chunk` bytes apart.
+__device__ __forceinline__ void widen16(const uint4& w, unsigned char* p, int chunk, int row, int v) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t out[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(in[e >> 1] >> ((e & 1) * 16))));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+    out[e] = pack_bf16x2(f.x, f.y);
+  }
+  p += (v >> 2) * chunk;
+  const int c16 = (v & 3) * 2;
+  *reinterpret_cast<uint4*>(p + ((c16 ^ (row & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
+  *reinterpret_cast<uint4*>(p + (((c16 + 1) ^ (row & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+}  // namespace pdev
+}  // namespace kvs
