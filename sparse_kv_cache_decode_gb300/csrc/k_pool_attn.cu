@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
   const uint64_t timeout_ns = (uint64_t)d.timeout_us * 1000ull;
   const int total = plan[2];            // the CTA's tiles
   auto wait = [&](uint64_t* bar, unsigned parity) {
@@ -488,42 +488,45 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
       if (g) pend1 = -1; else pend0 = -1;
       older = g ^ 1;
       const int slot = 2 * (info >> 3) + 1, s = slot % S;
-      if (!wait(&p_full[g], (pv_par >> g) & 1) || !wait(&kv_full[s], (slot / S) & 1)) {
-        ok = false;
-        return;
-      }
+      ok = __all_sync(0xffffffffu, wait(&kv_full[s], (slot / S) & 1) && wait(&p_full[g], (pv_par >> g) & 1));
+      if (!ok) return;
       pv_par ^= 1 << g;
       tc_fence_after();
       const uint64_t dv = dv0 + (uint64_t)((s * C::TILE) >> 4);
+      if (elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < TOK / 16; ++kk)
-        tc_mma_f16_ts(tmem + 256 + g * D, tmem + g * 128 + kk * 8, dv + (uint64_t)(kk * 2048 >> 4), id_pv,
-                      kk > 0 || !(info & 1));
-      if (!(info & 4) || g) tc_commit(&kv_empty[s]);
-      if (info & 2) tc_commit(&o_full[g]);
+        for (int kk = 0; kk < TOK / 16; ++kk)
+          tc_mma_f16_ts(tmem + 256 + g * D, tmem + g * 128 + kk * 8, dv + (uint64_t)(kk * 2048 >> 4), id_pv,
+                        kk > 0 || !(info & 1));
+        if (!(info & 4) || g) tc_commit(&kv_empty[s]);
+        if (info & 2) tc_commit(&o_full[g]);
+      }
+    };
+    auto flush = [&]() {
+      for (int y = 0; y < 2 && ok; ++y)
+        if ((older ? pend1 : pend0) >= 0) pv(older);
+        else if ((older ? pend0 : pend1) >= 0) pv(older ^ 1);
     };
     do {
-      const int cnt = plan[3];
-      if (lane == 0) {
-        for (int i = 0; i < cnt && ok; ++i, ++piece) {
-          const int nrows = pieces[i].nrows, n = pieces[i].n;
-          const bool pair = nrows > 128;
-          qb = nrows <= C::QHALF ? qb ^ 1 : 0;
-          const int n_ops = pair ? 2 * n : n;
-          if (!mbar_try_wait(&q_full[piece & 1], (piece >> 1) & 1)) {
-            // while Q is on its way: what is due
-            for (int y = 0; y < 2 && ok; ++y)
-              if ((older ? pend1 : pend0) >= 0) pv(older);
-              else if ((older ? pend0 : pend1) >= 0) pv(older ^ 1);
-            if (!ok || !wait(&q_full[piece & 1], (piece >> 1) & 1)) { ok = false; break; }
-          }
-          for (int x = 0; x < n_ops && ok; ++x) {
-            const int g = x & 1, tile = N + (pair ? x >> 1 : x), s = (2 * tile) % S;
-            while ((g ? pend1 : pend0) >= 0 && ok) pv((older ? pend1 : pend0) >= 0 ? older : g);
-            if (!ok || !wait(&kv_full[s], ((2 * tile) / S) & 1)) { ok = false; break; }
-            tc_fence_after();
-            const uint64_t dk = dr0 + (uint64_t)((s * C::TILE) >> 4);
-            const uint64_t da = dq0 + (uint64_t)((pair ? g * 128 : qb * C::QHALF) * 128 >> 4);
+      const int cnt = uniform(plan[3]);
+      for (int i = 0; i < cnt && ok; ++i, ++piece) {
+        const int nrows = uniform(pieces[i].nrows), n = uniform(pieces[i].n);
+        const bool pair = nrows > 128;
+        qb = nrows <= C::QHALF ? qb ^ 1 : 0;
+        const int n_ops = pair ? 2 * n : n;
+        if (!__all_sync(0xffffffffu, mbar_try_wait(&q_full[piece & 1], (piece >> 1) & 1))) {
+          flush();                       // while Q is on its way: what is due
+          if (ok) ok = __all_sync(0xffffffffu, wait(&q_full[piece & 1], (piece >> 1) & 1));
+        }
+        for (int x = 0; x < n_ops && ok; ++x) {
+          const int g = x & 1, tile = N + (pair ? x >> 1 : x), s = (2 * tile) % S;
+          while ((g ? pend1 : pend0) >= 0 && ok) pv((older ? pend1 : pend0) >= 0 ? older : g);
+          if (ok) ok = __all_sync(0xffffffffu, wait(&kv_full[s], ((2 * tile) / S) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dk = dr0 + (uint64_t)((s * C::TILE) >> 4);
+          const uint64_t da = dq0 + (uint64_t)((pair ? g * 128 : qb * C::QHALF) * 128 >> 4);
+          if (elect_one()) {
 #pragma unroll
             for (int k16 = 0; k16 < D / 16; ++k16)
               tc_mma_f16(tmem + g * 128, da + (uint64_t)(((k16 >> 2) * C::QCHUNK + (k16 & 3) * 32) >> 4),
@@ -531,23 +534,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
             tc_commit(&s_full[g]);
             if (!pair || g) tc_commit(&kv_empty[s]);
             if (x == n_ops - 1) tc_commit(q_free);
-            const int info = tile * 8 + (pair ? 4 : 0) + (x + 2 >= n_ops ? 2 : 0) + (x < 2 ? 1 : 0);
-            if (g) pend1 = info; else pend0 = info;
-            if ((g ? pend0 : pend1) < 0) older = g;
           }
-          N += n;
+          const int info = tile * 8 + (pair ? 4 : 0) + (x + 2 >= n_ops ? 2 : 0) + (x < 2 ? 1 : 0);
+          if (g) pend1 = info; else pend0 = info;
+          if ((g ? pend0 : pend1) < 0) older = g;
         }
-        for (int y = 0; y < 2 && ok; ++y)
-          if ((older ? pend1 : pend0) >= 0) pv(older);
-          else if ((older ? pend0 : pend1) >= 0) pv(older ^ 1);
+        N += n;
       }
+      if (ok) flush();
       __syncwarp();
     } while (more());
-    if (lane == 0) {
-      // every product issued by this thread has finished before the tensor memory is released
-      tc_commit(drained);
-      mbar_wait(drained, 0, kDrainTimeoutNs);
-    }
+    // every product issued here has finished before the tensor memory is released
+    if (elect_one()) tc_commit(drained);
+    mbar_wait(drained, 0, kDrainTimeoutNs);
     __syncwarp();
   } else if (warp < 4) {
     // ------------------------------------------------------------------ Q

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
   const uint64_t timeout_ns = (uint64_t)d.timeout_us * 1000ull;
   auto wait = [&](uint64_t* bar, unsigned parity) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -345,22 +345,23 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     int k = 0, J = 0, ops0 = 0, ops1 = 0;
     bool ok = true;
     do {
-      const int cnt = plan[3];
-      if (lane == 0) {
-        for (int i = 0; i < cnt && ok; ++i) {
-          const Piece& it = pieces[i];
-          const int n = it.n, groups = it.k0 + TOK < it.len ? 2 : 1;
-          for (int g = 0; g < groups && ok; ++g) ok = wait(&k_full[(k + g) % KS], ((k + g) / KS) & 1);
-          for (int j = 0; j < n && ok; ++j, ++J) {
-            const int s = J % QS;
-            if (!wait(&q_full[s], (J / QS) & 1)) { ok = false; break; }
-            const int tok0 = (it.rt0 + it.j0 + j) * T, nr = min(T, it.R - tok0) * d.G;
-            const uint32_t idesc = idesc_bf16_f32(128, (nr + 15) & ~15);
-            for (int g = 0; g < groups && ok; ++g) {
-              const int op = g ? ops1++ : ops0++, b = g * 2 + (op & 1);
-              if (op >= 2 && !wait(&s_empty[b], ((op >> 1) - 1) & 1)) { ok = false; break; }
-              tc_fence_after();
-              const uint64_t da = dk0 + (uint64_t)((((k + g) % KS) * C::TILE) >> 4), db = dq0 + (uint64_t)((s * C::TILE) >> 4);
+      const int cnt = uniform(plan[3]);
+      for (int i = 0; i < cnt && ok; ++i) {
+        const int n = uniform(pieces[i].n), groups = uniform(pieces[i].k0 + TOK < pieces[i].len ? 2 : 1);
+        const int tile0 = uniform(pieces[i].rt0 + pieces[i].j0), R = uniform(pieces[i].R);
+        for (int g = 0; g < groups && ok; ++g) ok = __all_sync(0xffffffffu, wait(&k_full[(k + g) % KS], ((k + g) / KS) & 1));
+        for (int j = 0; j < n && ok; ++j, ++J) {
+          const int s = J % QS;
+          ok = __all_sync(0xffffffffu, wait(&q_full[s], (J / QS) & 1));
+          const int nr = min(T, R - (tile0 + j) * T) * d.G;
+          const uint32_t idesc = idesc_bf16_f32(128, (nr + 15) & ~15);
+          for (int g = 0; g < groups && ok; ++g) {
+            const int op = g ? ops1++ : ops0++, b = g * 2 + (op & 1);
+            if (op >= 2) ok = __all_sync(0xffffffffu, wait(&s_empty[b], ((op >> 1) - 1) & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t da = dk0 + (uint64_t)((((k + g) % KS) * C::TILE) >> 4), db = dq0 + (uint64_t)((s * C::TILE) >> 4);
+            if (elect_one()) {
 #pragma unroll
               for (int k16 = 0; k16 < D / 16; ++k16) {
                 const uint64_t off = (uint64_t)(((k16 >> 2) * (TOK * 128) + (k16 & 3) * 32) >> 4);
@@ -371,15 +372,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
               if (j == n - 1) tc_commit(&k_empty[(k + g) % KS]);
             }
           }
-          k += groups;
         }
+        k += groups;
       }
       __syncwarp();
     } while (more());
-    if (lane == 0) {
-      tc_commit(drained);
-      mbar_wait(drained, 0, kDrainTimeoutNs);
-    }
+    if (elect_one()) tc_commit(drained);
+    mbar_wait(drained, 0, kDrainTimeoutNs);
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------------ Q tiles: T tokens x G heads x 64 dims a load

@@ -19,6 +19,16 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// One lane of the (whole) warp, always the same.  The products of a warp are issued under it from values that all
+// lanes hold, so that descriptors stay in uniform registers (measured for 128 x 64 x 16 products: 28 cycles to
+// issue one, against 51 under `lane == 0`).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}\n" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // pairs of fp32 in one 64-bit register
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
