@@ -5,8 +5,8 @@
 // visited in tiles of 128 tokens: the tiles of the first n_sink tokens, then those of the window's span.
 //   S = Q K^T (128 x 128, fp32 in tensor memory),  P = 2^(S scale log2 e - m) in bf16 over S's columns,
 //   O (128 x d, fp32 in tensor memory) += P V,      out = v_scale O / l,  l = sum of P before its rounding.
-// m is raised (and O rescaled) only when a tile's maximum passes it by more than 2^8, so P stays below 2^8.
-// P is rounded to bf16 (relative error 2^-9 on average of both signs, as the output's own rounding); S, m, l
+// m is raised (and O rescaled) only when a tile's maximum passes it by more than 2^32: the scale cancels in O / l and
+// fp32 has room for it (O < 2^32 * keys * |v|), so after the first tile a rescale is rare.  P is rounded to bf16 (relative error 2^-9 on average of both signs, as the output's own rounding); S, m, l
 // and O are fp32.
 //
 // Two softmax groups of 4 warps, one thread per row.  Where an item has more than 128 rows each group takes
@@ -37,7 +37,7 @@ namespace pa {
 using namespace pdev;
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kMaxGrowth = 8.f;
+constexpr float kMaxGrowth = 32.f;           // log2 of the largest P
 
 struct Split {
   int n_cta;
@@ -229,12 +229,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
   uint64_t* raw_full = bars + 16;       // [4] code tiles (E4M3)
   uint64_t* raw_empty = bars + 20;      // [4]
   uint64_t* s_full = bars + 24;         // [2]
-  uint64_t* p_full = bars + 26;         // [2]
-  uint64_t* o_full = bars + 28;         // [2]
-  uint64_t* q_full = bars + 30;         // [2] by piece parity
-  uint64_t* q_free = bars + 32;
-  uint64_t* drained = bars + 33;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 34);
+  uint64_t* p_full = bars + 26;         // [half][2]: P of the tile's first and last 64 keys
+  uint64_t* o_full = bars + 30;         // [2]
+  uint64_t* q_full = bars + 32;         // [2] by piece parity
+  uint64_t* q_free = bars + 34;
+  uint64_t* drained = bars + 35;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 36);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   // position and first tile of the CTA's next piece, its tiles still to plan, pieces planned, items, tiles per CTA
   volatile int* plan = reinterpret_cast<volatile int*>(tmem_slot + 2);
@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
     for (int g = 0; g < 2; ++g) {
       mbar_init(&s_full[g], 1);
       mbar_init(&p_full[g], 4);
+      mbar_init(&p_full[2 + g], 4);
       mbar_init(&o_full[g], 1);
     }
     mbar_init(&q_full[0], 2);
@@ -370,10 +371,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
   const uint64_t timeout_ns = (uint64_t)d.timeout_us * 1000ull;
   const int total = plan[2];            // the CTA's tiles
-  auto wait = [&](uint64_t* bar, unsigned parity) {
-    if (mbar_try_wait(bar, parity)) return true;
-    return slow_wait(bar, parity, timeout_ns, abort_flag, err);
-  };
+  auto wait = [&](uint64_t* bar, unsigned parity) { return bounded_wait(bar, parity, timeout_ns, abort_flag); };
   // Plans the CTA's next kPieces pieces (warp 0, a lane per piece).
   auto plan_pieces = [&]() {
     int pos = plan[0], j0 = plan[1], left = plan[2], cnt = 0;
@@ -471,8 +469,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
     for (int i = max(0, k - SLOTS); i < k; ++i) mbar_wait(&full[i % SLOTS], (i / SLOTS) & 1, kDrainTimeoutNs);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ products
-    // Operation x of a piece: S of tile x / 2 for group x % 2 (two row tiles), or of tile x for group x % 2 (one
-    // row tile).  Its PV is issued before the group's next S, which overwrites P, oldest first.
+    // Two row tiles: per K/V tile, group by group: PV of this tile once P is there, then S of the next tile, which
+    // overwrites P.  One row tile: S of tile x for group x % 2, PV of the group's last tile before it, oldest first,
+    // across pieces.  The tensor pipe idles whenever this thread is late, so the waits ahead of a product are few:
+    // K and V once per tile, P in halves.
     regs_dec<C::REGS_LOW>();
     const uint32_t id_qk = idesc_bf16_f32(128, TOK);
     const uint32_t id_pv = idesc_bf16_f32(128, D) | (1u << 16);     // V is read MN-major
@@ -480,68 +480,120 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
     const uint64_t dr0 = smem_desc_sw128(smem_u32(ring));
     const uint64_t dv0 = smem_desc_sw128_mn(smem_u32(ring), TOK * 128, 1024);
     int N = 0, piece = 0, qb = 0;   // tiles and pieces before this one, the half that holds its Q
-    int pend0 = -1, pend1 = -1;     // the groups' operations whose PV is due: tile * 8 + pair * 4 + last * 2 + first
-    int older = 0, pv_par = 0;      // the group whose operation came first; parity of each group's next P
+    int pend0 = -1, pend1 = -1;     // one row tile: the groups' operations whose PV is due: tile * 4 + last * 2 + first
+    int older = 0;                  // the group whose operation came first
+    unsigned par0 = 0, par1 = 0;    // parity of each group's next P
     bool ok = true;
-    auto pv = [&](int g) {
-      const int info = g ? pend1 : pend0;
+    auto qk = [&](int g, int s, int qrow) {
+      const uint64_t dk = dr0 + (uint64_t)(s * (C::TILE >> 4)), da = dq0 + (uint64_t)(qrow * (128 >> 4));
+#pragma unroll
+      for (int k16 = 0; k16 < D / 16; ++k16)
+        tc_mma_f16(tmem + g * 128, da + (uint64_t)(((k16 >> 2) * C::QCHUNK + (k16 & 3) * 32) >> 4),
+                   dk + (uint64_t)(((k16 >> 2) * (TOK * 128) + (k16 & 3) * 32) >> 4), id_qk, k16 != 0);
+      tc_commit(&s_full[g]);
+    };
+    auto pv = [&](int g, int s, bool first, unsigned& par) {
+      const uint64_t dv = dv0 + (uint64_t)(s * (C::TILE >> 4));
+      ok = wait(&p_full[g], par);
+      if (!ok) return;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < TOK / 32; ++kk)
+        tc_mma_f16_ts(tmem + 256 + g * D, tmem + g * 128 + kk * 8, dv + (uint64_t)(kk * 2048 >> 4), id_pv, kk > 0 || !first);
+      // the other half, while the first one's products run
+      ok = wait(&p_full[2 + g], par);
+      if (!ok) return;
+      par ^= 1;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = TOK / 32; kk < TOK / 16; ++kk)
+        tc_mma_f16_ts(tmem + 256 + g * D, tmem + g * 128 + kk * 8, dv + (uint64_t)(kk * 2048 >> 4), id_pv, 1);
+    };
+    auto pv_due = [&](int g) {
+      const int info = g ? pend1 : pend0, slot = 2 * (info >> 2) + 1, s = slot % S;
       if (g) pend1 = -1; else pend0 = -1;
       older = g ^ 1;
-      const int slot = 2 * (info >> 3) + 1, s = slot % S;
-      ok = __all_sync(0xffffffffu, wait(&kv_full[s], (slot / S) & 1) && wait(&p_full[g], (pv_par >> g) & 1));
+      ok = wait(&kv_full[s], (slot / S) & 1);
       if (!ok) return;
-      pv_par ^= 1 << g;
-      tc_fence_after();
-      const uint64_t dv = dv0 + (uint64_t)((s * C::TILE) >> 4);
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < TOK / 16; ++kk)
-          tc_mma_f16_ts(tmem + 256 + g * D, tmem + g * 128 + kk * 8, dv + (uint64_t)(kk * 2048 >> 4), id_pv,
-                        kk > 0 || !(info & 1));
-        if (!(info & 4) || g) tc_commit(&kv_empty[s]);
-        if (info & 2) tc_commit(&o_full[g]);
-      }
+      if (g) pv(1, s, info & 1, par1); else pv(0, s, info & 1, par0);
+      if (!ok) return;
+      tc_commit(&kv_empty[s]);
+      if (info & 2) tc_commit(&o_full[g]);
     };
     auto flush = [&]() {
-      for (int y = 0; y < 2 && ok; ++y)
-        if ((older ? pend1 : pend0) >= 0) pv(older);
-        else if ((older ? pend0 : pend1) >= 0) pv(older ^ 1);
+      for (int y = 0; y < 2 && ok; ++y) {
+        const int g = (older ? pend1 : pend0) >= 0 ? older : older ^ 1;
+        if ((g ? pend1 : pend0) >= 0) pv_due(g);
+      }
     };
     do {
-      const int cnt = uniform(plan[3]);
-      for (int i = 0; i < cnt && ok; ++i, ++piece) {
-        const int nrows = uniform(pieces[i].nrows), n = uniform(pieces[i].n);
-        const bool pair = nrows > 128;
-        qb = nrows <= C::QHALF ? qb ^ 1 : 0;
-        const int n_ops = pair ? 2 * n : n;
-        if (!__all_sync(0xffffffffu, mbar_try_wait(&q_full[piece & 1], (piece >> 1) & 1))) {
-          flush();                       // while Q is on its way: what is due
-          if (ok) ok = __all_sync(0xffffffffu, wait(&q_full[piece & 1], (piece >> 1) & 1));
-        }
-        for (int x = 0; x < n_ops && ok; ++x) {
-          const int g = x & 1, tile = N + (pair ? x >> 1 : x), s = (2 * tile) % S;
-          while ((g ? pend1 : pend0) >= 0 && ok) pv((older ? pend1 : pend0) >= 0 ? older : g);
-          if (ok) ok = __all_sync(0xffffffffu, wait(&kv_full[s], ((2 * tile) / S) & 1));
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t dk = dr0 + (uint64_t)((s * C::TILE) >> 4);
-          const uint64_t da = dq0 + (uint64_t)((pair ? g * 128 : qb * C::QHALF) * 128 >> 4);
-          if (elect_one()) {
-#pragma unroll
-            for (int k16 = 0; k16 < D / 16; ++k16)
-              tc_mma_f16(tmem + g * 128, da + (uint64_t)(((k16 >> 2) * C::QCHUNK + (k16 & 3) * 32) >> 4),
-                         dk + (uint64_t)(((k16 >> 2) * (TOK * 128) + (k16 & 3) * 32) >> 4), id_qk, k16 != 0);
-            tc_commit(&s_full[g]);
-            if (!pair || g) tc_commit(&kv_empty[s]);
-            if (x == n_ops - 1) tc_commit(q_free);
+      const int cnt = plan[3];
+      if (elect_one()) {
+        for (int i = 0; i < cnt && ok; ++i, ++piece) {
+          const int nrows = pieces[i].nrows, n = pieces[i].n;
+          qb = nrows <= C::QHALF ? qb ^ 1 : 0;
+          if (nrows > 128 || !mbar_try_wait(&q_full[piece & 1], (piece >> 1) & 1)) {
+            flush();                       // while Q is on its way: what is due
+            if (!ok || !wait(&q_full[piece & 1], (piece >> 1) & 1)) { ok = false; break; }
           }
-          const int info = tile * 8 + (pair ? 4 : 0) + (x + 2 >= n_ops ? 2 : 0) + (x < 2 ? 1 : 0);
-          if (g) pend1 = info; else pend0 = info;
-          if ((g ? pend0 : pend1) < 0) older = g;
+          if (QT == 2 && nrows > 128) {
+            int s = (2 * N) % S;
+            unsigned par = ((2 * N) / S) & 1;          // slot and parity of the next tile to wait for
+            auto next = [&]() {
+              if (++s == S) {
+                s = 0;
+                par ^= 1;
+              }
+            };
+            ok = wait(&kv_full[s], par);
+            if (!ok) break;
+            tc_fence_after();
+            qk(0, s, 0);
+            qk(1, s, 128);
+            tc_commit(&kv_empty[s]);
+            next();
+            for (int t = 0; t < n; ++t) {
+              const bool last = t + 1 == n;
+              if (last) tc_commit(q_free);
+              const int sv = s;
+              ok = wait(&kv_full[s], par);
+              next();
+              const int sk = s;
+              if (!last) {
+                ok = ok && wait(&kv_full[s], par);
+                next();
+              }
+              if (ok) pv(0, sv, t == 0, par0);
+              if (!ok) break;
+              if (last) tc_commit(&o_full[0]);
+              else qk(0, sk, 0);
+              pv(1, sv, t == 0, par1);
+              if (!ok) break;
+              tc_commit(&kv_empty[sv]);
+              if (last) tc_commit(&o_full[1]);
+              else {
+                qk(1, sk, 128);
+                tc_commit(&kv_empty[sk]);
+              }
+            }
+          } else {
+            for (int x = 0; x < n && ok; ++x) {
+              const int g = x & 1, tile = N + x, s = (2 * tile) % S;
+              while ((g ? pend1 : pend0) >= 0 && ok) pv_due((older ? pend1 : pend0) >= 0 ? older : g);
+              if (!ok || !wait(&kv_full[s], ((2 * tile) / S) & 1)) { ok = false; break; }
+              tc_fence_after();
+              qk(g, s, qb * C::QHALF);
+              tc_commit(&kv_empty[s]);
+              if (x == n - 1) tc_commit(q_free);
+              const int info = tile * 4 + (x + 2 >= n ? 2 : 0) + (x < 2 ? 1 : 0);
+              if (g) pend1 = info; else pend0 = info;
+              if ((g ? pend0 : pend1) < 0) older = g;
+            }
+          }
+          N += n;
         }
-        N += n;
+        if (ok) flush();
       }
-      if (ok) flush();
       __syncwarp();
     } while (more());
     // every product issued here has finished before the tensor memory is released
@@ -657,28 +709,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
           m = m_new;
           const float neg = m == -INFINITY ? 0.f : -m;
           const uint64_t sl22 = pack2(sl2, sl2), neg2 = pack2(neg, neg);
-          uint64_t ps0 = 0, ps1 = 0;
-#pragma unroll
-          for (int c0 = 0; c0 < 128; c0 += 32) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int i2 = 0; i2 < 32; i2 += 2) {
-              float a, b;
-              unpack2(fma2(pack2(s[c0 + i2], s[c0 + i2 + 1]), sl22, neg2), a, b);
-              a = ex2(a);
-              b = ex2(b);
-              if (i2 & 2) ps1 = add2(ps1, pack2(a, b));
-              else ps0 = add2(ps0, pack2(a, b));
-              pk[i2 / 2] = pack_bf16x2(a, b);
-            }
-            tmem_st16(tS + c0 / 2, pk);
-          }
-          {
-            float a, b;
-            unpack2(add2(ps0, ps1), a, b);
-            l += a + b;
-          }
-          tmem_wait_st();
           if (!FP8 && !tile_whole(it, base)) {
             // value rows that no row of the item sees (a row per thread)
             const int slot = 2 * (N + j) + 1;
@@ -692,9 +722,35 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
             }
             fence_proxy_async_smem();
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[g]);
+          uint64_t ps0 = 0, ps1 = 0;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int c0 = half * 64; c0 < half * 64 + 64; c0 += 32) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int i2 = 0; i2 < 32; i2 += 2) {
+                float a, b;
+                unpack2(fma2(pack2(s[c0 + i2], s[c0 + i2 + 1]), sl22, neg2), a, b);
+                a = ex2(a);
+                b = ex2(b);
+                if (i2 & 2) ps1 = add2(ps1, pack2(a, b));
+                else ps0 = add2(ps0, pack2(a, b));
+                pk[i2 / 2] = pack_bf16x2(a, b);
+              }
+              tmem_st16(tS + c0 / 2, pk);
+            }
+            // each half as soon as it is there: its products overlap the other half's exponentials
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * half + g]);
+          }
+          {
+            float a, b;
+            unpack2(add2(ps0, ps1), a, b);
+            l += a + b;
+          }
           ++n_ops;
         }
         // -------------------------------------------------------------- the piece's end
@@ -823,6 +879,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+    if (lane == 0 && *abort_flag) set_error(err, KVS_ERR_TIMEOUT);
   }
 }
 

@@ -251,10 +251,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
   const uint64_t timeout_ns = (uint64_t)d.timeout_us * 1000ull;
-  auto wait = [&](uint64_t* bar, unsigned parity) {
-    if (mbar_try_wait(bar, parity)) return true;
-    return slow_wait(bar, parity, timeout_ns, abort_flag, err);
-  };
+  auto wait = [&](uint64_t* bar, unsigned parity) { return bounded_wait(bar, parity, timeout_ns, abort_flag); };
   // Plans the next kPieces pieces (warp 0, a lane per item); items that no row sees are passed over.
   auto plan_pieces = [&]() {
     int pos = plan[0], j0 = plan[1], left = plan[2], cnt = 0;
@@ -562,6 +559,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+    if (lane == 0 && *abort_flag) set_error(err, KVS_ERR_TIMEOUT);
   }
 }
 

@@ -89,14 +89,19 @@ __device__ __forceinline__ Scan block_scan(int n, long long v, long long* ws, in
   return r;
 }
 
-// The rest of a bounded wait on a barrier that was not ready at once.
-__device__ __forceinline__ bool slow_wait(uint64_t* bar, unsigned parity, uint64_t timeout_ns, volatile int* abort_flag,
-                                       unsigned* err) {
-  const uint64_t t = global_timer_ns();
-  while (!mbar_try_wait(bar, parity)) {
+// Bounded wait for the phase of the given parity.  Code that runs once per tile beside the softmax's long unrolled
+// loops is limited by instruction fetch, so the rare path is short: the clock is read every 64th try, and the
+// kernel's end reports a time-out (abort_flag) once for all.
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, unsigned parity, uint64_t timeout_ns, volatile int* abort_flag) {
+  if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+  uint64_t t = 0;
+#pragma unroll 1
+  for (unsigned n = 0; !mbar_try_wait(bar, parity); ++n) {
+    if (n & 63u) continue;
     if (*abort_flag) return false;
-    if (global_timer_ns() - t > timeout_ns) {
-      set_error(err, KVS_ERR_TIMEOUT);
+    const uint64_t now = global_timer_ns();
+    if (n == 0) t = now;
+    if (now - t > timeout_ns) {
       *abort_flag = 1;
       return false;
     }
