@@ -5,8 +5,9 @@
 // visited in tiles of 128 tokens: the tiles of the first n_sink tokens, then those of the window's span.
 //   S = Q K^T (128 x 128, fp32 in tensor memory),  P = 2^(S scale log2 e - m) in bf16 over S's columns,
 //   O (128 x d, fp32 in tensor memory) += P V,      out = v_scale O / l,  l = sum of P before its rounding.
-// m is raised (and O rescaled) only when a tile's maximum passes it by more than 2^32: the scale cancels in O / l and
-// fp32 has room for it (O < 2^32 * keys * |v|), so after the first tile a rescale is rare.  P is rounded to bf16 (relative error 2^-9 on average of both signs, as the output's own rounding); S, m, l
+// m is the maximum of the first tile that a row sees.  It is not looked for again: the scale cancels in O / l and fp32
+// has room for weights above 1 (O < 2^40 * tiles * |v|), so it is enough to set m anew, and rescale O, when a tile's sum
+// passes 2^40 (a logit some 23 above the first tile's largest).  P is rounded to bf16 (relative error 2^-9 on average of both signs, as the output's own rounding); S, m, l
 // and O are fp32.
 //
 // Two softmax groups of 4 warps, one thread per row.  Where an item has more than 128 rows each group takes
@@ -37,7 +38,7 @@ namespace pa {
 using namespace pdev;
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kMaxGrowth = 32.f;           // log2 of the largest P
+constexpr float kMaxSum = 0x1p40f;              // largest sum of a tile's weights before m is set anew
 
 struct Split {
   int n_cta;
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
   uint64_t* raw_full = bars + 16;       // [4] code tiles (E4M3)
   uint64_t* raw_empty = bars + 20;      // [4]
   uint64_t* s_full = bars + 24;         // [2]
-  uint64_t* p_full = bars + 26;         // [half][2]: P of the tile's first and last 64 keys
+  uint64_t* p_full = bars + 26;         // [2]
   uint64_t* o_full = bars + 30;         // [2]
   uint64_t* q_full = bars + 32;         // [2] by piece parity
   uint64_t* q_free = bars + 34;
@@ -256,7 +257,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
     for (int g = 0; g < 2; ++g) {
       mbar_init(&s_full[g], 1);
       mbar_init(&p_full[g], 4);
-      mbar_init(&p_full[2 + g], 4);
       mbar_init(&o_full[g], 1);
     }
     mbar_init(&q_full[0], 2);
@@ -476,38 +476,31 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
     regs_dec<C::REGS_LOW>();
     const uint32_t id_qk = idesc_bf16_f32(128, TOK);
     const uint32_t id_pv = idesc_bf16_f32(128, D) | (1u << 16);     // V is read MN-major
-    const uint64_t dq0 = smem_desc_sw128(smem_u32(smem));
-    const uint64_t dr0 = smem_desc_sw128(smem_u32(ring));
-    const uint64_t dv0 = smem_desc_sw128_mn(smem_u32(ring), TOK * 128, 1024);
+    const uint32_t aq = smem_u32(smem) >> 4, ar = smem_u32(ring) >> 4;
+    constexpr uint32_t kV = (uint32_t)(TOK * 128 >> 4) << 16;       // from one 64-dim block of V to the next
     int N = 0, piece = 0, qb = 0;   // tiles and pieces before this one, the half that holds its Q
     int pend0 = -1, pend1 = -1;     // one row tile: the groups' operations whose PV is due: tile * 4 + last * 2 + first
     int older = 0;                  // the group whose operation came first
     unsigned par0 = 0, par1 = 0;    // parity of each group's next P
     bool ok = true;
     auto qk = [&](int g, int s, int qrow) {
-      const uint64_t dk = dr0 + (uint64_t)(s * (C::TILE >> 4)), da = dq0 + (uint64_t)(qrow * (128 >> 4));
+      const uint32_t k0 = ar + s * (C::TILE >> 4), q0 = aq + qrow * (128 >> 4), t = tmem + g * 128;
+      mma_ss<false>(t, q0, k0, id_qk);
 #pragma unroll
-      for (int k16 = 0; k16 < D / 16; ++k16)
-        tc_mma_f16(tmem + g * 128, da + (uint64_t)(((k16 >> 2) * C::QCHUNK + (k16 & 3) * 32) >> 4),
-                   dk + (uint64_t)(((k16 >> 2) * (TOK * 128) + (k16 & 3) * 32) >> 4), id_qk, k16 != 0);
+      for (int k16 = 1; k16 < D / 16; ++k16)
+        mma_ss<true>(t, q0 + (((k16 >> 2) * C::QCHUNK + (k16 & 3) * 32) >> 4), k0 + (((k16 >> 2) * (TOK * 128) + (k16 & 3) * 32) >> 4),
+                     id_qk);
       tc_commit(&s_full[g]);
     };
     auto pv = [&](int g, int s, bool first, unsigned& par) {
-      const uint64_t dv = dv0 + (uint64_t)(s * (C::TILE >> 4));
       ok = wait(&p_full[g], par);
-      if (!ok) return;
-      tc_fence_after();
-#pragma unroll
-      for (int kk = 0; kk < TOK / 32; ++kk)
-        tc_mma_f16_ts(tmem + 256 + g * D, tmem + g * 128 + kk * 8, dv + (uint64_t)(kk * 2048 >> 4), id_pv, kk > 0 || !first);
-      // the other half, while the first one's products run
-      ok = wait(&p_full[2 + g], par);
       if (!ok) return;
       par ^= 1;
       tc_fence_after();
+      const uint32_t v0 = (ar + s * (C::TILE >> 4)) | kV, t = tmem + 256 + g * D, p0 = tmem + g * 128;
+      mma_ts(t, p0, v0, id_pv, !first);
 #pragma unroll
-      for (int kk = TOK / 32; kk < TOK / 16; ++kk)
-        tc_mma_f16_ts(tmem + 256 + g * D, tmem + g * 128 + kk * 8, dv + (uint64_t)(kk * 2048 >> 4), id_pv, 1);
+      for (int kk = 1; kk < TOK / 16; ++kk) mma_ts(t, p0 + kk * 8, v0 + kk * (2048 >> 4), id_pv);
     };
     auto pv_due = [&](int g) {
       const int info = g ? pend1 : pend0, slot = 2 * (info >> 2) + 1, s = slot % S;
@@ -681,34 +674,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
                 if (!(vis & (1u << i2))) s[32 * w + i2] = -INFINITY;
             }
           }
-          float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-          for (int i2 = 4; i2 < 124; i2 += 8) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i2 + 2 * e], s[i2 + 2 * e + 1]);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[124 + e]);
-          const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-          const bool grow = tmax > m + kMaxGrowth || (m == -INFINITY && tmax != -INFINITY);
-          const float m_new = grow ? tmax : m;
-          // O holds earlier tiles' products (all finished: S of this tile was issued behind them)
-          if (__any_sync(0xffffffffu, grow && l > 0.f)) {
-            const float f = grow && l > 0.f ? ex2(m - m_new) : 1.f;
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 16) {
-              float ov[16];
-              uint32_t ow[16];
-              tmem_ld16(tO + c0, ov);
-#pragma unroll
-              for (int i2 = 0; i2 < 16; ++i2) ow[i2] = __float_as_uint(ov[i2] * f);
-              tmem_st16(tO + c0, ow);
-            }
-            l *= f;
-          }
-          m = m_new;
-          const float neg = m == -INFINITY ? 0.f : -m;
-          const uint64_t sl22 = pack2(sl2, sl2), neg2 = pack2(neg, neg);
           if (!FP8 && !tile_whole(it, base)) {
             // value rows that no row of the item sees (a row per thread)
             const int slot = 2 * (N + j) + 1;
@@ -722,11 +687,41 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
             }
             fence_proxy_async_smem();
           }
-          uint64_t ps0 = 0, ps1 = 0;
+          const uint64_t sl22 = pack2(sl2, sl2);
+          bool fix = m == -INFINITY;       // this row's m has to be set from the tile's maximum
+#pragma unroll 1
+          for (;;) {
+            if (__any_sync(0xffffffffu, fix)) {
+              float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
+              for (int i2 = 4; i2 < 124; i2 += 8) {
 #pragma unroll
-            for (int c0 = half * 64; c0 < half * 64 + 64; c0 += 32) {
+                for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i2 + 2 * e], s[i2 + 2 * e + 1]);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[124 + e]);
+              const float m_new = fix ? fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2) : m;
+              // O holds earlier tiles' products (all finished: S of this tile was issued behind them)
+              if (__any_sync(0xffffffffu, l > 0.f && m_new > m)) {
+                const float f = l > 0.f ? ex2(m - m_new) : 1.f;
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 16) {
+                  float ov[16];
+                  uint32_t ow[16];
+                  tmem_ld16(tO + c0, ov);
+#pragma unroll
+                  for (int i2 = 0; i2 < 16; ++i2) ow[i2] = __float_as_uint(ov[i2] * f);
+                  tmem_st16(tO + c0, ow);
+                }
+                l *= f;
+              }
+              m = m_new;
+            }
+            const float neg = m == -INFINITY ? 0.f : -m;
+            const uint64_t neg2 = pack2(neg, neg);
+            uint64_t ps0 = 0, ps1 = 0;
+#pragma unroll
+            for (int c0 = 0; c0 < 128; c0 += 32) {
               uint32_t pk[16];
 #pragma unroll
               for (int i2 = 0; i2 < 32; i2 += 2) {
@@ -740,17 +735,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
               }
               tmem_st16(tS + c0 / 2, pk);
             }
-            // each half as soon as it is there: its products overlap the other half's exponentials
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * half + g]);
-          }
-          {
             float a, b;
             unpack2(add2(ps0, ps1), a, b);
-            l += a + b;
+            // a row whose weights grew past the limit: set m anew and do the tile again (once: m is its maximum then)
+            fix = a + b > kMaxSum && !fix;
+            if (!__any_sync(0xffffffffu, fix)) {
+              l += a + b;
+              break;
+            }
           }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[g]);
           ++n_ops;
         }
         // -------------------------------------------------------------- the piece's end
