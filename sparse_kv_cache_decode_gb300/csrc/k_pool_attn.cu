@@ -538,37 +538,50 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
                 par ^= 1;
               }
             };
+            int sv = 0, sk = 0;
+            // V of tile t and K of tile t + 1, waited for ahead of the products before them
+            auto next_kv = [&](bool with_k) {
+              sv = s;
+              ok = wait(&kv_full[s], par);
+              next();
+              if (with_k) {
+                sk = s;
+                ok = ok && wait(&kv_full[s], par);
+                next();
+              }
+            };
             ok = wait(&kv_full[s], par);
             if (!ok) break;
             tc_fence_after();
             qk(0, s, 0);
-            qk(1, s, 128);
-            tc_commit(&kv_empty[s]);
+            const int s0 = s;
             next();
-            for (int t = 0; t < n; ++t) {
-              const bool last = t + 1 == n;
-              if (last) tc_commit(q_free);
-              const int sv = s;
-              ok = wait(&kv_full[s], par);
-              next();
-              const int sk = s;
-              if (!last) {
-                ok = ok && wait(&kv_full[s], par);
-                next();
-              }
-              if (ok) pv(0, sv, t == 0, par0);
+            next_kv(n > 1);
+            if (!ok) break;
+            qk(1, s0, 128);
+            tc_commit(&kv_empty[s0]);
+            for (int t = 0; t + 1 < n; ++t) {
+              pv(0, sv, t == 0, par0);
               if (!ok) break;
-              if (last) tc_commit(&o_full[0]);
-              else qk(0, sk, 0);
+              qk(0, sk, 0);
               pv(1, sv, t == 0, par1);
               if (!ok) break;
               tc_commit(&kv_empty[sv]);
-              if (last) tc_commit(&o_full[1]);
-              else {
-                qk(1, sk, 128);
-                tc_commit(&kv_empty[sk]);
-              }
+              const int s1 = sk;
+              next_kv(t + 2 < n);
+              if (!ok) break;
+              qk(1, s1, 128);
+              tc_commit(&kv_empty[s1]);
             }
+            if (!ok) break;
+            tc_commit(q_free);
+            pv(0, sv, n == 1, par0);
+            if (!ok) break;
+            tc_commit(&o_full[0]);
+            pv(1, sv, n == 1, par1);
+            if (!ok) break;
+            tc_commit(&kv_empty[sv]);
+            tc_commit(&o_full[1]);
           } else {
             for (int x = 0; x < n && ok; ++x) {
               const int g = x & 1, tile = N + x, s = (2 * tile) % S;
@@ -644,7 +657,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
         const bool live = r < nrows;
         const int row = it.row0 + r;
         // the keys this row sees, and those every row of this group sees
-        int hi = live ? it.len : 0, lo = 0, first = 0, hi_all = it.len, lo_all = 0, first_all = 0;
+        int hi = live ? it.len : 0, lo = 0, first = 0, hi_all = it.len, lo_all = 0;
         if (seqs.causal) {
           const int ra = it.row0 + (pair ? g * 128 : 0), rb = min(ra + 127, it.row0 + nrows - 1);
           const int p = it.p0 + row / d.G, pa = it.p0 + ra / d.G, pb = it.p0 + rb / d.G;
@@ -654,17 +667,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
             lo = max(0, p - seqs.window + 1);
             first = min(seqs.n_sink, lo);
             lo_all = max(0, pb - seqs.window + 1);
-            first_all = min(seqs.n_sink, max(0, pa - seqs.window + 1));
           }
         }
+        // tiles of the span that every row of the group sees as a whole: nothing to mask, no value row to zero
+        const int ja = it.ns + (lo_all + TOK - 1) / TOK - it.lo_tile - j0;
+        const unsigned n_whole = (unsigned)max(0, it.ns + hi_all / TOK - it.lo_tile - j0 - ja);
         float m = -INFINITY, l = 0.f;
         for (int j = pair ? 0 : g; j < n; j += pair ? 1 : 2) {
-          const int base = tile_base(it, j0 + j);
           wait(&s_full[g], n_ops & 1);
           tc_fence_after();
           float s[128];
           tmem_ld128(tS, s);
-          if (!((base + TOK <= hi_all && base >= lo_all) || base + TOK <= first_all)) {
+          if ((unsigned)(j - ja) >= n_whole) {
+            const int base = tile_base(it, j0 + j);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
               const int off = base + 32 * w;
@@ -673,19 +688,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
               for (int i2 = 0; i2 < 32; ++i2)
                 if (!(vis & (1u << i2))) s[32 * w + i2] = -INFINITY;
             }
-          }
-          if (!FP8 && !tile_whole(it, base)) {
-            // value rows that no row of the item sees (a row per thread)
-            const int slot = 2 * (N + j) + 1;
-            wait(&kv_full[slot % S], (slot / S) & 1);
-            if (!key_seen(it, base + lr)) {
-              unsigned char* vr = ring + (slot % S) * C::TILE + lr * 128;
+            if (!FP8 && !tile_whole(it, base)) {
+              // value rows that no row of the item sees (a row per thread)
+              const int slot = 2 * (N + j) + 1;
+              wait(&kv_full[slot % S], (slot / S) & 1);
+              if (!key_seen(it, base + lr)) {
+                unsigned char* vr = ring + (slot % S) * C::TILE + lr * 128;
 #pragma unroll
-              for (int b = 0; b < C::CHUNKS; ++b)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(vr + b * (TOK * 128) + e * 16) = make_uint4(0, 0, 0, 0);
+                for (int b = 0; b < C::CHUNKS; ++b)
+#pragma unroll 1
+                  for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(vr + b * (TOK * 128) + e * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
             }
-            fence_proxy_async_smem();
           }
           const uint64_t sl22 = pack2(sl2, sl2);
           bool fix = m == -INFINITY;       // this row's m has to be set from the tile's maximum
