@@ -1,7 +1,5 @@
 // Device helpers of the pool kernels that run on the tensor cores.
 #pragma once
-#include <cuda_fp16.h>
-
 #include "kvs_pool.cuh"
 #include "kvs_ptx.cuh"
 
@@ -137,22 +135,28 @@ __device__ __forceinline__ bool bounded_wait(uint64_t* bar, unsigned parity, uin
   return true;
 }
 
-// 16 E4M3 codes (vector v of a row) as bf16, exactly (through f16, which holds every E4M3 value), into the row of a
-// K-major 128-byte-swizzled tile: `p` the row in its first 64-dim chunk, chunks `chunk` bytes apart.
+// Four E4M3 codes as bf16 pairs (codes 0, 1 and 2, 3), exactly: a code's exponent and mantissa bits at bf16's places
+// stand for its value times 2^-120, subnormals included, and the product with 2^120 is exact.  All of it runs at the
+// full integer and fma rates, which the conversion instructions do not.  (The NaN codes come out as +-480: pools
+// hold finite values.)
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);   // a code in each half's upper byte
+  const uint32_t x = ((a >> 4) & 0x07f007f0u) | (a & 0x80008000u), y = ((b >> 4) & 0x07f007f0u) | (b & 0x80008000u);
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(0x7b807b80u));           // 0x7b80: 2^120
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(0x7b807b80u));
+}
+// 16 E4M3 codes (vector v of a row) as bf16 into the row of a K-major 128-byte-swizzled tile: `p` the row in its first
+// 64-dim chunk, chunks `chunk` bytes apart.
 __device__ __forceinline__ void widen16(const uint4& w, unsigned char* p, int chunk, int row, int v) {
-  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-  uint32_t out[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    uint32_t h2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(in[e >> 1] >> ((e & 1) * 16))));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-    out[e] = pack_bf16x2(f.x, f.y);
-  }
+  uint4 x, y;
+  widen4(w.x, x.x, x.y);
+  widen4(w.y, x.z, x.w);
+  widen4(w.z, y.x, y.y);
+  widen4(w.w, y.z, y.w);
   p += (v >> 2) * chunk;
   const int c16 = (v & 3) * 2;
-  *reinterpret_cast<uint4*>(p + ((c16 ^ (row & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
-  *reinterpret_cast<uint4*>(p + (((c16 + 1) ^ (row & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
+  *reinterpret_cast<uint4*>(p + ((c16 ^ (row & 7)) << 4)) = x;
+  *reinterpret_cast<uint4*>(p + (((c16 + 1) ^ (row & 7)) << 4)) = y;
 }
 
 }  // namespace pdev
