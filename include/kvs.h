@@ -367,7 +367,7 @@ kvs_status kvs_quantize_e4m3(const void* d_src_bf16, void* d_dst, size_t n, floa
  * never used and may hold anything; keys that some row sees must be finite.
  *
  * Supported: head dim 64 or 128; block_size 16, 32, 64 or 128; 1 to 128 query heads per kv head;
- * max_req <= 2048 with max_req * n_kv_head <= 65535.
+ * max_req <= 2048 with max_req * n_kv_head <= 65535; max_tokens * (H_q / H_kv) <= 2^25.
  * Calls are asynchronous on `stream` and capturable; the workspace is scratch of one call at a time,
  * so calls on one kvs_pool must not overlap on the GPU, captured graphs that hold them included
  * (a second kvs_pool over the same K/V memory, with a workspace of its own, may run beside it).

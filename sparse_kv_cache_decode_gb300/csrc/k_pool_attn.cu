@@ -27,7 +27,7 @@
 // anything, and 0 * NaN would reach every row.  All waits are bounded (KVS_ERR_TIMEOUT).
 #include <algorithm>
 
-#include "kvs_pool_dev.cuh"
+#include "kvs_pool_sched.cuh"
 #include "kvs_tmem128.cuh"
 
 namespace kvs {
@@ -36,34 +36,6 @@ namespace {
 namespace pa {
 
 using namespace pdev;
-
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kMaxSum = 0x1p40f;              // largest sum of a tile's weights before m is set anew
-
-struct Split {
-  int n_cta;
-  int min_per;      // tiles per CTA at least
-};
-
-// One item's partial state: which rows, and the last CTA that holds a piece of it (begun: in this CTA).
-struct Meta {
-  int t0, row0, nrows, head0, c1, seq, pad0, pad1;
-};
-
-// Scratch: meta [n_cta]; (m, l) [n_cta][2][256]; O [n_cta][2][256][d].
-struct Scratch {
-  Meta* meta;
-  float2* ml;
-  float* o;
-};
-
-__host__ __device__ inline Scratch scratch_of(void* p, int n_cta) {
-  Scratch s;
-  s.meta = static_cast<Meta*>(p);
-  s.ml = reinterpret_cast<float2*>(s.meta + n_cta);
-  s.o = reinterpret_cast<float*>(s.ml + (size_t)n_cta * 512);
-  return s;
-}
 
 template <int D, bool FP8, int QT>
 struct Cfg {
@@ -95,117 +67,6 @@ struct Cfg {
   static_assert(STAGES >= 3, "shared memory plan");
   static_assert(OFF_TAB + 4 * (kPoolMaxReq + 1) + 1024 <= MAX_SMEM, "shared memory plan");
 };
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float y;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
-// A CTA's piece of an item: rows [row0, row0 + nrows) of head h of sequence s against n of the item's nt tiles,
-// from tile j0 on.  The item's rows see the keys [0, first) and [lo, hi).
-struct __align__(16) Piece {
-  int s, h, t0, row0, nrows;
-  int p0;                 // position of the sequence's first query token
-  int len;
-  int first, lo, hi;
-  int ns, lo_tile, nt;    // tiles of the first tokens, first tile of the span, tiles in all
-  int j0, n;
-  int pad;
-};
-static_assert(sizeof(Piece) == 64, "smem plan");
-
-__device__ __forceinline__ void item_span(const PoolSeqs& q, int G, Piece& it) {
-  if (!q.causal) {
-    it.first = 0;
-    it.lo = 0;
-    it.hi = it.len;
-  } else {
-    const int pa = it.p0 + it.row0 / G, pb = it.p0 + (it.row0 + it.nrows - 1) / G;
-    it.hi = max(0, pb + 1);
-    it.lo = q.window ? max(0, pa - q.window + 1) : 0;
-    it.first = min(q.n_sink, it.lo);
-  }
-  it.lo_tile = it.lo / TOK;
-  it.ns = min((it.first + TOK - 1) / TOK, it.lo_tile);
-  it.nt = max(1, it.ns + (it.hi + TOK - 1) / TOK - it.lo_tile);
-}
-
-// Row block rb of a sequence: its rows and span.
-template <int RB>
-__device__ __forceinline__ void item_rows(const PoolSeqs& q, int G, const SeqInfo& r, int rb, Piece& it) {
-  it.t0 = r.t0;
-  it.len = r.len;
-  it.p0 = r.len - (r.t1 - r.t0);
-  it.row0 = rb * RB;
-  it.nrows = max(0, min(RB, (r.t1 - r.t0) * G - it.row0));
-  item_span(q, G, it);
-}
-
-// Item number `pos` of the dealt-out order: position p = c * K + k is item k * n + c (the first n_items % n
-// columns are one longer).
-__device__ __forceinline__ int dealt(int p, int n_items, int n) {
-  const int K = n_items / n, r = n_items - K * n;
-  const int wide = r * (K + 1);
-  if (p < wide) return (p % (K + 1)) * n + p / (K + 1);
-  p -= wide;
-  return (p % K) * n + r + p / K;
-}
-
-// Item i: the sequences' items follow one another, row block by row block, head by head.
-template <int RB>
-__device__ __forceinline__ Piece item_at(const PoolDims& d, const PoolSeqs& q, const int* tab, int i, unsigned* err) {
-  // the last sequence with tab[s] <= i (empty sequences hold no items, so it is the one that does)
-  int lo = 0, hi = q.n_seq;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (tab[mid] <= i) lo = mid; else hi = mid;
-  }
-  Piece it;
-  it.s = lo;
-  const SeqInfo r = pool_seq(d, q, lo, err);
-  const int local = i - tab[lo], rb = local / d.Hkv;
-  it.h = local - rb * d.Hkv;
-  item_rows<RB>(q, d.G, r, rb, it);
-  return it;
-}
-
-__device__ __forceinline__ int tile_base(const Piece& it, int j) { return (j < it.ns ? j : it.lo_tile + j - it.ns) * TOK; }
-__device__ __forceinline__ bool key_seen(const Piece& it, int t) { return t < it.first || (t >= it.lo && t < it.hi); }
-// every key of the tile at `base` is seen by some row
-__device__ __forceinline__ bool tile_whole(const Piece& it, int base) {
-  return (base >= it.lo && base + TOK <= it.hi) || base + TOK <= it.first;
-}
-
-// out / lse of one row from its joined state: D columns by the caller.
-struct RowOut {
-  float w_prev, w_new;    // weights of the earlier call's row and of this row's O
-  float lse2;
-};
-__device__ __forceinline__ RowOut row_out(const PoolAttnOut& o, bool has_prev, size_t row, float m, float l, float v_scale) {
-  RowOut r;
-  r.w_prev = 0.f;
-  r.w_new = l > 0.f ? v_scale / l : 0.f;
-  r.lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
-  if (has_prev) {
-    const float a = o.prev_lse2[row], M = fmaxf(a, r.lse2);
-    if (M != -INFINITY) {
-      const float ea = ex2(a - M), eb = ex2(r.lse2 - M), inv = 1.f / (ea + eb);
-      r.w_prev = ea * inv;
-      r.w_new *= eb * inv;
-      r.lse2 = M + log2f(ea + eb);
-    }
-  }
-  return r;
-}
-__device__ __forceinline__ void row_lse(const PoolAttnOut& o, size_t row, float lse2) {
-  if (o.lse) o.lse[row] = lse2 * kLn2;
-  if (o.lse2) o.lse2[row] = lse2;
-}
-// 4 columns of a finished row at element e of the output arrays
-__device__ __forceinline__ void row_store4(const PoolAttnOut& o, size_t e, float4 y) {
-  if (o.part_out) *reinterpret_cast<float4*>(o.part_out + e) = y;
-  else *reinterpret_cast<uint2*>(o.out + e) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-}
 
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
@@ -239,7 +100,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   // position and first tile of the CTA's next piece, its tiles still to plan, pieces planned, items, tiles per CTA
   volatile int* plan = reinterpret_cast<volatile int*>(tmem_slot + 2);
-  const Piece* pieces = reinterpret_cast<const Piece*>(smem + C::OFF_PIECES);
+  Piece* pieces = reinterpret_cast<Piece*>(smem + C::OFF_PIECES);
   int* tab = reinterpret_cast<int*>(smem + C::OFF_TAB);               // [n_seq + 1] items before each sequence
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x;
@@ -272,148 +133,22 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   kvs_pdl_entry();
 
-  // ------------------------------------------------------------------ the CTA's range of tiles
-  const Scratch sc = scratch_of(scratch, sp.n_cta);
-  {
-    long long* ws = reinterpret_cast<long long*>(ml);
-    const int per_s = (seqs.n_seq + C::THREADS - 1) / C::THREADS;
-    const int s0 = min(seqs.n_seq, tid * per_s), s1 = min(seqs.n_seq, s0 + per_s);
-    // items and, in the order of sequences, tiles of this thread's sequences
-    auto seq_work = [&](int s, int* items) {
-      const SeqInfo r = pool_seq(d, seqs, s, err);
-      const int n_rb = (int)(((long long)(r.t1 - r.t0) * d.G + RB - 1) / RB);
-      *items = n_rb * d.Hkv;
-      long long v = 0;
-      if (QT == 1)
-        for (int rb = 0; rb < n_rb; ++rb) {
-          Piece it;
-          item_rows<RB>(seqs, d.G, r, rb, it);
-          v += (long long)it.nt * d.Hkv;
-        }
-      return v;
-    };
-    int mine = 0, n1 = 0;
-    long long tiles = 0, v1 = 0;
-    for (int s = s0; s < s1; ++s) {
-      v1 = seq_work(s, &n1);
-      mine += n1;
-      tiles += v1;
-    }
-    Scan r = block_scan(mine, tiles, ws, NW);
-    const int n_items = r.n_all;
-    {
-      int at = r.n;
-      for (int s = s0; s < s1; ++s) {
-        tab[s] = at;
-        if (s + 1 < s1) {      // the last one's count is not needed
-          seq_work(s, &n1);
-          at += n1;
-        }
-      }
-      if (tid == 0) tab[seqs.n_seq] = n_items;
-    }
-    // with two row tiles the items are dealt out: the tiles in that order
-    int i0 = 0, i1 = 0;
-    if (QT == 2) {
-      __syncthreads();
-      const int per_i = (n_items + C::THREADS - 1) / C::THREADS;
-      i0 = min(n_items, tid * per_i);
-      i1 = min(n_items, i0 + per_i);
-      tiles = 0;
-      for (int p = i0; p < i1; ++p) tiles += item_at<RB>(d, seqs, tab, dealt(p, n_items, sp.n_cta), err).nt;
-      r = block_scan(0, tiles, ws, NW);
-    }
-    const long long per = max((long long)sp.min_per, (r.v_all + sp.n_cta - 1) / sp.n_cta);
-    const long long f0 = per * c, f1 = min(r.v_all, f0 + per);
-    if (f0 < f1 && f0 >= r.v && f0 < r.v + tiles) {
-      long long f = r.v;
-      int p = -1, j = 0;
-      if (QT == 2) {
-        for (p = i0; p < i1; ++p) {
-          const int nt = item_at<RB>(d, seqs, tab, dealt(p, n_items, sp.n_cta), err).nt;
-          if (f0 < f + nt) break;
-          f += nt;
-        }
-        j = (int)(f0 - f);
-      } else {
-        for (int s = s0; s < s1 && p < 0; ++s) {
-          const long long v = s1 - s0 == 1 ? v1 : seq_work(s, &n1);
-          if (f0 >= f + v) {
-            f += v;
-            continue;
-          }
-          const SeqInfo q1 = pool_seq(d, seqs, s, err);
-          for (int rb = 0; p < 0; ++rb) {
-            Piece it;
-            item_rows<RB>(seqs, d.G, q1, rb, it);
-            const long long w = (long long)it.nt * d.Hkv;
-            if (f0 < f + w) {
-              const int h = (int)((f0 - f) / it.nt);
-              p = tab[s] + rb * d.Hkv + h;
-              j = (int)(f0 - f - (long long)h * it.nt);
-            }
-            f += w;
-          }
-        }
-      }
-      plan[0] = p;
-      plan[1] = j;
-      plan[2] = (int)(f1 - f0);
-    }
-    if (tid == 0) {
-      plan[4] = n_items;
-      plan[5] = (int)per;
-    }
-  }
+  cta_range<RB, QT == 2, C::THREADS>(d, seqs, tab, reinterpret_cast<long long*>(ml), plan, sp, c, err);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
   const uint64_t timeout_ns = (uint64_t)d.timeout_us * 1000ull;
-  const int total = plan[2];            // the CTA's tiles
+  const Scratch sc = scratch_of(scratch, sp.n_cta);
   auto wait = [&](uint64_t* bar, unsigned parity) { return bounded_wait(bar, parity, timeout_ns, abort_flag); };
-  // Plans the CTA's next kPieces pieces (warp 0, a lane per piece).
-  auto plan_pieces = [&]() {
-    int pos = plan[0], j0 = plan[1], left = plan[2], cnt = 0;
-    const int n_items = plan[4];
-    for (int x = 0; x < kPieces && left > 0; x += 32) {
-      Piece it;
-      it.nt = 0;
-      if (pos + lane < n_items)
-        it = item_at<RB>(d, seqs, tab, QT == 2 ? dealt(pos + lane, n_items, sp.n_cta) : pos + lane, err);
-      it.j0 = lane == 0 ? j0 : 0;
-      const long long w = it.nt - it.j0;
-      long long incl = w;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      it.n = (int)max(0ll, min(w, left - (incl - w)));
-      if (it.n > 0) const_cast<Piece*>(pieces)[x + lane] = it;
-      const int got = __popc(__ballot_sync(0xffffffffu, it.n > 0));
-      const long long all = __shfl_sync(0xffffffffu, incl, 31);
-      left = (int)max(0ll, left - all);
-      pos += got;
-      cnt += got;
-      j0 = 0;
-    }
-    __syncwarp();
-    if (lane == 0) {
-      plan[0] = pos;
-      plan[1] = 0;
-      plan[2] = pos < n_items ? left : 0;
-      plan[3] = cnt;
-    }
-  };
-  if (warp == 0) plan_pieces();
+  if (warp == 0) plan_pieces<RB, QT == 2>(d, seqs, tab, plan, pieces, sp.n_cta, err);
   __syncthreads();
   // Between two lists of pieces (long calls only): every role is done with the old one.
   auto more = [&]() {
     const int l = plan[2];
     __syncthreads();
     if (l <= 0) return false;
-    if (warp == 0) plan_pieces();
+    if (warp == 0) plan_pieces<RB, QT == 2>(d, seqs, tab, plan, pieces, sp.n_cta, err);
     __syncthreads();
     return true;
   };
@@ -625,7 +360,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
         constexpr int VEC = D / 8;       // 16-byte vectors of a row
         for (int x = tid - 64; x < it.nrows * VEC; x += 64) {
           const int r = x / VEC, v = x - r * VEC, row = it.row0 + r;
-          const int tok = row / d.G, g = row - tok * d.G, at = r + qb * C::QHALF;
+          const int tok = div_g(d, row), g = row - tok * d.G, at = r + qb * C::QHALF;
           const __nv_bfloat16* src = q + (it.t0 + tok) * q_stride + (it.h * d.G + g) * D + v * 8;
           unsigned char* dst = smem + (v >> 3) * C::QCHUNK + at * 128 + (((v & 7) ^ (at & 7)) << 4);
           cp_async16(dst, src, 16);
@@ -660,7 +395,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
         int hi = live ? it.len : 0, lo = 0, first = 0, hi_all = it.len, lo_all = 0;
         if (seqs.causal) {
           const int ra = it.row0 + (pair ? g * 128 : 0), rb = min(ra + 127, it.row0 + nrows - 1);
-          const int p = it.p0 + row / d.G, pa = it.p0 + ra / d.G, pb = it.p0 + rb / d.G;
+          const int p = it.p0 + div_g(d, row), pa = it.p0 + div_g(d, ra), pb = it.p0 + div_g(d, rb);
           hi = live ? max(0, p + 1) : 0;
           hi_all = max(0, pa + 1);
           if (seqs.window) {
@@ -767,7 +502,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
         }
         // -------------------------------------------------------------- the piece's end
         const bool begun = j0 == 0, done = j0 + n == it.nt, whole = begun && done;
-        const int tok = it.t0 + row / d.G, head = it.h * d.G + row % d.G;
+        const int tok = it.t0 + div_g(d, row), head = it.h * d.G + row - div_g(d, row) * d.G;
         const size_t orow = (size_t)tok * d.Hq + head;
         const size_t prow = ((size_t)c * 2 + (begun ? 1 : 0)) * 256 + r;      // partial state's place
         const bool has_prev = o.prev_out && it.s >= o.prev_req[0] && it.s < o.prev_req[o.n_prev];
@@ -814,16 +549,24 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
             }
             if (!live) continue;
             if (whole) {
+              if (has_prev && ro.w_prev > 0.f) {       // the earlier call's row, all of it on its way at once
+                float4 z[8];
 #pragma unroll
-              for (int i2 = 0; i2 < 32; i2 += 4) {
-                float4 y = has ? make_float4(x[i2] * ro.w_new, x[i2 + 1] * ro.w_new, x[i2 + 2] * ro.w_new, x[i2 + 3] * ro.w_new)
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
-                if (has_prev && ro.w_prev > 0.f) {
-                  const float4 z = *reinterpret_cast<const float4*>(o.prev_out + orow * D + c0 + i2);
-                  y = make_float4(y.x + ro.w_prev * z.x, y.y + ro.w_prev * z.y, y.z + ro.w_prev * z.z, y.w + ro.w_prev * z.w);
+                for (int i2 = 0; i2 < 8; ++i2) z[i2] = __ldg(reinterpret_cast<const float4*>(o.prev_out + orow * D + c0) + i2);
+#pragma unroll
+                for (int i2 = 0; i2 < 8; ++i2) {
+                  x[4 * i2] = (has ? x[4 * i2] * ro.w_new : 0.f) + ro.w_prev * z[i2].x;
+                  x[4 * i2 + 1] = (has ? x[4 * i2 + 1] * ro.w_new : 0.f) + ro.w_prev * z[i2].y;
+                  x[4 * i2 + 2] = (has ? x[4 * i2 + 2] * ro.w_new : 0.f) + ro.w_prev * z[i2].z;
+                  x[4 * i2 + 3] = (has ? x[4 * i2 + 3] * ro.w_new : 0.f) + ro.w_prev * z[i2].w;
                 }
-                row_store4(o, orow * D + c0 + i2, y);
+              } else {
+#pragma unroll
+                for (int i2 = 0; i2 < 32; ++i2) x[i2] = has ? x[i2] * ro.w_new : 0.f;
               }
+#pragma unroll
+              for (int i2 = 0; i2 < 32; i2 += 4)
+                row_store4(o, orow * D + c0 + i2, make_float4(x[i2], x[i2 + 1], x[i2 + 2], x[i2 + 3]));
             } else {
 #pragma unroll
               for (int i2 = 0; i2 < 32; i2 += 4)
@@ -947,7 +690,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 #pragma unroll
   for (int w = 16; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
   const int row = mt.row0 + r;
-  const size_t orow = (size_t)(mt.t0 + row / d.G) * d.Hq + mt.head0 + row % d.G;
+  const size_t orow = (size_t)(mt.t0 + div_g(d, row)) * d.Hq + mt.head0 + row % d.G;
   const bool has_prev = o.prev_out && mt.seq >= o.prev_req[0] && mt.seq < o.prev_req[o.n_prev];
   const RowOut ro = row_out(o, has_prev, orow, M, l, d.v_scale);
 #pragma unroll
@@ -979,18 +722,23 @@ cudaError_t launch(const PoolDims& d, const CUtensorMap* tm, const __nv_bfloat16
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // an item has at most 128 * QT rows, and no more than the call has
-  const int rows = (int)std::min<long long>(C::RB, (long long)seqs.n_tok * d.G);
-  launch_pdl(pool_merge_kernel<D>, dim3(sp.n_cta, (rows + kMergeWarps - 1) / kMergeWarps), dim3(kMergeWarps * 32), 0, s, d, o,
-             scratch, sp.n_cta);
-  return cudaGetLastError();
+  return launch_pool_merge(d, o, scratch, sp.n_cta, (int)std::min<long long>(C::RB, (long long)seqs.n_tok * d.G), s);
 }
 
 }  // namespace pa
 }  // namespace
 
+cudaError_t launch_pool_merge(const PoolDims& d, const PoolAttnOut& o, void* scratch, int n_cta, int rows, cudaStream_t s) {
+  using namespace pa;
+  const dim3 grid(n_cta, (rows + kMergeWarps - 1) / kMergeWarps);
+  if (d.d == 128) launch_pdl(pool_merge_kernel<128>, grid, dim3(kMergeWarps * 32), 0, s, d, o, scratch, n_cta);
+  else launch_pdl(pool_merge_kernel<64>, grid, dim3(kMergeWarps * 32), 0, s, d, o, scratch, n_cta);
+  return cudaGetLastError();
+}
+
 size_t pool_attn_scratch_bytes(const PoolDims& d) {
   const size_t n = device_sm_count();
-  return n * (sizeof(pa::Meta) + 512 * (sizeof(float2) + (size_t)d.d * 4));
+  return n * (sizeof(pdev::Meta) + 512 * (sizeof(float2) + (size_t)d.d * 4));
 }
 
 cudaError_t launch_pool_attn(const PoolDims& d, const unsigned char*, const unsigned char*, const CUtensorMap* tm,
@@ -998,7 +746,10 @@ cudaError_t launch_pool_attn(const PoolDims& d, const unsigned char*, const unsi
                              void* scratch, unsigned* err, cudaStream_t s, int* n_launched) {
   using namespace pa;
   *n_launched = 2;
-  // rows per (sequence, head) on average: more than 128 rows pay for two row tiles per K/V tile
+  // rows per (sequence, head) on average: few take the products' column side, more than 128 pay for two row tiles per
+  // K/V tile
+  const long long rows = ((long long)seqs.n_tok * d.G + seqs.n_seq - 1) / seqs.n_seq;
+  if (rows <= (d.fp8 ? 32 : 64)) return launch_pool_decode(d, tm, q, q_stride, seqs, o, (int)rows, scratch, err, s);
   const bool two = (long long)seqs.n_tok * d.G > 128ll * seqs.n_seq;
   if (d.d == 128) {
     if (d.fp8) return two ? launch<128, true, 2>(d, tm, q, q_stride, seqs, o, scratch, err, s)

@@ -1,0 +1,594 @@
+// Device-resident pools: attention for few rows per (sequence, kv head) on the 5th-generation tensor cores.
+//
+// A decode step has G rows (a group's heads) per K/V row, drafts a few times that: far fewer than a product's 128-row
+// side.  Here the tokens take that side, and the rows the columns (NB = 8, 16, 32 or 64 of them):
+//   S^T = K Q^T (128 tokens x NB),   P^T = 2^(S^T scale log2 e - m) in bf16,   O^T += V^T P^T (d x NB)
+// so that a tile of 128 tokens costs two products of 16 x (d / 16 + 8) small columns, and the 128 threads of the softmax
+// share its exponentials, a token each: the kernel is bound by the K/V bytes.  V is read as the product's A operand with
+// the dims contiguous (MN-major) from the same tile that the tensor loads bring; P^T goes through shared memory.
+// S^T and O^T are in tensor memory.  m (per row) is the maximum of the first tile that the row sees and is set anew
+// only when a weight passes 2^40; the sums l are kept per thread and reduced at a piece's end.
+//
+// The tiles of all items form one sequence that is cut into equal ranges, one per CTA (one per SM), as in the kernel
+// for many rows; the same merge kernel joins the items that a cut splits.
+//
+// Roles: warp 0 brings K/V tiles, warp 1 issues the products (S^T of a tile before O^T of the tile before it, across
+// pieces), warp 2 loads Q, warps 4-7 are the softmax; with E4M3 pools warps 8-15 widen the codes to bf16 tiles.
+// Value rows that no row of the item sees are zeroed before their product.  All waits are bounded.
+#include <algorithm>
+
+#include "kvs_pool_sched.cuh"
+
+namespace kvs {
+
+namespace {
+namespace pd {
+
+using namespace pdev;
+
+constexpr float kMaxArg = 40.f;     // log2 of the largest weight before m is set anew
+
+template <int D, bool FP8, int NB>
+struct Cfg {
+  static constexpr int CHUNKS = D / 64;
+  static constexpr int NQ = NB < 16 ? 16 : NB;                // columns of the products
+  static constexpr int QCHUNK = NQ * 128;                     // 64 dims of the rows
+  static constexpr int QBUF = CHUNKS * QCHUNK;                // one item's Q (two are held)
+  static constexpr int PBUF = TOK * 128;                      // P^T: 128 tokens, 64 columns of room (two are held)
+  static constexpr int TILE = TOK * D * 2;
+  static constexpr int CODES = TOK * D;
+  static constexpr int THREADS = FP8 ? 512 : 256;
+  static constexpr int FIXED = 4096 + 512 + 1024 + 4 * (kPoolMaxReq + 1) + kPieces * 64 + 2 * QBUF + 2 * PBUF;
+  static constexpr int ROOM = MAX_SMEM - FIXED;
+  static constexpr int STAGES = FP8 ? (D == 128 ? 3 : 4) : (ROOM / TILE > 8 ? 8 : ROOM / TILE);     // bf16 tiles
+  static constexpr int STG_ROOM = FP8 ? (ROOM - STAGES * TILE) / CODES : 0;
+  static constexpr int STAGING = STG_ROOM > 8 ? 8 : STG_ROOM;                                       // code tiles
+  static constexpr int OFF_P = 2 * QBUF;
+  static constexpr int OFF_RING = OFF_P + 2 * PBUF;
+  static constexpr int OFF_STG = OFF_RING + STAGES * TILE;
+  static constexpr int OFF_ML = OFF_STG + STAGING * CODES;    // m, l and maxima: 16 x 64 floats
+  static constexpr int OFF_BAR = OFF_ML + 4096;
+  static constexpr int OFF_PIECES = OFF_BAR + 512;
+  static constexpr int OFF_TAB = OFF_PIECES + kPieces * 64;
+  static_assert(STAGES >= 3 && (!FP8 || STAGING >= 2), "shared memory plan");
+  static_assert(OFF_TAB + 4 * (kPoolMaxReq + 1) + 1024 <= MAX_SMEM, "shared memory plan");
+};
+
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Whether any of the 128 softmax threads says so (named barrier 1).
+__device__ __forceinline__ bool group_any(bool x) {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+               : "=r"(r)
+               : "r"((uint32_t)x)
+               : "memory");
+  return r != 0;
+}
+
+template <int D, bool FP8, int NB>
+__global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
+    pool_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, PoolDims d,
+                       const __nv_bfloat16* __restrict__ q, long long q_stride, PoolSeqs seqs, PoolAttnOut o, void* scratch,
+                       Split sp, unsigned* err) {
+  using C = Cfg<D, FP8, NB>;
+  constexpr int S = C::STAGES, NQ = C::NQ;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* ring = smem + C::OFF_RING;
+  unsigned char* stg = smem + C::OFF_STG;
+  float* m_s = reinterpret_cast<float*>(smem + C::OFF_ML);            // [64] m of the rows, -inf: none yet
+  float* l_s = m_s + 64;                                              // [64] sums at a piece's end
+  float* f_s = m_s + 128;                                             // [64] factors of a new m
+  float* x_s = m_s + 256;                                             // [4][64] maxima or sums by warp
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* kv_full = bars;             // [8]
+  uint64_t* kv_empty = bars + 8;        // [8]
+  uint64_t* raw_full = bars + 16;       // [8] code tiles
+  uint64_t* raw_empty = bars + 24;      // [8]
+  uint64_t* s_full = bars + 32;         // [2]
+  uint64_t* s_free = bars + 34;         // [2]
+  uint64_t* p_full = bars + 36;         // [2]
+  uint64_t* p_free = bars + 38;         // [2]
+  uint64_t* q_full = bars + 40;         // [2] by piece
+  uint64_t* q_free = bars + 42;         // [2]
+  uint64_t* o_full = bars + 44;         // [2]
+  uint64_t* o_free = bars + 46;         // [2]
+  uint64_t* drained = bars + 48;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 49);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* plan = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  Piece* pieces = reinterpret_cast<Piece*>(smem + C::OFF_PIECES);
+  int* tab = reinterpret_cast<int*>(smem + C::OFF_TAB);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int c = blockIdx.x;
+
+  if (tid == 0) {
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&kv_full[i], FP8 ? 8 : 1);
+      mbar_init(&kv_empty[i], 1);
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], 4);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&p_free[i], 1);
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_free[i], 1);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_free[i], 4);
+    }
+    mbar_init(drained, 1);
+    *abort_flag = 0;
+    plan[0] = plan[1] = plan[2] = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 256);
+  kvs_pdl_entry();
+  cta_range<NB, false, C::THREADS>(d, seqs, tab, reinterpret_cast<long long*>(x_s), plan, sp, c, err);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
+  const uint64_t timeout_ns = (uint64_t)d.timeout_us * 1000ull;
+  const Scratch sc = scratch_of(scratch, sp.n_cta);
+  auto wait = [&](uint64_t* bar, unsigned parity) { return bounded_wait(bar, parity, timeout_ns, abort_flag); };
+  if (warp == 0) plan_pieces<NB, false>(d, seqs, tab, plan, pieces, sp.n_cta, err);
+  __syncthreads();
+  // Between two lists of pieces (long calls only): every role is done with the old one.
+  auto more = [&]() {
+    const int l = plan[2];
+    __syncthreads();
+    if (l <= 0) return false;
+    if (warp == 0) plan_pieces<NB, false>(d, seqs, tab, plan, pieces, sp.n_cta, err);
+    __syncthreads();
+    return true;
+  };
+  // tensor memory: S^T [2 buffers], O^T [2, by piece]
+  auto tS = [&](int b) { return tmem + b * 64; };
+  auto tO = [&](int b) { return tmem + 128 + b * 64; };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ K/V tiles: a lane per block of a tile
+    constexpr int BOXES = FP8 ? 1 : C::CHUNKS;
+    constexpr int SLOTS = FP8 ? C::STAGING : S;
+    uint64_t* full = FP8 ? raw_full : kv_full;
+    uint64_t* empty = FP8 ? raw_empty : kv_empty;
+    const int pages = TOK >> d.log2bs;
+    const int box_bytes = d.bs * (FP8 ? D : 128);
+    int k = 0, s = 0;
+    unsigned par = 1;                 // of the slot's last release (the first round is free)
+    bool ok = true;
+    do {
+      const int cnt = plan[3];
+      for (int i = 0; i < cnt && ok; ++i) {
+        const Piece it = pieces[i];
+        const int* table = seqs.table + (size_t)it.s * d.nb_max;
+        // the slot of this lane's block of tile j, fetched a tile ahead; -1: no row sees the block
+        auto look = [&](int j) {
+          if (lane >= pages || j >= it.j0 + it.n) return -1;
+          const int b0 = tile_base(it, j) + (lane << d.log2bs), b1 = b0 + d.bs;
+          return b0 < it.first || (b0 < it.hi && b1 > it.lo) ? table[b0 >> d.log2bs] : -2;
+        };
+        int slot = look(it.j0);
+        for (int j = it.j0; j < it.j0 + it.n && ok; ++j) {
+          const int now = slot;
+          slot = look(j + 1);
+          int row = -1;
+          if (lane < pages && now != -2) {
+            if (now < 0 || now >= d.n_slots) set_error(err, KVS_ERR_BAD_INDEX);
+            else row = (now * d.Hkv + it.h) * d.bs;
+          }
+          const int n_load = __popc(__ballot_sync(0xffffffffu, row >= 0));
+          for (int x = 0; x < 2; ++x, ++k) {
+            ok = k < SLOTS || __all_sync(0xffffffffu, wait(&empty[s], par));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], (unsigned)(n_load * BOXES * box_bytes));
+            __syncwarp();
+            if (row >= 0) {
+              unsigned char* dst = FP8 ? stg + s * C::CODES + lane * box_bytes : ring + s * C::TILE + lane * box_bytes;
+#pragma unroll
+              for (int b = 0; b < BOXES; ++b) tma_load_2d(dst + b * (TOK * 128), x ? &tmV : &tmK, b * 64, row, &full[s]);
+            }
+            if (++s == SLOTS) {
+              s = 0;
+              par ^= 1;
+            }
+          }
+        }
+      }
+    } while (more());
+    __syncwarp();
+    // no tensor load may still be writing this CTA's shared memory when it exits
+    for (int i = max(0, k - SLOTS); i < k; ++i) mbar_wait(&full[i % SLOTS], (i / SLOTS) & 1, kDrainTimeoutNs);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ products
+    const uint32_t id_s = idesc_bf16_f32(128, NQ);
+    const uint32_t id_o = idesc_bf16_f32(128, NQ) | (1u << 15) | (1u << 16);      // V and P^T are read MN-major
+    const uint32_t aq = smem_u32(smem) >> 4, ap = smem_u32(smem + C::OFF_P) >> 4, ar = smem_u32(ring) >> 4;
+    // V^T: 64-dim blocks of a tile 16 KiB apart; at d = 64 the second block gives lanes 64-127, which are not used: it is
+    // read 1 KiB on, still inside this CTA's shared memory
+    constexpr uint32_t kV = (uint32_t)((D == 128 ? TOK * 128 : 1024) >> 4) << 16;
+    int T = 0, pc = 0;                // tile and piece of the next S^T
+    int To = 0, po = 0;               // and of the next O^T
+    bool ok = true;
+    do {
+      const int cnt = plan[3];
+      if (elect_one()) {
+        int is = 0, js = 0, io = 0, jo = 0;      // the same within this list of pieces
+        int n_s = cnt > 0 ? pieces[0].n : 0, n_o = n_s;
+        auto s_t = [&]() {
+          const int s = (2 * T) % S, b = T & 1;
+          if (js == 0) ok = wait(&q_full[pc & 1], (pc >> 1) & 1);
+          ok = ok && wait(&kv_full[s], ((2 * T) / S) & 1) && (T < 2 || wait(&s_free[b], ((T >> 1) - 1) & 1));
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t k0 = ar + s * (C::TILE >> 4), q0 = aq + (pc & 1) * (C::QBUF >> 4), t = tS(b);
+          mma_ss<false>(t, k0, q0, id_s);
+#pragma unroll
+          for (int k16 = 1; k16 < D / 16; ++k16)
+            mma_ss<true>(t, k0 + (((k16 >> 2) * (TOK * 128) + (k16 & 3) * 32) >> 4),
+                         q0 + (((k16 >> 2) * C::QCHUNK + (k16 & 3) * 32) >> 4), id_s);
+          tc_commit(&s_full[b]);
+          tc_commit(&kv_empty[s]);
+          ++T;
+          if (++js == n_s) {
+            tc_commit(&q_free[pc & 1]);
+            js = 0;
+            ++pc;
+            if (++is < cnt) n_s = pieces[is].n;
+          }
+        };
+        auto o_t = [&]() {
+          const int s = (2 * To + 1) % S, b = To & 1;
+          ok = wait(&kv_full[s], ((2 * To + 1) / S) & 1) && wait(&p_full[b], (To >> 1) & 1) &&
+               (jo > 0 || po < 2 || wait(&o_free[po & 1], ((po >> 1) - 1) & 1));
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t v0 = (ar + s * (C::TILE >> 4)) | kV, p0 = ap + b * (C::PBUF >> 4), t = tO(po & 1);
+          if (jo == 0) mma_ss<false>(t, v0, p0, id_o);
+          else mma_ss<true>(t, v0, p0, id_o);
+#pragma unroll
+          for (int kk = 1; kk < TOK / 16; ++kk) mma_ss<true>(t, v0 + kk * (2048 >> 4), p0 + kk * (2048 >> 4), id_o);
+          tc_commit(&kv_empty[s]);
+          tc_commit(&p_free[b]);
+          ++To;
+          if (++jo == n_o) {
+            tc_commit(&o_full[po & 1]);
+            jo = 0;
+            ++po;
+            if (++io < cnt) n_o = pieces[io].n;
+          }
+        };
+        while (ok && is < cnt) {
+          s_t();
+          if (ok && T - To == 2) o_t();
+        }
+        while (ok && To < T) o_t();
+      }
+      __syncwarp();
+    } while (more());
+    // every product issued here has finished before the tensor memory is released
+    if (elect_one()) tc_commit(drained);
+    mbar_wait(drained, 0, kDrainTimeoutNs);
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ Q, a piece ahead
+    int piece = 0;
+    bool ok = true;
+    do {
+      const int cnt = plan[3];
+      for (int i = 0; i < cnt && ok; ++i, ++piece) {
+        const Piece& it = pieces[i];
+        const int nrows = it.nrows, row0 = it.row0, t0 = it.t0, h = it.h;
+        ok = piece < 2 || __all_sync(0xffffffffu, wait(&q_free[piece & 1], ((piece >> 1) - 1) & 1));
+        if (!ok) break;
+        constexpr int VEC = D / 8;       // 16-byte vectors of a row
+        unsigned char* buf = smem + (piece & 1) * C::QBUF;
+        for (int x = lane; x < nrows * VEC; x += 32) {
+          const int r = x / VEC, v = x - r * VEC, row = row0 + r, tok = div_g(d, row), g = row - tok * d.G;
+          cp_async16(buf + (v >> 3) * C::QCHUNK + r * 128 + (((v & 7) ^ (r & 7)) << 4),
+                     q + (t0 + tok) * q_stride + (h * d.G + g) * D + v * 8, 16);
+        }
+        cp_async_commit();
+        cp_async_wait_all();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[piece & 1]);
+      }
+    } while (more());
+    cp_async_wait_all();
+  } else if (warp == 3) {
+    while (more()) {
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------ softmax and output: a token (a dim) per thread
+    const int lr = (warp - 4) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp - 4) * 32) << 16;
+    const float sl2 = d.scale * d.k_scale * kLog2e;
+    int T = 0, piece = 0;
+    if (lr == 0) sc.meta[c].nrows = 0;
+    do {
+      const int cnt = plan[3];
+      for (int i = 0; i < cnt; ++i, ++piece) {
+        const Piece it = pieces[i];
+        const int n = it.n, nrows = it.nrows;
+        // tiles of the span that every row sees as a whole
+        int hi_all = it.len, lo_all = 0;
+        if (seqs.causal) {
+          hi_all = max(0, it.p0 + div_g(d, it.row0) + 1);
+          lo_all = seqs.window ? max(0, it.p0 + div_g(d, it.row0 + nrows - 1) - seqs.window + 1) : 0;
+        }
+        const int ja = it.ns + (lo_all + TOK - 1) / TOK - it.lo_tile - it.j0;
+        const unsigned n_whole = (unsigned)max(0, it.ns + hi_all / TOK - it.lo_tile - it.j0 - ja);
+        float l[NB];
+#pragma unroll
+        for (int x = 0; x < NB; ++x) l[x] = 0.f;
+        if (lr < 64) m_s[lr] = -INFINITY;
+        bool fresh = true;                       // some row has no m yet
+        for (int j = 0; j < n; ++j, ++T) {
+          const int b = T & 1;
+          wait(&s_full[b], (T >> 1) & 1);
+          tc_fence_after();
+          float x[NB];
+          if constexpr (NB == 8) tmem_ld8(tS(b) + lanes, x);
+          else if constexpr (NB == 16) tmem_ld16(tS(b) + lanes, x);
+          else if constexpr (NB == 32) tmem_ld32(tS(b) + lanes, x);
+          else tmem_ld64(tS(b) + lanes, x);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[b]);
+          if ((unsigned)(j - ja) >= n_whole) {
+            // the columns that see this token: rows from its own position on, to the window's end
+            const int base = tile_base(it, it.j0 + j), t = base + lr;
+            int ca = 0, cb = t < it.len ? nrows : 0;
+            if (seqs.causal) {
+              ca = (int)min((long long)NB, max(0ll, (long long)(t - it.p0) * d.G - it.row0));
+              if (seqs.window && t >= seqs.n_sink)
+                cb = (int)min((long long)cb, max(0ll, ((long long)t + seqs.window - it.p0) * d.G - it.row0));
+            }
+            const uint32_t v0 = bits_below(cb) & ~bits_below(ca), v1 = bits_below(cb - 32) & ~bits_below(ca - 32);
+#pragma unroll
+            for (int y = 0; y < NB; ++y)
+              if (!((y < 32 ? v0 : v1) & (1u << (y & 31)))) x[y] = -INFINITY;
+            if (!FP8 && !tile_whole(it, base)) {
+              // value rows that no row of the item sees
+              const int slot = 2 * T + 1;
+              wait(&kv_full[slot % S], (slot / S) & 1);
+              if (!key_seen(it, t)) {
+                unsigned char* vr = ring + (slot % S) * C::TILE + lr * 128;
+#pragma unroll
+                for (int e = 0; e < C::CHUNKS * 8; ++e)
+                  *reinterpret_cast<uint4*>(vr + (e >> 3) * (TOK * 128) + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+              }
+            }
+          }
+          // P's room: free once the product of the tile before last has read it
+          if (T >= 2) wait(&p_free[b], ((T >> 1) - 1) & 1);
+#pragma unroll 1
+          for (int pass = 0;; ++pass) {          // twice at most
+            if (pass > 0 || fresh) {
+              // m of rows that have none, or that a weight has outgrown: the tile's maximum
+#pragma unroll
+              for (int y = 0; y < NB; ++y) {
+                const float v = warp_max(x[y]);
+                if (lane == 0) x_s[(warp - 4) * 64 + y] = v;
+              }
+              named_bar_sync(2, 128);
+              if (lr < NB) {
+                const float v = fmaxf(fmaxf(x_s[lr], x_s[64 + lr]), fmaxf(x_s[128 + lr], x_s[192 + lr])) * sl2, m = m_s[lr];
+                const float m2 = m == -INFINITY || v > m + kMaxArg ? v : m;
+                f_s[lr] = m == -INFINITY || m2 == m ? 1.f : ex2(m - m2);
+                m_s[lr] = m2;
+              }
+              named_bar_sync(2, 128);
+              bool none = false, scaled = false;
+#pragma unroll
+              for (int y = 0; y < NB; ++y) {
+                none = none || (y < nrows && m_s[y] == -INFINITY);
+                scaled = scaled || f_s[y] != 1.f;
+              }
+              fresh = none;
+              if (scaled) {
+                // O^T holds the earlier tiles' products: all must have finished
+                if (T >= 1) wait(&p_free[b ^ 1], ((T - 1) >> 1) & 1);
+                tc_fence_after();
+#pragma unroll
+                for (int y = 0; y < NB; ++y) l[y] *= f_s[y];
+                if (j > 0) {
+#pragma unroll 1
+                  for (int y = 0; y < NQ; y += 16) {
+                    float ov[16];
+                    uint32_t ow[16];
+                    tmem_ld16(tO(piece & 1) + lanes + y, ov);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(y + e < NB ? ov[e] * f_s[y + e] : ov[e]);
+                    tmem_st16(tO(piece & 1) + lanes + y, ow);
+                  }
+                  tmem_wait_st();
+                }
+              }
+              named_bar_sync(2, 128);       // the factors have been read
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int y = 0; y < NB; ++y) {
+              const float m = m_s[y];
+              const float a = fmaf(x[y], sl2, m == -INFINITY ? 0.f : -m);
+              if (y < nrows) top = fmaxf(top, a);
+            }
+            if (pass > 0 || !group_any(top > kMaxArg)) break;
+          }
+          unsigned char* pr = smem + C::OFF_P + b * C::PBUF + lr * 128;
+#pragma unroll
+          for (int y = 0; y < NB; y += 8) {
+            float p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float m = m_s[y + e];
+              p[e] = ex2(fmaf(x[y + e], sl2, m == -INFINITY ? 0.f : -m));
+              l[y + e] += p[e];
+            }
+            *reinterpret_cast<uint4*>(pr + (((y >> 3) ^ (lr & 7)) << 4)) =
+                make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7]));
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[b]);
+        }
+        // -------------------------------------------------------------- the piece's end: sums, then O^T, a dim per thread
+#pragma unroll
+        for (int y = 0; y < NB; ++y) {
+#pragma unroll
+          for (int w = 16; w; w >>= 1) l[y] += __shfl_xor_sync(0xffffffffu, l[y], w);
+          if (lane == 0) x_s[(warp - 4) * 64 + y] = l[y];
+        }
+        named_bar_sync(2, 128);
+        const bool begun = it.j0 == 0, done = it.j0 + n == it.nt, whole = begun && done;
+        const bool has_prev = o.prev_out && it.s >= o.prev_req[0] && it.s < o.prev_req[o.n_prev];
+        if (lr < nrows) {
+          const float lsum = (x_s[lr] + x_s[64 + lr]) + (x_s[128 + lr] + x_s[192 + lr]);
+          l_s[lr] = lsum;
+          const int row = it.row0 + lr, tok = div_g(d, row);
+          if (whole) {
+            const size_t orow = (size_t)(it.t0 + tok) * d.Hq + it.h * d.G + row - tok * d.G;
+            const RowOut ro = row_out(o, has_prev, orow, m_s[lr], lsum, d.v_scale);
+            f_s[lr] = ro.w_new;
+            x_s[lr] = ro.w_prev;
+            row_lse(o, orow, ro.lse2);
+          } else {
+            sc.ml[((size_t)c * 2 + (begun ? 1 : 0)) * 256 + lr] = make_float2(m_s[lr], lsum);
+          }
+        }
+        named_bar_sync(2, 128);
+        wait(&o_full[piece & 1], (piece >> 1) & 1);
+        tc_fence_after();
+        if (D == 128 || warp < 6) {
+#pragma unroll 1
+          for (int y0 = 0; y0 < nrows; y0 += 8) {
+            float v[8], z[8];
+            size_t at[8];
+            tmem_ld8(tO(piece & 1) + lanes + y0, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int y = y0 + e, row = it.row0 + min(y, nrows - 1), tok = div_g(d, row);
+              at[e] = ((size_t)(it.t0 + tok) * d.Hq + it.h * d.G + row - tok * d.G) * D + lr;
+              z[e] = whole && has_prev && y < nrows && x_s[y] > 0.f ? __ldg(o.prev_out + at[e]) : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int y = y0 + e;
+              if (y >= nrows) continue;
+              if (!(l_s[y] > 0.f)) v[e] = 0.f;
+              if (whole) {
+                const float r = v[e] * f_s[y] + (has_prev && x_s[y] > 0.f ? x_s[y] * z[e] : 0.f);
+                if (o.part_out) o.part_out[at[e]] = r;
+                else o.out[at[e]] = __float2bfloat16(r);
+              } else {
+                sc.o[(((size_t)c * 2 + (begun ? 1 : 0)) * 256 + y) * D + lr] = v[e];
+              }
+            }
+          }
+        }
+        if (begun && !done && lr == 0) {
+          // the item goes on in the next CTAs: up to the one that holds its last tile
+          const int per = plan[5];
+          const long long f_end = (long long)per * c + (T - n) + it.nt;
+          sc.meta[c] = {it.t0, it.row0, nrows, it.h * d.G, (int)((f_end - 1) / per), it.s, 0, 0};
+        }
+        tc_fence_before();
+        named_bar_sync(2, 128);          // sums and factors have been read
+        if (lane == 0) mbar_arrive(&o_free[piece & 1]);
+      }
+    } while (more());
+  } else if constexpr (FP8) {
+    // ------------------------------------------------------------------ E4M3 codes -> bf16 tiles
+    int k = 0;
+    bool ok = true;
+    do {
+      const int cnt = plan[3];
+      for (int i = 0; i < cnt && ok; ++i) {
+        const Piece& it = pieces[i];
+        const int j1 = it.j0 + it.n;
+        for (int j = it.j0; j < j1 && ok; ++j) {
+          const int base = tile_base(it, j);
+          const bool part = !tile_whole(it, base);
+          for (int x = 0; x < 2; ++x, ++k) {
+            const int s = k % S, rs = k % C::STAGING;
+            ok = __all_sync(0xffffffffu, wait(&raw_full[rs], (k / C::STAGING) & 1) &&
+                                             (k < S || wait(&kv_empty[s], ((k / S) & 1) ^ 1)));
+            if (!ok) break;
+            constexpr int VEC = D / 16;              // 16-code vectors of a row
+#pragma unroll
+            for (int y = tid - 256; y < TOK * VEC; y += 256) {
+              const int row = y / VEC, v = y - row * VEC;
+              uint4 w = *reinterpret_cast<const uint4*>(stg + rs * C::CODES + row * D + v * 16);
+              if (x && part && !key_seen(it, base + row)) w = make_uint4(0, 0, 0, 0);
+              widen16(w, ring + s * C::TILE + row * 128, TOK * 128, row, v);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&raw_empty[rs]);
+              mbar_arrive(&kv_full[s]);
+            }
+          }
+        }
+      }
+    } while (more());
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+    if (lane == 0 && *abort_flag) set_error(err, KVS_ERR_TIMEOUT);
+  }
+}
+
+template <int D, bool FP8, int NB>
+cudaError_t launch(const PoolDims& d, const CUtensorMap* tm, const __nv_bfloat16* q, long long q_stride,
+                   const PoolSeqs& seqs, const PoolAttnOut& o, void* scratch, unsigned* err, cudaStream_t s) {
+  using C = Cfg<D, FP8, NB>;
+  auto kern = pool_decode_kernel<D, FP8, NB>;
+  const int smem = C::OFF_TAB + 4 * (seqs.n_seq + 1) + 1024;
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), MAX_SMEM);
+  if (e != cudaSuccess) return e;
+  const Split sp = {device_sm_count(), 2};
+  launch_pdl(kern, dim3(sp.n_cta), dim3(C::THREADS), smem, s, tm[0], tm[1], d, q, q_stride, seqs, o, scratch, sp, err);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_pool_merge(d, o, scratch, sp.n_cta, (int)std::min<long long>(NB, (long long)seqs.n_tok * d.G), s);
+}
+
+template <int D, bool FP8>
+cudaError_t launch_nb(int nb, const PoolDims& d, const CUtensorMap* tm, const __nv_bfloat16* q, long long q_stride,
+                      const PoolSeqs& seqs, const PoolAttnOut& o, void* scratch, unsigned* err, cudaStream_t s) {
+  if (nb <= 8) return launch<D, FP8, 8>(d, tm, q, q_stride, seqs, o, scratch, err, s);
+  if (nb <= 16) return launch<D, FP8, 16>(d, tm, q, q_stride, seqs, o, scratch, err, s);
+  if (nb <= 32) return launch<D, FP8, 32>(d, tm, q, q_stride, seqs, o, scratch, err, s);
+  return launch<D, FP8, 64>(d, tm, q, q_stride, seqs, o, scratch, err, s);
+}
+
+}  // namespace pd
+}  // namespace
+
+cudaError_t launch_pool_decode(const PoolDims& d, const CUtensorMap* tm, const __nv_bfloat16* q, long long q_stride,
+                               const PoolSeqs& seqs, const PoolAttnOut& o, int nb, void* scratch, unsigned* err,
+                               cudaStream_t s) {
+  if (d.d == 128)
+    return d.fp8 ? pd::launch_nb<128, true>(nb, d, tm, q, q_stride, seqs, o, scratch, err, s)
+                 : pd::launch_nb<128, false>(nb, d, tm, q, q_stride, seqs, o, scratch, err, s);
+  return d.fp8 ? pd::launch_nb<64, true>(nb, d, tm, q, q_stride, seqs, o, scratch, err, s)
+               : pd::launch_nb<64, false>(nb, d, tm, q, q_stride, seqs, o, scratch, err, s);
+}
+
+}  // namespace kvs

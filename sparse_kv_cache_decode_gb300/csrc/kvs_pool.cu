@@ -40,9 +40,9 @@ bool pool_dims(const kvs_pool_config* c, PoolDims* d) {
   if (c->kv_dtype != KVS_KV_BF16 && c->kv_dtype != KVS_KV_FP8_E4M3) return false;
   if (!(c->softmax_scale >= 0.f) || isinf(c->softmax_scale)) return false;
   if (!(c->k_scale >= 0.f) || !(c->v_scale >= 0.f) || isinf(c->k_scale) || isinf(c->v_scale)) return false;
-  // rows of a layer are tensor-load coordinates (32 bits), and row tiles are counted in 32 bits
+  // rows of a layer are tensor-load coordinates (32 bits), and rows of a (request, kv head) are divided by G through 2^32 / G
   if ((long long)c->n_slots * c->n_kv_head * c->block_size > 0x7fff0000ll) return false;
-  if ((long long)c->max_tokens * (c->n_q_head / c->n_kv_head) > 0x7fff0000ll) return false;
+  if ((long long)c->max_tokens * (c->n_q_head / c->n_kv_head) > (1 << 25)) return false;
   d->NL = c->n_layer;
   d->n_slots = c->n_slots;
   d->Hq = c->n_q_head;
@@ -50,6 +50,7 @@ bool pool_dims(const kvs_pool_config* c, PoolDims* d) {
   d->G = c->n_q_head / c->n_kv_head;
   d->d = c->head_dim;
   d->bs = c->block_size;
+  d->g_magic = (unsigned)(((1ull << 32) + d->G - 1) / d->G);
   d->log2bs = 0;
   while ((1 << d->log2bs) < d->bs) ++d->log2bs;
   d->max_ctx = c->max_ctx;

@@ -10,6 +10,7 @@ constexpr int kPoolMaxReq = 2048;   // requests (or prefixes) per call
 struct PoolDims {
   int NL, n_slots;
   int Hq, Hkv, G, d, bs, log2bs;
+  unsigned g_magic;       // ceil(2^32 / G), for division by G (G > 1)
   int max_ctx, nb_max, max_req, max_tokens, max_prefix_tokens;
   int fp8, ebytes;
   float scale;            // softmax scale
@@ -90,6 +91,10 @@ size_t pool_attn_scratch_bytes(const PoolDims& d);
 cudaError_t launch_pool_attn(const PoolDims& d, const unsigned char* k, const unsigned char* v, const CUtensorMap* tm,
                              const __nv_bfloat16* q, long long q_stride, const PoolSeqs& seqs, const PoolAttnOut& o,
                              void* scratch, unsigned* err, cudaStream_t s, int* n_launched);
+// The kernel for few rows per (sequence, kv head): row blocks of nb (up to 64) rows.
+cudaError_t launch_pool_decode(const PoolDims& d, const CUtensorMap* tm, const __nv_bfloat16* q, long long q_stride,
+                               const PoolSeqs& seqs, const PoolAttnOut& o, int nb, void* scratch, unsigned* err,
+                               cudaStream_t s);
 size_t pool_weight_scratch_bytes();
 cudaError_t launch_pool_weight(const PoolDims& d, const CUtensorMap* tm, const __nv_bfloat16* q, long long q_stride,
                                const PoolSeqs& seqs, const float* lse2, float* weight, void* scratch, unsigned* err,
