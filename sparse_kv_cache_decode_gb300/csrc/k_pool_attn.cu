@@ -424,16 +424,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
                 if (!(vis & (1u << i2))) s[32 * w + i2] = -INFINITY;
             }
             if (!FP8 && !tile_whole(it, base)) {
-              // value rows that no row of the item sees (a row per thread)
+              // value rows that no row of the item sees
               const int slot = 2 * (N + j) + 1;
               wait(&kv_full[slot % S], (slot / S) & 1);
-              if (!key_seen(it, base + lr)) {
-                unsigned char* vr = ring + (slot % S) * C::TILE + lr * 128;
-#pragma unroll
-                for (int b = 0; b < C::CHUNKS; ++b)
-#pragma unroll 1
-                  for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(vr + b * (TOK * 128) + e * 16) = make_uint4(0, 0, 0, 0);
-              }
+              zero_rows(ring + (slot % S) * C::TILE, C::CHUNKS, lr & ~31, __ballot_sync(0xffffffffu, !key_seen(it, base + lr)));
               fence_proxy_async_smem();
             }
           }

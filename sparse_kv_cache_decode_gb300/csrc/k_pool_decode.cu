@@ -1,7 +1,7 @@
 // Device-resident pools: attention for few rows per (sequence, kv head) on the 5th-generation tensor cores.
 //
 // A decode step has G rows (a group's heads) per K/V row, drafts a few times that: far fewer than a product's 128-row
-// side.  Here the tokens take that side, and the rows the columns (NB = 8, 16, 32 or 64 of them):
+// side.  Here the tokens take that side, and the rows the columns (NB = 8, 16, 32 or, with bf16 pools, 64 of them):
 //   S^T = K Q^T (128 tokens x NB),   P^T = 2^(S^T scale log2 e - m) in bf16,   O^T += V^T P^T (d x NB)
 // so that a tile of 128 tokens costs two products of 16 x (d / 16 + 8) small columns, and the 128 threads of the softmax
 // share its exponentials, a token each: the kernel is bound by the K/V bytes.  V is read as the product's A operand with
@@ -59,16 +59,6 @@ __device__ __forceinline__ float warp_max(float x) {
   asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
-// Whether any of the 128 softmax threads says so (named barrier 1).
-__device__ __forceinline__ bool group_any(bool x) {
-  uint32_t r;
-  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-               : "=r"(r)
-               : "r"((uint32_t)x)
-               : "memory");
-  return r != 0;
-}
-
 template <int D, bool FP8, int NB>
 __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
     pool_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, PoolDims d,
@@ -84,6 +74,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
   float* l_s = m_s + 64;                                              // [64] sums at a piece's end
   float* f_s = m_s + 128;                                             // [64] factors of a new m
   float* x_s = m_s + 256;                                             // [4][64] maxima or sums by warp
+  long long* at_s = reinterpret_cast<long long*>(m_s + 512);          // [64] places of the output rows
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* kv_full = bars;             // [8]
   uint64_t* kv_empty = bars + 8;        // [8]
@@ -97,10 +88,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
   uint64_t* q_free = bars + 42;         // [2]
   uint64_t* o_full = bars + 44;         // [2]
   uint64_t* o_free = bars + 46;         // [2]
-  uint64_t* drained = bars + 48;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 49);
+  uint64_t* vote = bars + 48;           // [2] every softmax warp has looked at its weights' size
+  uint64_t* drained = bars + 50;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 51);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* plan = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  volatile int* outgrown = reinterpret_cast<volatile int*>(tmem_slot + 8);     // [2] a weight has outgrown m
   Piece* pieces = reinterpret_cast<Piece*>(smem + C::OFF_PIECES);
   int* tab = reinterpret_cast<int*>(smem + C::OFF_TAB);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -122,6 +115,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
       mbar_init(&q_free[i], 1);
       mbar_init(&o_full[i], 1);
       mbar_init(&o_free[i], 4);
+      mbar_init(&vote[i], 4);
+      outgrown[i] = 0;
     }
     mbar_init(drained, 1);
     *abort_flag = 0;
@@ -322,8 +317,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
         const int n = it.n, nrows = it.nrows;
         // tiles of the span that every row sees as a whole
         int hi_all = it.len, lo_all = 0;
+        const int pa = it.p0 + div_g(d, it.row0), pa_row = it.row0 - div_g(d, it.row0) * d.G;   // first row's position, head
         if (seqs.causal) {
-          hi_all = max(0, it.p0 + div_g(d, it.row0) + 1);
+          hi_all = max(0, pa + 1);
           lo_all = seqs.window ? max(0, it.p0 + div_g(d, it.row0 + nrows - 1) - seqs.window + 1) : 0;
         }
         const int ja = it.ns + (lo_all + TOK - 1) / TOK - it.lo_tile - it.j0;
@@ -336,46 +332,44 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
         for (int j = 0; j < n; ++j, ++T) {
           const int b = T & 1;
           wait(&s_full[b], (T >> 1) & 1);
+          // P's room: free once the product of the tile before last has read it
+          if (T >= 2) wait(&p_free[b], ((T >> 1) - 1) & 1);
           tc_fence_after();
-          float x[NB];
-          if constexpr (NB == 8) tmem_ld8(tS(b) + lanes, x);
-          else if constexpr (NB == 16) tmem_ld16(tS(b) + lanes, x);
-          else if constexpr (NB == 32) tmem_ld32(tS(b) + lanes, x);
-          else tmem_ld64(tS(b) + lanes, x);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_free[b]);
-          if ((unsigned)(j - ja) >= n_whole) {
+          const bool edge = (unsigned)(j - ja) >= n_whole;
+          const int base = tile_base(it, it.j0 + j), t = base + lr;
+          uint32_t v0 = 0xffffffffu, v1 = 0xffffffffu;
+          if (edge) {
             // the columns that see this token: rows from its own position on, to the window's end
-            const int base = tile_base(it, it.j0 + j), t = base + lr;
             int ca = 0, cb = t < it.len ? nrows : 0;
             if (seqs.causal) {
-              ca = (int)min((long long)NB, max(0ll, (long long)(t - it.p0) * d.G - it.row0));
-              if (seqs.window && t >= seqs.n_sink)
-                cb = (int)min((long long)cb, max(0ll, ((long long)t + seqs.window - it.p0) * d.G - it.row0));
+              if (t > pa) ca = min(t - pa, NB + 1) * d.G - pa_row;
+              if (seqs.window && t >= seqs.n_sink) cb = min(cb, min(max(t - pa + seqs.window, 0), NB + 1) * d.G - pa_row);
             }
-            const uint32_t v0 = bits_below(cb) & ~bits_below(ca), v1 = bits_below(cb - 32) & ~bits_below(ca - 32);
-#pragma unroll
-            for (int y = 0; y < NB; ++y)
-              if (!((y < 32 ? v0 : v1) & (1u << (y & 31)))) x[y] = -INFINITY;
+            v0 = bits_below(cb) & ~bits_below(ca);
+            v1 = bits_below(cb - 32) & ~bits_below(ca - 32);
             if (!FP8 && !tile_whole(it, base)) {
               // value rows that no row of the item sees
               const int slot = 2 * T + 1;
               wait(&kv_full[slot % S], (slot / S) & 1);
-              if (!key_seen(it, t)) {
-                unsigned char* vr = ring + (slot % S) * C::TILE + lr * 128;
-#pragma unroll
-                for (int e = 0; e < C::CHUNKS * 8; ++e)
-                  *reinterpret_cast<uint4*>(vr + (e >> 3) * (TOK * 128) + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-              }
+              zero_rows(ring + (slot % S) * C::TILE, C::CHUNKS, lr & ~31, __ballot_sync(0xffffffffu, !key_seen(it, t)));
             }
           }
-          // P's room: free once the product of the tile before last has read it
-          if (T >= 2) wait(&p_free[b], ((T >> 1) - 1) & 1);
+          unsigned char* pr = smem + C::OFF_P + b * C::PBUF + lr * 128;
+          float x[NB];
 #pragma unroll 1
-          for (int pass = 0;; ++pass) {          // twice at most
-            if (pass > 0 || fresh) {
-              // m of rows that have none, or that a weight has outgrown: the tile's maximum
+          for (bool first = true;; first = false) {
+            if constexpr (NB == 8) tmem_ld8(tS(b) + lanes, x);
+            else if constexpr (NB == 16) tmem_ld16(tS(b) + lanes, x);
+            else if constexpr (NB == 32) tmem_ld32(tS(b) + lanes, x);
+            else tmem_ld64(tS(b) + lanes, x);
+            if (edge) {
+#pragma unroll
+              for (int y = 0; y < NB; ++y)
+                if (!((y < 32 ? v0 : v1) & (1u << (y & 31)))) x[y] = -INFINITY;
+            }
+            const bool set = fresh || !first;
+            if (set) {
+              // m of rows that have none, or that a weight has outgrown: the tile's maximum.  All 128 threads.
 #pragma unroll
               for (int y = 0; y < NB; ++y) {
                 const float v = warp_max(x[y]);
@@ -388,12 +382,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
                 f_s[lr] = m == -INFINITY || m2 == m ? 1.f : ex2(m - m2);
                 m_s[lr] = m2;
               }
+              if (lr == 0) outgrown[b] = 0;
               named_bar_sync(2, 128);
               bool none = false, scaled = false;
 #pragma unroll
               for (int y = 0; y < NB; ++y) {
                 none = none || (y < nrows && m_s[y] == -INFINITY);
-                scaled = scaled || f_s[y] != 1.f;
+                scaled = scaled || (y < nrows && f_s[y] != 1.f);
               }
               fresh = none;
               if (scaled) {
@@ -409,36 +404,44 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
                     uint32_t ow[16];
                     tmem_ld16(tO(piece & 1) + lanes + y, ov);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(y + e < NB ? ov[e] * f_s[y + e] : ov[e]);
+                    for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(y + e < nrows ? ov[e] * f_s[y + e] : ov[e]);
                     tmem_st16(tO(piece & 1) + lanes + y, ow);
                   }
                   tmem_wait_st();
                 }
               }
-              named_bar_sync(2, 128);       // the factors have been read
             }
             float top = -INFINITY;
 #pragma unroll
-            for (int y = 0; y < NB; ++y) {
-              const float m = m_s[y];
-              const float a = fmaf(x[y], sl2, m == -INFINITY ? 0.f : -m);
-              if (y < nrows) top = fmaxf(top, a);
-            }
-            if (pass > 0 || !group_any(top > kMaxArg)) break;
-          }
-          unsigned char* pr = smem + C::OFF_P + b * C::PBUF + lr * 128;
+            for (int y = 0; y < NB; y += 8) {
 #pragma unroll
-          for (int y = 0; y < NB; y += 8) {
-            float p[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float m = m_s[y + e];
-              p[e] = ex2(fmaf(x[y + e], sl2, m == -INFINITY ? 0.f : -m));
-              l[y + e] += p[e];
+              for (int e = 0; e < 8; ++e) {
+                const float m = m_s[y + e], arg = fmaf(x[y + e], sl2, m == -INFINITY ? 0.f : -m);
+                if (y + e < nrows) top = fmaxf(top, arg);
+                x[y + e] = ex2(arg);
+              }
+              *reinterpret_cast<uint4*>(pr + (((y >> 3) ^ (lr & 7)) << 4)) =
+                  make_uint4(pack_bf16x2(x[y], x[y + 1]), pack_bf16x2(x[y + 2], x[y + 3]), pack_bf16x2(x[y + 4], x[y + 5]),
+                             pack_bf16x2(x[y + 6], x[y + 7]));
             }
-            *reinterpret_cast<uint4*>(pr + (((y >> 3) ^ (lr & 7)) << 4)) =
-                make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7]));
+            // a weight that outgrows m: the warps vote (once a tile, so that the phases follow T), and all do the tile
+            // again with a new m
+            if (first) {
+              const bool big = !set && __any_sync(0xffffffffu, top > kMaxArg);
+              if (lane == 0) {
+                if (big) outgrown[b] = 1;
+                mbar_arrive(&vote[b]);
+              }
+            }
+            if (set) break;
+            wait(&vote[b], (T >> 1) & 1);
+            if (!outgrown[b]) break;
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[b]);
+#pragma unroll
+          for (int y = 0; y < NB; ++y) l[y] += x[y];
           fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
@@ -458,8 +461,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
           const float lsum = (x_s[lr] + x_s[64 + lr]) + (x_s[128 + lr] + x_s[192 + lr]);
           l_s[lr] = lsum;
           const int row = it.row0 + lr, tok = div_g(d, row);
+          const size_t orow = (size_t)(it.t0 + tok) * d.Hq + it.h * d.G + row - tok * d.G;
+          at_s[lr] = (long long)((whole ? orow : ((size_t)c * 2 + (begun ? 1 : 0)) * 256 + lr) * D);
           if (whole) {
-            const size_t orow = (size_t)(it.t0 + tok) * d.Hq + it.h * d.G + row - tok * d.G;
             const RowOut ro = row_out(o, has_prev, orow, m_s[lr], lsum, d.v_scale);
             f_s[lr] = ro.w_new;
             x_s[lr] = ro.w_prev;
@@ -475,26 +479,22 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
 #pragma unroll 1
           for (int y0 = 0; y0 < nrows; y0 += 8) {
             float v[8], z[8];
-            size_t at[8];
             tmem_ld8(tO(piece & 1) + lanes + y0, v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int y = y0 + e, row = it.row0 + min(y, nrows - 1), tok = div_g(d, row);
-              at[e] = ((size_t)(it.t0 + tok) * d.Hq + it.h * d.G + row - tok * d.G) * D + lr;
-              z[e] = whole && has_prev && y < nrows && x_s[y] > 0.f ? __ldg(o.prev_out + at[e]) : 0.f;
-            }
+            for (int e = 0; e < 8; ++e)
+              z[e] = whole && has_prev && y0 + e < nrows && x_s[y0 + e] > 0.f ? __ldg(o.prev_out + at_s[y0 + e] + lr) : 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const int y = y0 + e;
-              if (y >= nrows) continue;
+              if (y >= nrows) break;
               if (!(l_s[y] > 0.f)) v[e] = 0.f;
-              if (whole) {
-                const float r = v[e] * f_s[y] + (has_prev && x_s[y] > 0.f ? x_s[y] * z[e] : 0.f);
-                if (o.part_out) o.part_out[at[e]] = r;
-                else o.out[at[e]] = __float2bfloat16(r);
-              } else {
-                sc.o[(((size_t)c * 2 + (begun ? 1 : 0)) * 256 + y) * D + lr] = v[e];
+              if (!whole) {
+                sc.o[at_s[y] + lr] = v[e];
+                continue;
               }
+              const float r = v[e] * f_s[y] + (has_prev && x_s[y] > 0.f ? x_s[y] * z[e] : 0.f);
+              if (o.part_out) o.part_out[at_s[y] + lr] = r;
+              else o.out[at_s[y] + lr] = __float2bfloat16(r);
             }
           }
         }
@@ -510,8 +510,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
       }
     } while (more());
   } else if constexpr (FP8) {
-    // ------------------------------------------------------------------ E4M3 codes -> bf16 tiles
-    int k = 0;
+    // ------------------------------------------------------------------ E4M3 codes -> bf16 tiles, in the ring's order
+    const int th = tid - 256;
+    int k = 0, s = 0, rs = 0;
+    unsigned par = 1, rpar = 0;       // of the slot's last release, of the codes
     bool ok = true;
     do {
       const int cnt = plan[3];
@@ -521,24 +523,41 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
         for (int j = it.j0; j < j1 && ok; ++j) {
           const int base = tile_base(it, j);
           const bool part = !tile_whole(it, base);
+#pragma unroll 1
           for (int x = 0; x < 2; ++x, ++k) {
-            const int s = k % S, rs = k % C::STAGING;
-            ok = __all_sync(0xffffffffu, wait(&raw_full[rs], (k / C::STAGING) & 1) &&
-                                             (k < S || wait(&kv_empty[s], ((k / S) & 1) ^ 1)));
+            ok = __all_sync(0xffffffffu, wait(&raw_full[rs], rpar));
             if (!ok) break;
-            constexpr int VEC = D / 16;              // 16-code vectors of a row
+            constexpr int VEC = D / 16, PER = TOK * VEC / 256;              // 16-code vectors of a row, of a thread
+            const unsigned char* src = stg + rs * C::CODES;
+            uint4 w[PER];
 #pragma unroll
-            for (int y = tid - 256; y < TOK * VEC; y += 256) {
-              const int row = y / VEC, v = y - row * VEC;
-              uint4 w = *reinterpret_cast<const uint4*>(stg + rs * C::CODES + row * D + v * 16);
-              if (x && part && !key_seen(it, base + row)) w = make_uint4(0, 0, 0, 0);
-              widen16(w, ring + s * C::TILE + row * 128, TOK * 128, row, v);
+            for (int e = 0; e < PER; ++e) w[e] = *reinterpret_cast<const uint4*>(src + (th + e * 256) * 16);
+            if (x && part) {
+#pragma unroll
+              for (int e = 0; e < PER; ++e)
+                if (!key_seen(it, base + (th + e * 256) / VEC)) w[e] = make_uint4(0, 0, 0, 0);
+            }
+            ok = k < S || __all_sync(0xffffffffu, wait(&kv_empty[s], par));
+            if (!ok) break;
+            unsigned char* dst = ring + s * C::TILE;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+              const int y = th + e * 256, row = y / VEC;
+              widen16(w[e], dst + row * 128, TOK * 128, row, y - row * VEC);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
               mbar_arrive(&raw_empty[rs]);
               mbar_arrive(&kv_full[s]);
+            }
+            if (++s == S) {
+              s = 0;
+              par ^= 1;
+            }
+            if (++rs == C::STAGING) {
+              rs = 0;
+              rpar ^= 1;
             }
           }
         }
@@ -574,8 +593,9 @@ cudaError_t launch_nb(int nb, const PoolDims& d, const CUtensorMap* tm, const __
                       const PoolSeqs& seqs, const PoolAttnOut& o, void* scratch, unsigned* err, cudaStream_t s) {
   if (nb <= 8) return launch<D, FP8, 8>(d, tm, q, q_stride, seqs, o, scratch, err, s);
   if (nb <= 16) return launch<D, FP8, 16>(d, tm, q, q_stride, seqs, o, scratch, err, s);
-  if (nb <= 32) return launch<D, FP8, 32>(d, tm, q, q_stride, seqs, o, scratch, err, s);
-  return launch<D, FP8, 64>(d, tm, q, q_stride, seqs, o, scratch, err, s);
+  if constexpr (!FP8)
+    if (nb > 32) return launch<D, FP8, 64>(d, tm, q, q_stride, seqs, o, scratch, err, s);
+  return launch<D, FP8, 32>(d, tm, q, q_stride, seqs, o, scratch, err, s);
 }
 
 }  // namespace pd

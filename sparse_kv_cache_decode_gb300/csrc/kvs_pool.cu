@@ -215,6 +215,8 @@ kvs_status kvs_pool_attn(kvs_pool* c, int layer, const void* d_q, long long q_st
   if (n_req == 0 || n_tok == 0) return KVS_OK;
   if (!query_ok(c, d_q, q_stride, d_cu_q, d_ctx_len, d_block2slot, d_out)) return KVS_ERR_INVALID_ARG;
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(d_q);
+  if (window >= d.max_ctx) window = 0;           // no key is that far away (and position + window stays in 32 bits)
+  if (n_sink > d.max_ctx) n_sink = d.max_ctx;
   const unsigned char* k = c->k + layer * c->layer_bytes;
   const PoolSeqs seqs = {d_cu_q, nullptr, d_ctx_len, d_block2slot, n_req, n_req, n_tok, 1, window, n_sink};
   const PoolAttnOut o = {static_cast<__nv_bfloat16*>(d_out), d_lse, d_weight ? c->lse2 : nullptr, nullptr, nullptr, nullptr,

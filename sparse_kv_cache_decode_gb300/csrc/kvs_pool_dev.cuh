@@ -55,6 +55,19 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
       : "memory");
 }
 
+// Zeroes, in a tile of 128-byte rows with `chunks` 64-dim chunks, those of the calling warp's 32 rows (from row0 on) whose bit
+// is set: 8 lanes a row, so that the stores of a step fill all banks.
+__device__ __forceinline__ void zero_rows(unsigned char* tile, int chunks, int row0, uint32_t rows) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int i = 0; i < 32; i += 4) {
+    const int r = i + (lane >> 3);
+    if ((rows >> r) & 1u)
+      for (int b = 0; b < chunks; ++b)
+        *reinterpret_cast<uint4*>(tile + b * (TOK * 128) + (row0 + r) * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+  }
+}
+
 // 8 columns of a thread's tensor-memory lane
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
   uint32_t r[8];

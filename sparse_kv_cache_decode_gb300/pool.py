@@ -43,6 +43,7 @@ class Pool:
             raise KvsError(1, "kvs_pool_workspace_bytes")
         self.nb_max = (cfg.max_ctx + cfg.block_size - 1) // cfg.block_size
         self.device = k.device
+        self.index = k.get_device()          # -1 on the CPU
         shape = (cfg.n_layer, cfg.n_slots, cfg.n_kv_head, cfg.block_size, cfg.head_dim)
         kinds = _FP8 if cfg.kv_dtype == KV_DTYPE["fp8"] else _BF16
         self._whole(k, "k", kinds, shape)
@@ -69,80 +70,87 @@ class Pool:
         except Exception:
             pass
 
-    # ------------------------------------------------------------------ checks
+    # ------------------------------------------------------------------ checks (every call: kept short)
     def _whole(self, t, name, dtypes, shape):
-        """A contiguous tensor of this device."""
+        """Pointer of a contiguous tensor of this device."""
+        if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == self.index:
+            return t.data_ptr()
         if t.dtype not in dtypes:
             raise ValueError(f"{name}: dtype {t.dtype}, expected {dtypes[0]}")
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{name}: not contiguous")
-        if t.device != self.device:
-            raise ValueError(f"{name}: on {t.device}, the pool is on {self.device}")
-        return t.data_ptr()
+        raise ValueError(f"{name}: on {t.device}, the pool is on {self.device}")
 
     def _tokens(self, t, name, heads):
-        """Rows [n_tok][heads][d] of bf16, contiguous within a token: (pointer, token stride)."""
+        """Rows [n_tok][heads][d] of bf16, contiguous within a token: (pointer, token stride, tokens)."""
         d = self.cfg.head_dim
         if t.dtype not in _BF16:
             raise ValueError(f"{name}: dtype {t.dtype}, expected {_BF16[0]}")
         if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
             raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (n_tok, {heads}, {d})")
+        n = t.shape[0]
         s0, s1, s2 = t.stride()
         if s2 != 1 or (heads > 1 and s1 != d):
             raise ValueError(f"{name}: a token's rows must be contiguous")
-        if t.device != self.device:
+        if t.get_device() != self.index:
             raise ValueError(f"{name}: on {t.device}, the pool is on {self.device}")
-        if t.shape[0] > 1 and s0 < heads * d:
+        if n <= 1:
+            s0 = heads * d
+        elif s0 < heads * d:
             raise ValueError(f"{name}: tokens overlap")
-        return t.data_ptr(), (s0 if t.shape[0] > 1 else heads * d)
+        return t.data_ptr(), s0, n
 
     def _batch(self, ctx_len, block2slot, cu_q=None):
         n_req = ctx_len.shape[0]
-        p = self._whole(ctx_len, "ctx_len", _I32, (n_req,)), self._whole(block2slot, "block2slot", _I32, (n_req, self.nb_max))
-        if cu_q is None:
-            return n_req, *p
-        return n_req, self._whole(cu_q, "cu_q", _I32, (n_req + 1,)), *p
+        ctx = self._whole(ctx_len, "ctx_len", _I32, (n_req,))
+        tab = self._whole(block2slot, "block2slot", _I32, (n_req, self.nb_max))
+        return (n_req, ctx, tab) if cu_q is None else (n_req, self._whole(cu_q, "cu_q", _I32, (n_req + 1,)), ctx, tab)
 
-    def _call(self, fn, where, *args, stream=None):
-        if torch.cuda.current_device() != self.device.index:
-            with torch.cuda.device(self.device):
-                return self._call(fn, where, *args, stream=stream)
+    def _stream(self, stream):
         if stream is None:
-            stream = torch.cuda.current_stream()
-        _check(fn(self.h, *args, stream if isinstance(stream, int) else stream.cuda_stream), where)
+            return torch.cuda.current_stream(self.index).cuda_stream
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
+    def _call(self, fn, where, *args):
+        if self.h is None:
+            raise ValueError("Pool: closed")
+        if torch.cuda.current_device() == self.index:
+            status = fn(self.h, *args)
+        else:
+            with torch.cuda.device(self.index):
+                status = fn(self.h, *args)
+        if status != 0:
+            raise KvsError(status, where)
 
     # ------------------------------------------------------------------ C-ABI forwards
     def append(self, layer, k_new, v_new, cu_q, ctx_len, block2slot, stream=None):
         """kvs_pool_append: the call's new tokens, k_new and v_new [n_tok][H_kv][d] bf16, into the pool."""
-        kp, ks = self._tokens(k_new, "k_new", self.cfg.n_kv_head)
-        vp, vs = self._tokens(v_new, "v_new", self.cfg.n_kv_head)
-        n_tok = k_new.shape[0]
-        if v_new.shape[0] != n_tok or ks != vs:
+        kp, ks, n_tok = self._tokens(k_new, "k_new", self.cfg.n_kv_head)
+        vp, vs, n_v = self._tokens(v_new, "v_new", self.cfg.n_kv_head)
+        if n_v != n_tok or ks != vs:
             raise ValueError("k_new and v_new: different numbers or strides of tokens")
         n_req, cu, ctx, tab = self._batch(ctx_len, block2slot, cu_q)
-        self._call(self.L.kvs_pool_append, "kvs_pool_append", layer, kp, vp, ks, cu, ctx, tab, n_req, n_tok, stream=stream)
+        self._call(self.L.kvs_pool_append, "kvs_pool_append", layer, kp, vp, ks, cu, ctx, tab, n_req, n_tok, self._stream(stream))
 
     def attn(self, layer, q, cu_q, ctx_len, block2slot, out, window=0, n_sink=0, lse=None, weight=None, stream=None):
         """kvs_pool_attn: causal attention (window, n_sink: a sliding window and first tokens that stay visible);
         weight accumulates each key's softmax weight."""
         c = self.cfg
-        qp, qs = self._tokens(q, "q", c.n_q_head)
-        n_tok = q.shape[0]
+        qp, qs, n_tok = self._tokens(q, "q", c.n_q_head)
         n_req, cu, ctx, tab = self._batch(ctx_len, block2slot, cu_q)
         o = self._whole(out, "out", _BF16, (n_tok, c.n_q_head, c.head_dim))
         ls = None if lse is None else self._whole(lse, "lse", _F32, (n_tok, c.n_q_head))
         w = None if weight is None else self._whole(weight, "weight", _F32, (n_req, c.n_kv_head, c.max_ctx))
         self._call(self.L.kvs_pool_attn, "kvs_pool_attn", layer, qp, qs, cu, ctx, tab, n_req, n_tok, window, n_sink, o, ls, w,
-                   stream=stream)
+                   self._stream(stream))
 
     def prefix_attn(self, layer, q, cu_q, ctx_len, block2slot, prefix_req, prefix_len, prefix2slot, out, lse=None,
                     stream=None):
         """kvs_pool_prefix_attn: requests [prefix_req[i], prefix_req[i + 1]) see prefix i, then their own tokens."""
         c = self.cfg
-        qp, qs = self._tokens(q, "q", c.n_q_head)
-        n_tok = q.shape[0]
+        qp, qs, n_tok = self._tokens(q, "q", c.n_q_head)
         n_req, cu, ctx, tab = self._batch(ctx_len, block2slot, cu_q)
         n_pre = prefix_len.shape[0]
         pr = self._whole(prefix_req, "prefix_req", _I32, (n_pre + 1,))
@@ -151,7 +159,7 @@ class Pool:
         o = self._whole(out, "out", _BF16, (n_tok, c.n_q_head, c.head_dim))
         ls = None if lse is None else self._whole(lse, "lse", _F32, (n_tok, c.n_q_head))
         self._call(self.L.kvs_pool_prefix_attn, "kvs_pool_prefix_attn", layer, qp, qs, cu, ctx, tab, n_req, n_tok, pr, pl, pt,
-                   n_pre, o, ls, stream=stream)
+                   n_pre, o, ls, self._stream(stream))
 
     def evict(self, layer, weight, ctx_len, block2slot, keep, n_sink, n_recent, dst2slot, kept, n_kept, weight_out,
               stream=None):
@@ -164,7 +172,7 @@ class Pool:
         nk = self._whole(n_kept, "n_kept", _I32, (n_req,))
         wo = self._whole(weight_out, "weight_out", _F32, (n_req, c.n_kv_head, c.max_ctx))
         self._call(self.L.kvs_pool_evict, "kvs_pool_evict", layer, w, ctx, tab, n_req, keep, n_sink, n_recent, dst, kp, nk, wo,
-                   stream=stream)
+                   self._stream(stream))
 
     def launch_count(self) -> int:
         return int(self.L.kvs_pool_launch_count(self.h))

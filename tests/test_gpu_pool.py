@@ -43,6 +43,27 @@ def check_attn(c, got, lse, window=0, sink=0, weights=None):
     assert (got[end:] == 7.0).all() and (lse[end:] == 7.0).all()     # rows behind the last request
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m", [1, 5, 24])
+def test_many_tiles_per_sm(m, d, kv):
+    """Ranges of a dozen tiles and more per SM, where the tile rings wrap several times, cut inside items: equal
+    queries against equal keys, so that one request's oracle serves for all."""
+    hq, hk, n, b = 8, 2, 2500, 64
+    c = PoolCase(m * d, [n], [m], hq, hk, d, 64, kv).cuda(max_req=b, max_tokens=m * b)
+    q = c.d_q.repeat(b, 1, 1)
+    cu = torch.arange(0, m * b + 1, m, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    lse = torch.empty((m * b, hq), device="cuda")
+    c.pool.attn(0, q, cu, c.d_ctx.repeat(b), c.d_table.repeat(b, 1), out, lse=lse)
+    torch.cuda.synchronize()
+    assert c.pool.poll_error() == 0
+    ref, ref_lse, mag, _ = pool_attend(c.query(0), *c.rows[0], c.softmax_scale)
+    out, lse = out.view(b, m, hq, d).double().cpu().numpy(), lse.view(b, m, hq).cpu().numpy()
+    for r in range(b):
+        check_out(out[r], lse[r], ref, ref_lse, mag, d, f"request {r}")
+
+
 HEADS = [(8, 2, 128), (4, 4, 64), (12, 4, 128), (7, 1, 64), (16, 2, 64), (32, 2, 128)]
 
 SINGLE = [  # contexts, window, sink, block size
