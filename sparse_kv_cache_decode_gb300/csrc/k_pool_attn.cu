@@ -743,7 +743,7 @@ cudaError_t launch_pool_attn(const PoolDims& d, const unsigned char*, const unsi
   // rows per (sequence, head) on average: few take the products' column side, more than 128 pay for two row tiles per
   // K/V tile
   const long long rows = ((long long)seqs.n_tok * d.G + seqs.n_seq - 1) / seqs.n_seq;
-  if (rows <= (d.fp8 ? 32 : 64)) return launch_pool_decode(d, tm, q, q_stride, seqs, o, (int)rows, scratch, err, s);
+  if (rows <= (d.fp8 ? 32 : 64)) return launch_pool_decode(d, tm, q, q_stride, seqs, o, (int)rows, scratch, err, s, n_launched);
   const bool two = (long long)seqs.n_tok * d.G > 128ll * seqs.n_seq;
   if (d.d == 128) {
     if (d.fp8) return two ? launch<128, true, 2>(d, tm, q, q_stride, seqs, o, scratch, err, s)

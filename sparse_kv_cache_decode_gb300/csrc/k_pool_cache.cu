@@ -56,22 +56,30 @@ __global__ void __launch_bounds__(kAppendThreads)
 // One CTA per (request, kv head).  The k-th largest weight of the tokens between the first n_sink and the
 // last n_recent is found by radix selection on the ordered keys (score_key: NaN lowest, -0 == +0), 11 bits
 // a pass: eleven bits split the exponent's range fine enough that few tokens share a histogram bin.
+// Each bin has four counters, by lane, as the lanes of a warp often meet in a bin.
 // Each warp owns a contiguous run of tokens, so the kept indices come out in order from one count per
 // warp, a scan over the warps and ballots, without a barrier per step.
+// Five passes read the keys: contexts of up to kSelCached tokens are copied to shared memory first, 8 loads in flight a
+// thread (reading them from L2 in each pass took 39 us at 32K tokens, latency all of it); longer ones are read 8 at a
+// time from L2.
 constexpr int kSelThreads = 1024;
 constexpr int kSelBins = 2048;
+constexpr int kSelCached = 45056;
+constexpr int kSelCopies = 4;
 
+template <bool CACHED>
 __global__ void __launch_bounds__(kSelThreads)
     pool_evict_select_kernel(PoolDims d, const float* __restrict__ weight, const int* __restrict__ ctx_len, int keep,
                              int n_sink, int n_recent, int* __restrict__ kept, int* __restrict__ n_kept,
                              unsigned* err) {
   kvs_pdl_entry();
-  __shared__ int hist[kSelBins];
+  extern __shared__ uint32_t keys[];       // [len] (CACHED)
+  __shared__ __align__(16) int hist[kSelBins * kSelCopies];
   __shared__ int warp_a[32], warp_b[32];
   __shared__ int pick[2];
   const int u = blockIdx.x, r = u / d.Hkv, h = u - r * d.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int NW = kSelThreads / 32;
+  constexpr int NW = kSelThreads / 32, UN = 8;
   int len = ctx_len[r];
   if (len < 0 || len > d.max_ctx) {
     if (tid == 0) set_error(err, KVS_ERR_BAD_INDEX);
@@ -85,6 +93,17 @@ __global__ void __launch_bounds__(kSelThreads)
     for (int i = tid; i < n; i += kSelThreads) out[i] = i;
     return;
   }
+  if (CACHED) {
+    for (int t0 = tid; t0 < len; t0 += UN * kSelThreads) {
+      float v[UN];
+#pragma unroll
+      for (int i = 0; i < UN; ++i) v[i] = t0 + i * kSelThreads < len ? w[t0 + i * kSelThreads] : 0.f;
+#pragma unroll
+      for (int i = 0; i < UN; ++i)
+        if (t0 + i * kSelThreads < len) keys[t0 + i * kSelThreads] = score_key(v[i]);
+    }
+  }
+  auto key_of = [&](int t) { return CACHED ? keys[t] : score_key(__ldcg(w + t)); };
   // tokens [lo, hi) compete for k places
   const int lo = n_sink, hi = len - n_recent, k = keep - n_sink - n_recent;
   uint32_t prefix = 0;        // key bits decided so far
@@ -93,18 +112,24 @@ __global__ void __launch_bounds__(kSelThreads)
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11, bins = 1 << bits;
-      for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+      for (int i = tid; i < kSelBins; i += kSelThreads) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
       __syncthreads();
-      for (int t = lo + tid; t < hi; t += kSelThreads) {
-        const uint32_t key = score_key(w[t]);
-        if (pass == 0 || (key >> (shift + bits)) == prefix) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
+      for (int t0 = lo + tid; t0 < hi; t0 += UN * kSelThreads) {
+        uint32_t key[UN];
+#pragma unroll
+        for (int i = 0; i < UN; ++i) key[i] = t0 + i * kSelThreads < hi ? key_of(t0 + i * kSelThreads) : 0u;
+#pragma unroll
+        for (int i = 0; i < UN; ++i)
+          if (t0 + i * kSelThreads < hi && (pass == 0 || (key[i] >> (shift + bits)) == prefix))
+            atomicAdd(&hist[((key[i] >> shift) & (bins - 1)) * kSelCopies + (lane & 3)], 1);
       }
       __syncthreads();
       // the bin of the left-th key from the top: thread i owns the two bins bins-1-2i and bins-2-2i
       int c0 = 0, c1 = 0;
       if (2 * tid < bins) {
-        c0 = hist[bins - 1 - 2 * tid];
-        c1 = hist[bins - 2 - 2 * tid];
+        const int4 a = reinterpret_cast<const int4*>(hist)[bins - 1 - 2 * tid], b4 = reinterpret_cast<const int4*>(hist)[bins - 2 - 2 * tid];
+        c0 = a.x + a.y + a.z + a.w;
+        c1 = b4.x + b4.y + b4.z + b4.w;
       }
       int x = c0 + c1;
 #pragma unroll
@@ -129,17 +154,26 @@ __global__ void __launch_bounds__(kSelThreads)
   } else {
     prefix = 0xffffffffu;     // no key is above it, and no place is left for its equals
     left = 0;
+    __syncthreads();          // the cached keys
   }
   // `left` places go to the earliest keys equal to the threshold, the rest to every key above it
   const int per = ((len + NW - 1) / NW + 31) / 32 * 32;
   const int b = min(len, warp * per), e = min(len, b + per);
   int n_gt = 0, n_eq = 0;
-  for (int t0 = b; t0 < e; t0 += 32) {
-    const int t = t0 + lane;
-    const bool in = t < e, mid = in && t >= lo && t < hi;
-    const uint32_t key = mid ? score_key(w[t]) : 0u;
-    n_gt += __popc(__ballot_sync(0xffffffffu, in && (!mid || key > prefix)));
-    n_eq += __popc(__ballot_sync(0xffffffffu, mid && key == prefix));
+  for (int t0 = b; t0 < e; t0 += 32 * UN) {
+    uint32_t key[UN];
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      const int t = t0 + 32 * i + lane;
+      key[i] = t < e && t >= lo && t < hi ? key_of(t) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      const int t = t0 + 32 * i + lane;
+      const bool in = t < e, mid = in && t >= lo && t < hi;
+      n_gt += __popc(__ballot_sync(0xffffffffu, in && (!mid || key[i] > prefix)));
+      n_eq += __popc(__ballot_sync(0xffffffffu, mid && key[i] == prefix));
+    }
   }
   if (lane == 0) {
     warp_a[warp] = n_gt;
@@ -151,25 +185,34 @@ __global__ void __launch_bounds__(kSelThreads)
     at += warp_a[i] + min(warp_b[i], max(0, left - eq));
     eq += warp_b[i];
   }
-  for (int t0 = b; t0 < e; t0 += 32) {
-    const int t = t0 + lane;
-    const bool in = t < e, mid = in && t >= lo && t < hi;
-    const uint32_t key = mid ? score_key(w[t]) : 0u;
-    const bool same = mid && key == prefix;
-    const unsigned eqs = __ballot_sync(0xffffffffu, same);
-    const bool take = in && (!mid || key > prefix || (same && eq + __popc(eqs & ((1u << lane) - 1)) < left));
-    const unsigned m = __ballot_sync(0xffffffffu, take);
-    if (take) out[at + __popc(m & ((1u << lane) - 1))] = t;
-    at += __popc(m);
-    eq += __popc(eqs);
+  for (int t0 = b; t0 < e; t0 += 32 * UN) {
+    uint32_t key[UN];
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      const int t = t0 + 32 * i + lane;
+      key[i] = t < e && t >= lo && t < hi ? key_of(t) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      const int t = t0 + 32 * i + lane;
+      const bool in = t < e, mid = in && t >= lo && t < hi;
+      const bool same = mid && key[i] == prefix;
+      const unsigned eqs = __ballot_sync(0xffffffffu, same);
+      const bool take = in && (!mid || key[i] > prefix || (same && eq + __popc(eqs & ((1u << lane) - 1)) < left));
+      const unsigned m = __ballot_sync(0xffffffffu, take);
+      if (take) out[at + __popc(m & ((1u << lane) - 1))] = t;
+      at += __popc(m);
+      eq += __popc(eqs);
+    }
   }
 }
 
 // ------------------------------------------------------------------ evict: gather
 // One warp copies 32 / VECS kept tokens of a (request, kv head) at a time, VECS 16-byte vectors of K and V
-// rows together, kGatherDeep steps in flight.
+// rows together, kGatherDeep of them in flight: first all indices, then all slots, then all rows, so that a CTA pays
+// three load latencies for its tokens and not three for each.
 constexpr int kGatherThreads = 256;
-constexpr int kGatherDeep = 4;
+constexpr int kGatherDeep = 8;
 
 template <int VECS>   // 16-byte vectors of a token's K and V rows: 2 * d * ebytes / 16
 __global__ void __launch_bounds__(kGatherThreads)
@@ -181,41 +224,58 @@ __global__ void __launch_bounds__(kGatherThreads)
   constexpr int PER = 32 / VECS;                                   // tokens per warp and step
   constexpr int SPAN = kGatherThreads / 32 * PER * kGatherDeep;    // tokens per CTA
   const int u = blockIdx.y, r = u / d.Hkv, h = u - r * d.Hkv;
-  int len = ctx_len[r];
-  if (len < 0 || len > d.max_ctx) return;                          // reported by the selection
-  const int n = min(keep, len);
   const int first = blockIdx.x * SPAN;
-  if (first >= n) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / VECS, vec = lane % VECS;
   const bool is_v = vec >= VECS / 2;
   const int part = vec % (VECS / 2);
   unsigned char* pool = is_v ? vpool : kpool;
-  const int row_bytes = VECS / 2 * 16;
-  uint4 x[kGatherDeep];
-  size_t to[kGatherDeep];
-  bool ok[kGatherDeep];
+  constexpr int row_bytes = VECS / 2 * 16;
+  int t[kGatherDeep];
+  // (entries past the kept ones are in the buffer, and not used)
 #pragma unroll
   for (int j = 0; j < kGatherDeep; ++j) {
     const int i = first + (j * (kGatherThreads / 32) + warp) * PER + sub;
-    ok[j] = i < n;
-    if (!ok[j]) continue;
-    const int t = kept[(size_t)u * keep + i];
-    const int from_slot = table[(size_t)r * d.nb_max + (t >> d.log2bs)];
-    const int to_slot = dst[(size_t)r * d.nb_max + (i >> d.log2bs)];
-    if (vec == 0) weight_out[(size_t)u * d.max_ctx + i] = weight[(size_t)u * d.max_ctx + t];
-    if (from_slot < 0 || from_slot >= d.n_slots || to_slot < 0 || to_slot >= d.n_slots) {
-      set_error(err, KVS_ERR_BAD_INDEX);
-      ok[j] = false;
-      continue;
+    t[j] = i < keep ? kept[(size_t)u * keep + i] : 0;
+  }
+  int len = ctx_len[r];
+  if (len < 0 || len > d.max_ctx) return;                          // reported by the selection
+  const int n = min(keep, len);
+  if (first >= n) return;
+  int from_slot[kGatherDeep], to_slot[kGatherDeep];
+  float wt[kGatherDeep];
+#pragma unroll
+  for (int j = 0; j < kGatherDeep; ++j) {
+    const int i = first + (j * (kGatherThreads / 32) + warp) * PER + sub;
+    from_slot[j] = to_slot[j] = -1;
+    if (i < n) {
+      from_slot[j] = table[(size_t)r * d.nb_max + (t[j] >> d.log2bs)];
+      to_slot[j] = dst[(size_t)r * d.nb_max + (i >> d.log2bs)];
+      if (vec == 0) wt[j] = weight[(size_t)u * d.max_ctx + t[j]];
     }
-    const size_t from = (((size_t)from_slot * d.Hkv + h) * d.bs + (t & (d.bs - 1))) * row_bytes + part * 16;
-    to[j] = (((size_t)to_slot * d.Hkv + h) * d.bs + (i & (d.bs - 1))) * row_bytes + part * 16;
-    x[j] = *reinterpret_cast<const uint4*>(pool + from);
+  }
+  uint4 x[kGatherDeep];
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < kGatherDeep; ++j) {
+    const int i = first + (j * (kGatherThreads / 32) + warp) * PER + sub;
+    const bool ok = from_slot[j] >= 0 && from_slot[j] < d.n_slots && to_slot[j] >= 0 && to_slot[j] < d.n_slots;
+    bad = bad || (i < n && !ok);
+    if (ok)
+      x[j] = __ldcs(reinterpret_cast<const uint4*>(
+          pool + (((size_t)from_slot[j] * d.Hkv + h) * d.bs + (t[j] & (d.bs - 1))) * row_bytes + part * 16));
+    else
+      to_slot[j] = -1;
   }
 #pragma unroll
-  for (int j = 0; j < kGatherDeep; ++j)
-    if (ok[j]) *reinterpret_cast<uint4*>(pool + to[j]) = x[j];
+  for (int j = 0; j < kGatherDeep; ++j) {
+    const int i = first + (j * (kGatherThreads / 32) + warp) * PER + sub;
+    if (to_slot[j] >= 0)
+      *reinterpret_cast<uint4*>(pool + (((size_t)to_slot[j] * d.Hkv + h) * d.bs + (i & (d.bs - 1))) * row_bytes + part * 16) =
+          x[j];
+    if (i < n && vec == 0) weight_out[(size_t)u * d.max_ctx + i] = wt[j];
+  }
+  if (bad) set_error(err, KVS_ERR_BAD_INDEX);
 }
 
 }  // namespace
@@ -233,8 +293,16 @@ cudaError_t launch_pool_evict(const PoolDims& d, unsigned char* k, unsigned char
                               const int* ctx_len, const int* table, int n_req, int keep, int n_sink, int n_recent,
                               const int* dst, int* kept, int* n_kept, float* weight_out, unsigned* err,
                               cudaStream_t s) {
-  launch_pdl(pool_evict_select_kernel, dim3(n_req * d.Hkv), dim3(kSelThreads), 0, s, d, weight, ctx_len, keep, n_sink,
-             n_recent, kept, n_kept, err);
+  if (d.max_ctx <= kSelCached) {
+    const int smem = d.max_ctx * 4;
+    cudaError_t e1 = set_max_dynamic_smem(reinterpret_cast<const void*>(pool_evict_select_kernel<true>), kSelCached * 4);
+    if (e1 != cudaSuccess) return e1;
+    launch_pdl(pool_evict_select_kernel<true>, dim3(n_req * d.Hkv), dim3(kSelThreads), smem, s, d, weight, ctx_len, keep, n_sink,
+               n_recent, kept, n_kept, err);
+  } else {
+    launch_pdl(pool_evict_select_kernel<false>, dim3(n_req * d.Hkv), dim3(kSelThreads), 0, s, d, weight, ctx_len, keep, n_sink,
+               n_recent, kept, n_kept, err);
+  }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int vecs = 2 * d.d * d.ebytes / 16;

@@ -10,10 +10,12 @@
 // only when a weight passes 2^40; the sums l are kept per thread and reduced at a piece's end.
 //
 // The tiles of all items form one sequence that is cut into equal ranges, one per CTA (one per SM), as in the kernel
-// for many rows; the same merge kernel joins the items that a cut splits.
+// for many rows; the same merge kernel joins the items that a cut splits.  (Joining them in the last of an item's CTAs to
+// finish saves a launch, but its fences and serial loads cost more: 16.7 us against 13.3 for one request's token.)
 //
 // Roles: warp 0 brings K/V tiles, warp 1 issues the products (S^T of a tile before O^T of the tile before it, across
-// pieces), warp 2 loads Q, warps 4-7 are the softmax; with E4M3 pools warps 8-15 widen the codes to bf16 tiles.
+// pieces), warp 2 loads Q, warps 4-7 are the softmax; with E4M3 pools warps 8-11 (K) and 12-15 (V)
+// widen the codes to bf16 tiles.
 // Value rows that no row of the item sees are zeroed before their product.  All waits are bounded.
 #include <algorithm>
 
@@ -33,25 +35,26 @@ struct Cfg {
   static constexpr int CHUNKS = D / 64;
   static constexpr int NQ = NB < 16 ? 16 : NB;                // columns of the products
   static constexpr int QCHUNK = NQ * 128;                     // 64 dims of the rows
-  static constexpr int QBUF = CHUNKS * QCHUNK;                // one item's Q (two are held)
-  static constexpr int PBUF = TOK * 128;                      // P^T: 128 tokens, 64 columns of room (two are held)
+  static constexpr int QBUF = CHUNKS * QCHUNK;                // one item's Q
+  static constexpr int QB = FP8 && NB == 32 ? 1 : 2;          // items whose Q is held
+  // P^T: 128 tokens of 128 bytes, 64 columns of room: two tiles of up to 32 columns side by side, or one of 64
+  static constexpr int PBYTES = (NB == 64 ? 2 : 1) * TOK * 128;
+  static constexpr int PSTEP = NB == 64 ? TOK * 128 : 64;     // bytes from one tile's P^T to the other's
   static constexpr int TILE = TOK * D * 2;
   static constexpr int CODES = TOK * D;
   static constexpr int THREADS = FP8 ? 512 : 256;
-  static constexpr int FIXED = 4096 + 512 + 1024 + 4 * (kPoolMaxReq + 1) + kPieces * 64 + 2 * QBUF + 2 * PBUF;
-  static constexpr int ROOM = MAX_SMEM - FIXED;
-  static constexpr int STAGES = FP8 ? (D == 128 ? 3 : 4) : (ROOM / TILE > 8 ? 8 : ROOM / TILE);     // bf16 tiles
-  static constexpr int STG_ROOM = FP8 ? (ROOM - STAGES * TILE) / CODES : 0;
-  static constexpr int STAGING = STG_ROOM > 8 ? 8 : STG_ROOM;                                       // code tiles
-  static constexpr int OFF_P = 2 * QBUF;
-  static constexpr int OFF_RING = OFF_P + 2 * PBUF;
-  static constexpr int OFF_STG = OFF_RING + STAGES * TILE;
-  static constexpr int OFF_ML = OFF_STG + STAGING * CODES;    // m, l and maxima: 16 x 64 floats
-  static constexpr int OFF_BAR = OFF_ML + 4096;
+  static constexpr int ROOM = MAX_SMEM - 3072 - 512 - 2048 - 4 * (kPoolMaxReq + 1) - kPieces * 64 - QB * QBUF - PBYTES;
+  // bf16 tiles; with E4M3 pools two of K and two of V, widened by warps of their own
+  static constexpr int STAGES = FP8 ? 4 : ROOM / TILE > 8 ? 8 : ROOM / TILE;
+  static constexpr int OFF_P = QB * QBUF;
+  static constexpr int OFF_RING = OFF_P + PBYTES;
+  static constexpr int OFF_ML = OFF_RING + STAGES * TILE;     // m, l, factors, maxima by warp, places: 3 KiB
+  static constexpr int OFF_BAR = OFF_ML + 3072;
   static constexpr int OFF_PIECES = OFF_BAR + 512;
-  static constexpr int OFF_TAB = OFF_PIECES + kPieces * 64;
-  static_assert(STAGES >= 3 && (!FP8 || STAGING >= 2), "shared memory plan");
-  static_assert(OFF_TAB + 4 * (kPoolMaxReq + 1) + 1024 <= MAX_SMEM, "shared memory plan");
+  static constexpr int OFF_STG = (OFF_PIECES + kPieces * 64 + 1023) / 1024 * 1024;   // code tiles (E4M3), then the table
+  // shared memory with `staging` code tiles
+  static int bytes(int staging, int n_seq) { return OFF_STG + staging * CODES + 4 * (n_seq + 1) + 1024; }
+  static_assert(STAGES >= 3 && OFF_STG + (FP8 ? 2 * CODES : 0) + 4 * (kPoolMaxReq + 1) + 1024 <= MAX_SMEM, "shared memory plan");
 };
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -63,7 +66,7 @@ template <int D, bool FP8, int NB>
 __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
     pool_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, PoolDims d,
                        const __nv_bfloat16* __restrict__ q, long long q_stride, PoolSeqs seqs, PoolAttnOut o, void* scratch,
-                       Split sp, unsigned* err) {
+                       Split sp, int staging, unsigned* err) {
   using C = Cfg<D, FP8, NB>;
   constexpr int S = C::STAGES, NQ = C::NQ;
   extern __shared__ unsigned char smem_raw[];
@@ -95,16 +98,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
   volatile int* plan = reinterpret_cast<volatile int*>(tmem_slot + 2);
   volatile int* outgrown = reinterpret_cast<volatile int*>(tmem_slot + 8);     // [2] a weight has outgrown m
   Piece* pieces = reinterpret_cast<Piece*>(smem + C::OFF_PIECES);
-  int* tab = reinterpret_cast<int*>(smem + C::OFF_TAB);
+  int* tab = reinterpret_cast<int*>(smem + C::OFF_STG + staging * C::CODES);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x;
 
   if (tid == 0) {
     for (int i = 0; i < 8; ++i) {
-      mbar_init(&kv_full[i], FP8 ? 8 : 1);
+      mbar_init(&kv_full[i], FP8 ? 4 : 1);
       mbar_init(&kv_empty[i], 1);
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 8);
+      mbar_init(&raw_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
   if (warp == 0) {
     // ------------------------------------------------------------------ K/V tiles: a lane per block of a tile
     constexpr int BOXES = FP8 ? 1 : C::CHUNKS;
-    constexpr int SLOTS = FP8 ? C::STAGING : S;
+    const int SLOTS = FP8 ? staging : S;
     uint64_t* full = FP8 ? raw_full : kv_full;
     uint64_t* empty = FP8 ? raw_empty : kv_empty;
     const int pages = TOK >> d.log2bs;
@@ -225,7 +228,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
           ok = ok && wait(&kv_full[s], ((2 * T) / S) & 1) && (T < 2 || wait(&s_free[b], ((T >> 1) - 1) & 1));
           if (!ok) return;
           tc_fence_after();
-          const uint32_t k0 = ar + s * (C::TILE >> 4), q0 = aq + (pc & 1) * (C::QBUF >> 4), t = tS(b);
+          const uint32_t k0 = ar + s * (C::TILE >> 4), q0 = aq + (pc % C::QB) * (C::QBUF >> 4), t = tS(b);
           mma_ss<false>(t, k0, q0, id_s);
 #pragma unroll
           for (int k16 = 1; k16 < D / 16; ++k16)
@@ -247,7 +250,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
                (jo > 0 || po < 2 || wait(&o_free[po & 1], ((po >> 1) - 1) & 1));
           if (!ok) return;
           tc_fence_after();
-          const uint32_t v0 = (ar + s * (C::TILE >> 4)) | kV, p0 = ap + b * (C::PBUF >> 4), t = tO(po & 1);
+          const uint32_t v0 = (ar + s * (C::TILE >> 4)) | kV, p0 = ap + b * (C::PSTEP >> 4), t = tO(po & 1);
           if (jo == 0) mma_ss<false>(t, v0, p0, id_o);
           else mma_ss<true>(t, v0, p0, id_o);
 #pragma unroll
@@ -283,10 +286,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
       for (int i = 0; i < cnt && ok; ++i, ++piece) {
         const Piece& it = pieces[i];
         const int nrows = it.nrows, row0 = it.row0, t0 = it.t0, h = it.h;
-        ok = piece < 2 || __all_sync(0xffffffffu, wait(&q_free[piece & 1], ((piece >> 1) - 1) & 1));
+        const int behind = piece - C::QB;      // the piece whose Q is there
+        ok = behind < 0 || __all_sync(0xffffffffu, wait(&q_free[behind & 1], (behind >> 1) & 1));
         if (!ok) break;
         constexpr int VEC = D / 8;       // 16-byte vectors of a row
-        unsigned char* buf = smem + (piece & 1) * C::QBUF;
+        unsigned char* buf = smem + (piece % C::QB) * C::QBUF;
         for (int x = lane; x < nrows * VEC; x += 32) {
           const int r = x / VEC, v = x - r * VEC, row = row0 + r, tok = div_g(d, row), g = row - tok * d.G;
           cp_async16(buf + (v >> 3) * C::QCHUNK + r * 128 + (((v & 7) ^ (r & 7)) << 4),
@@ -354,7 +358,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
               zero_rows(ring + (slot % S) * C::TILE, C::CHUNKS, lr & ~31, __ballot_sync(0xffffffffu, !key_seen(it, t)));
             }
           }
-          unsigned char* pr = smem + C::OFF_P + b * C::PBUF + lr * 128;
+          unsigned char* pr = smem + C::OFF_P + (NB == 64 ? b * C::PSTEP : 0) + lr * 128;
+          const int pc0 = NB == 64 ? 0 : b * 4;        // its first 16-byte chunk
           float x[NB];
 #pragma unroll 1
           for (bool first = true;; first = false) {
@@ -420,7 +425,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
                 if (y + e < nrows) top = fmaxf(top, arg);
                 x[y + e] = ex2(arg);
               }
-              *reinterpret_cast<uint4*>(pr + (((y >> 3) ^ (lr & 7)) << 4)) =
+              *reinterpret_cast<uint4*>(pr + (((pc0 + (y >> 3)) ^ (lr & 7)) << 4)) =
                   make_uint4(pack_bf16x2(x[y], x[y + 1]), pack_bf16x2(x[y + 2], x[y + 3]), pack_bf16x2(x[y + 4], x[y + 5]),
                              pack_bf16x2(x[y + 6], x[y + 7]));
             }
@@ -510,9 +515,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
       }
     } while (more());
   } else if constexpr (FP8) {
-    // ------------------------------------------------------------------ E4M3 codes -> bf16 tiles, in the ring's order
-    const int th = tid - 256;
-    int k = 0, s = 0, rs = 0;
+    // ------------------------------------------------------------------ E4M3 codes -> bf16 tiles: K (warps 8-11), V (12-15)
+    // Each has every other slot of both rings to itself, so its waits never look two phases ahead.
+    const int x = (warp - 8) >> 2, th = tid & 127;
+    int k = x, s = x, rs = x;
     unsigned par = 1, rpar = 0;       // of the slot's last release, of the codes
     bool ok = true;
     do {
@@ -520,45 +526,43 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
       for (int i = 0; i < cnt && ok; ++i) {
         const Piece& it = pieces[i];
         const int j1 = it.j0 + it.n;
-        for (int j = it.j0; j < j1 && ok; ++j) {
+        for (int j = it.j0; j < j1 && ok; ++j, k += 2) {
+          ok = __all_sync(0xffffffffu, wait(&raw_full[rs], rpar));
+          if (!ok) break;
+          constexpr int VEC = D / 16, PER = TOK * VEC / 128;              // 16-code vectors of a row, of a thread
+          const unsigned char* src = stg + rs * C::CODES;
+          uint4 w[PER];
+#pragma unroll
+          for (int e = 0; e < PER; ++e) w[e] = *reinterpret_cast<const uint4*>(src + (th + e * 128) * 16);
           const int base = tile_base(it, j);
-          const bool part = !tile_whole(it, base);
-#pragma unroll 1
-          for (int x = 0; x < 2; ++x, ++k) {
-            ok = __all_sync(0xffffffffu, wait(&raw_full[rs], rpar));
-            if (!ok) break;
-            constexpr int VEC = D / 16, PER = TOK * VEC / 256;              // 16-code vectors of a row, of a thread
-            const unsigned char* src = stg + rs * C::CODES;
-            uint4 w[PER];
+          if (x && !tile_whole(it, base)) {
 #pragma unroll
-            for (int e = 0; e < PER; ++e) w[e] = *reinterpret_cast<const uint4*>(src + (th + e * 256) * 16);
-            if (x && part) {
+            for (int e = 0; e < PER; ++e)
+              if (!key_seen(it, base + (th + e * 128) / VEC)) w[e] = make_uint4(0, 0, 0, 0);
+          }
+          ok = k < S || __all_sync(0xffffffffu, wait(&kv_empty[s], par));
+          if (!ok) break;
+          unsigned char* dst = ring + s * C::TILE;
 #pragma unroll
-              for (int e = 0; e < PER; ++e)
-                if (!key_seen(it, base + (th + e * 256) / VEC)) w[e] = make_uint4(0, 0, 0, 0);
-            }
-            ok = k < S || __all_sync(0xffffffffu, wait(&kv_empty[s], par));
-            if (!ok) break;
-            unsigned char* dst = ring + s * C::TILE;
-#pragma unroll
-            for (int e = 0; e < PER; ++e) {
-              const int y = th + e * 256, row = y / VEC;
-              widen16(w[e], dst + row * 128, TOK * 128, row, y - row * VEC);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&raw_empty[rs]);
-              mbar_arrive(&kv_full[s]);
-            }
-            if (++s == S) {
-              s = 0;
-              par ^= 1;
-            }
-            if (++rs == C::STAGING) {
-              rs = 0;
-              rpar ^= 1;
-            }
+          for (int e = 0; e < PER; ++e) {
+            const int y = th + e * 128, row = y / VEC;
+            widen16(w[e], dst + row * 128, TOK * 128, row, y - row * VEC);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&kv_full[s]);
+            mbar_arrive(&raw_empty[rs]);
+          }
+          s += 2;
+          if (s >= S) {
+            s = x;
+            par ^= 1;
+          }
+          rs += 2;
+          if (rs >= staging) {
+            rs = x;
+            rpar ^= 1;
           }
         }
       }
@@ -575,27 +579,31 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
 
 template <int D, bool FP8, int NB>
 cudaError_t launch(const PoolDims& d, const CUtensorMap* tm, const __nv_bfloat16* q, long long q_stride,
-                   const PoolSeqs& seqs, const PoolAttnOut& o, void* scratch, unsigned* err, cudaStream_t s) {
+                   const PoolSeqs& seqs, const PoolAttnOut& o, void* scratch, unsigned* err, cudaStream_t s, int* n_launched) {
   using C = Cfg<D, FP8, NB>;
   auto kern = pool_decode_kernel<D, FP8, NB>;
-  const int smem = C::OFF_TAB + 4 * (seqs.n_seq + 1) + 1024;
   cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), MAX_SMEM);
   if (e != cudaSuccess) return e;
   const Split sp = {device_sm_count(), 2};
-  launch_pdl(kern, dim3(sp.n_cta), dim3(C::THREADS), smem, s, tm[0], tm[1], d, q, q_stride, seqs, o, scratch, sp, err);
+  // code tiles in flight: as many as fit beside the table of the sequences
+  const int staging = !FP8 ? 0 : C::bytes(8, seqs.n_seq) <= MAX_SMEM ? 8 : C::bytes(4, seqs.n_seq) <= MAX_SMEM ? 4 : 2;
+  launch_pdl(kern, dim3(sp.n_cta), dim3(C::THREADS), C::bytes(staging, seqs.n_seq), s, tm[0], tm[1], d, q, q_stride, seqs, o,
+             scratch, sp, staging, err);
   e = cudaGetLastError();
+  *n_launched = 1;
   if (e != cudaSuccess) return e;
+  *n_launched = 2;
   return launch_pool_merge(d, o, scratch, sp.n_cta, (int)std::min<long long>(NB, (long long)seqs.n_tok * d.G), s);
 }
 
 template <int D, bool FP8>
 cudaError_t launch_nb(int nb, const PoolDims& d, const CUtensorMap* tm, const __nv_bfloat16* q, long long q_stride,
-                      const PoolSeqs& seqs, const PoolAttnOut& o, void* scratch, unsigned* err, cudaStream_t s) {
-  if (nb <= 8) return launch<D, FP8, 8>(d, tm, q, q_stride, seqs, o, scratch, err, s);
-  if (nb <= 16) return launch<D, FP8, 16>(d, tm, q, q_stride, seqs, o, scratch, err, s);
+                      const PoolSeqs& seqs, const PoolAttnOut& o, void* scratch, unsigned* err, cudaStream_t s, int* n_launched) {
+  if (nb <= 8) return launch<D, FP8, 8>(d, tm, q, q_stride, seqs, o, scratch, err, s, n_launched);
+  if (nb <= 16) return launch<D, FP8, 16>(d, tm, q, q_stride, seqs, o, scratch, err, s, n_launched);
   if constexpr (!FP8)
-    if (nb > 32) return launch<D, FP8, 64>(d, tm, q, q_stride, seqs, o, scratch, err, s);
-  return launch<D, FP8, 32>(d, tm, q, q_stride, seqs, o, scratch, err, s);
+    if (nb > 32) return launch<D, FP8, 64>(d, tm, q, q_stride, seqs, o, scratch, err, s, n_launched);
+  return launch<D, FP8, 32>(d, tm, q, q_stride, seqs, o, scratch, err, s, n_launched);
 }
 
 }  // namespace pd
@@ -603,12 +611,12 @@ cudaError_t launch_nb(int nb, const PoolDims& d, const CUtensorMap* tm, const __
 
 cudaError_t launch_pool_decode(const PoolDims& d, const CUtensorMap* tm, const __nv_bfloat16* q, long long q_stride,
                                const PoolSeqs& seqs, const PoolAttnOut& o, int nb, void* scratch, unsigned* err,
-                               cudaStream_t s) {
+                               cudaStream_t s, int* n_launched) {
   if (d.d == 128)
-    return d.fp8 ? pd::launch_nb<128, true>(nb, d, tm, q, q_stride, seqs, o, scratch, err, s)
-                 : pd::launch_nb<128, false>(nb, d, tm, q, q_stride, seqs, o, scratch, err, s);
-  return d.fp8 ? pd::launch_nb<64, true>(nb, d, tm, q, q_stride, seqs, o, scratch, err, s)
-               : pd::launch_nb<64, false>(nb, d, tm, q, q_stride, seqs, o, scratch, err, s);
+    return d.fp8 ? pd::launch_nb<128, true>(nb, d, tm, q, q_stride, seqs, o, scratch, err, s, n_launched)
+                 : pd::launch_nb<128, false>(nb, d, tm, q, q_stride, seqs, o, scratch, err, s, n_launched);
+  return d.fp8 ? pd::launch_nb<64, true>(nb, d, tm, q, q_stride, seqs, o, scratch, err, s, n_launched)
+               : pd::launch_nb<64, false>(nb, d, tm, q, q_stride, seqs, o, scratch, err, s, n_launched);
 }
 
 }  // namespace kvs

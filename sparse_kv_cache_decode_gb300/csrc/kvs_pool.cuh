@@ -95,7 +95,7 @@ cudaError_t launch_pool_attn(const PoolDims& d, const unsigned char* k, const un
 // 32 with E4M3 pools).
 cudaError_t launch_pool_decode(const PoolDims& d, const CUtensorMap* tm, const __nv_bfloat16* q, long long q_stride,
                                const PoolSeqs& seqs, const PoolAttnOut& o, int nb, void* scratch, unsigned* err,
-                               cudaStream_t s);
+                               cudaStream_t s, int* n_launched);
 size_t pool_weight_scratch_bytes();
 cudaError_t launch_pool_weight(const PoolDims& d, const CUtensorMap* tm, const __nv_bfloat16* q, long long q_stride,
                                const PoolSeqs& seqs, const float* lse2, float* weight, void* scratch, unsigned* err,
