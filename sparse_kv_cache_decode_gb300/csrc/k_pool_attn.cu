@@ -1,7 +1,8 @@
 // Device-resident pools: attention of ragged query rows over paged K/V on the 5th-generation tensor cores.
 //
 // Rows.  The rows of a (sequence, kv head) are its query tokens times the group's G heads, row = token * G + g,
-// so one K/V tile serves a whole group.  An item is a block of 128 * QT such rows; the keys its rows see are
+// so one K/V tile serves a whole group.  A row tile holds the heads of 128 / G whole tokens, an item up to two of
+// them; the keys its rows see are
 // visited in tiles of 128 tokens: the tiles of the first n_sink tokens, then those of the window's span.
 //   S = Q K^T (128 x 128, fp32 in tensor memory),  P = 2^(S scale log2 e - m) in bf16 over S's columns,
 //   O (128 x d, fp32 in tensor memory) += P V,      out = v_scale O / l,  l = sum of P before its rounding.
@@ -10,8 +11,8 @@
 // passes 2^40 (a logit some 23 above the first tile's largest).  P is rounded to bf16 (relative error 2^-9 on average of both signs, as the output's own rounding); S, m, l
 // and O are fp32.
 //
-// Two softmax groups of 4 warps, one thread per row.  Where an item has more than 128 rows each group takes
-// 128 of them and both read every K/V tile; where it has at most 128 the groups take the tiles in turn over
+// Two softmax groups of 4 warps, one thread per row.  Where an item has two row tiles each group takes
+// one of them and both read every K/V tile; where it has one the groups take the tiles in turn over
 // the same rows, and their states are joined at the end.  Either way one group's products run while the other
 // computes its exponentials.
 //
@@ -21,7 +22,7 @@
 // Lengths, offsets and tables are read on the device: each CTA derives the sequence and its range from them.
 //
 // Roles: warp 0 brings K/V tiles with tensor loads, one per block and 64 dims, skipping blocks that no row of the
-// item sees; warp 1 issues the products; warps 2-3 load Q; warps 4-11 are the softmax groups; with E4M3 pools
+// item sees; warp 1 issues the products; warp 2 brings Q; warps 4-11 are the softmax groups; with E4M3 pools
 // warps 12-15 widen the codes to bf16 tiles (every E4M3 value is exact in bf16).
 // Value rows that no row of the item sees are zeroed in shared memory before their product: they may hold
 // anything, and 0 * NaN would reach every row.  All waits are bounded (KVS_ERR_TIMEOUT).
@@ -37,14 +38,11 @@ namespace pa {
 
 using namespace pdev;
 
-template <int D, bool FP8, int QT>
+template <int D, bool FP8>
 struct Cfg {
   static constexpr int CHUNKS = D / 64;                       // 64-dim (128-byte) chunks of a bf16 row
-  // Q: QT tiles of 128 rows; with one tile half a tile more, so that the next item's Q (at most 64 rows) can
-  // be brought to the half the current one leaves free (rows past an item's last are never used)
-  static constexpr int QROWS = QT == 1 ? 192 : 256;
-  static constexpr int QHALF = QT == 1 ? 64 : 128;
-  static constexpr int QCHUNK = QROWS * 128;
+  // Q: two row tiles, of one item or (up to one row tile each) of two items in turn
+  static constexpr int QCHUNK = 256 * 128;
   static constexpr int QBYTES = CHUNKS * QCHUNK;
   static constexpr int TILE = TOK * D * 2;                    // one bf16 K or V tile
   static constexpr int CODES = TOK * D;                       // one tile of E4M3 codes
@@ -57,13 +55,15 @@ struct Cfg {
   // registers of the helper and the softmax warps (the groups of 128 threads share the launch's registers)
   static constexpr int REGS_LOW = 72, REGS_HIGH = FP8 ? 184 : 216;
   static_assert(FP8 ? 2 * REGS_LOW + 2 * REGS_HIGH <= 4 * 128 : REGS_LOW + 2 * REGS_HIGH <= 3 * 168, "register plan");
-  static constexpr int RB = TOK * QT;
   static constexpr int OFF_RING = QBYTES;
   static constexpr int OFF_STG = OFF_RING + STAGES * TILE;
   static constexpr int OFF_ML = OFF_STG + STAGING * CODES;
   static constexpr int OFF_BAR = OFF_ML + 2048;
   static constexpr int OFF_PIECES = OFF_BAR + 512;
-  static constexpr int OFF_TAB = OFF_PIECES + kPieces * 64;
+  // room for 32 rows of 64 bytes a softmax warp, through which outputs are written row by row (d = 128 with E4M3 pools has none)
+  static constexpr bool STAGE_OUT = ROOM - STAGING * CODES - STAGES * TILE >= 16384;
+  static constexpr int OFF_OUT = OFF_PIECES + kPieces * 64;
+  static constexpr int OFF_TAB = OFF_OUT + (STAGE_OUT ? 16384 : 0);
   static_assert(STAGES >= 3, "shared memory plan");
   static_assert(OFF_TAB + 4 * (kPoolMaxReq + 1) + 1024 <= MAX_SMEM, "shared memory plan");
 };
@@ -73,13 +73,14 @@ __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.a
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
 
-template <int D, bool FP8, int QT>
-__global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
-    pool_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, PoolDims d,
-                     const __nv_bfloat16* __restrict__ q, long long q_stride, PoolSeqs seqs, PoolAttnOut o,
-                     void* scratch, Split sp, unsigned* err) {
-  using C = Cfg<D, FP8, QT>;
-  constexpr int RB = C::RB, S = C::STAGES, NW = C::THREADS / 32;
+template <int D, bool FP8>
+__global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
+    pool_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ CUtensorMap tmQ, PoolDims d, PoolSeqs seqs, PoolAttnOut o, void* scratch,
+                     Split sp, unsigned* err) {
+  using C = Cfg<D, FP8>;
+  constexpr int S = C::STAGES;
+  const int RT = d.rt, RB = 2 * RT;     // rows of a row tile, of an item
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* ring = smem + C::OFF_RING;
@@ -120,8 +121,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
       mbar_init(&p_full[g], 4);
       mbar_init(&o_full[g], 1);
     }
-    mbar_init(&q_full[0], 2);
-    mbar_init(&q_full[1], 2);
+    mbar_init(&q_full[0], 1);
+    mbar_init(&q_full[1], 1);
     mbar_init(q_free, 1);
     mbar_init(drained, 1);
     *abort_flag = 0;
@@ -129,11 +130,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
     mbar_fence_init();
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmQ);
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   kvs_pdl_entry();
 
-  cta_range<RB, QT == 2, C::THREADS>(d, seqs, tab, reinterpret_cast<long long*>(ml), plan, sp, c, err);
+  cta_range<true, C::THREADS>(d, seqs, RB, tab, reinterpret_cast<long long*>(ml), plan, sp, c, err);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -141,14 +143,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
   const uint64_t timeout_ns = (uint64_t)d.timeout_us * 1000ull;
   const Scratch sc = scratch_of(scratch, sp.n_cta);
   auto wait = [&](uint64_t* bar, unsigned parity) { return bounded_wait(bar, parity, timeout_ns, abort_flag); };
-  if (warp == 0) plan_pieces<RB, QT == 2>(d, seqs, tab, plan, pieces, sp.n_cta, err);
+  if (warp == 0) plan_pieces<true>(d, seqs, RB, tab, plan, pieces, sp.n_cta, err);
   __syncthreads();
   // Between two lists of pieces (long calls only): every role is done with the old one.
   auto more = [&]() {
     const int l = plan[2];
     __syncthreads();
     if (l <= 0) return false;
-    if (warp == 0) plan_pieces<RB, QT == 2>(d, seqs, tab, plan, pieces, sp.n_cta, err);
+    if (warp == 0) plan_pieces<true>(d, seqs, RB, tab, plan, pieces, sp.n_cta, err);
     __syncthreads();
     return true;
   };
@@ -259,12 +261,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
       if (elect_one()) {
         for (int i = 0; i < cnt && ok; ++i, ++piece) {
           const int nrows = pieces[i].nrows, n = pieces[i].n;
-          qb = nrows <= C::QHALF ? qb ^ 1 : 0;
-          if (nrows > 128 || !mbar_try_wait(&q_full[piece & 1], (piece >> 1) & 1)) {
+          qb = nrows <= RT ? qb ^ 1 : 0;
+          if (nrows > RT || !mbar_try_wait(&q_full[piece & 1], (piece >> 1) & 1)) {
             flush();                       // while Q is on its way: what is due
             if (!ok || !wait(&q_full[piece & 1], (piece >> 1) & 1)) { ok = false; break; }
           }
-          if (QT == 2 && nrows > 128) {
+          if (nrows > RT) {
             int s = (2 * N) % S;
             unsigned par = ((2 * N) / S) & 1;          // slot and parity of the next tile to wait for
             auto next = [&]() {
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
               while ((g ? pend1 : pend0) >= 0 && ok) pv_due((older ? pend1 : pend0) >= 0 ? older : g);
               if (!ok || !wait(&kv_full[s], ((2 * tile) / S) & 1)) { ok = false; break; }
               tc_fence_after();
-              qk(g, s, qb * C::QHALF);
+              qk(g, s, qb * 128);
               tc_commit(&kv_empty[s]);
               if (x == n - 1) tc_commit(q_free);
               const int info = tile * 4 + (x + 2 >= n ? 2 : 0) + (x < 2 ? 1 : 0);
@@ -341,38 +343,39 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
     if (elect_one()) tc_commit(drained);
     mbar_wait(drained, 0, kDrainTimeoutNs);
     __syncwarp();
-  } else if (warp < 4) {
-    // ------------------------------------------------------------------ Q
-    // Two items of at most QHALF rows each use the two halves; otherwise Q waits for the last item's products.
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ Q: whole tokens, so one load per row tile and chunk
+    // Two items of at most one row tile each use the two places; otherwise Q waits for the last item's products.
     regs_dec<C::REGS_LOW>();
     int piece = 0, qb = 0, last_small = 1;
     bool ok = true;
     do {
       const int cnt = plan[3];
-      for (int i = 0; i < cnt && ok; ++i, ++piece) {
-        const Piece it = pieces[i];
-        const int small = it.nrows <= C::QHALF;
-        qb = small ? qb ^ 1 : 0;
-        const int behind = small && last_small ? piece - 2 : piece - 1;    // the piece that must be through
-        last_small = small;
-        ok = behind < 0 || __all_sync(0xffffffffu, wait(q_free, behind & 1));
-        if (!ok) break;
-        constexpr int VEC = D / 8;       // 16-byte vectors of a row
-        for (int x = tid - 64; x < it.nrows * VEC; x += 64) {
-          const int r = x / VEC, v = x - r * VEC, row = it.row0 + r;
-          const int tok = div_g(d, row), g = row - tok * d.G, at = r + qb * C::QHALF;
-          const __nv_bfloat16* src = q + (it.t0 + tok) * q_stride + (it.h * d.G + g) * D + v * 8;
-          unsigned char* dst = smem + (v >> 3) * C::QCHUNK + at * 128 + (((v & 7) ^ (at & 7)) << 4);
-          cp_async16(dst, src, 16);
+      if (elect_one()) {
+        for (int i = 0; i < cnt && ok; ++i, ++piece) {
+          const Piece& it = pieces[i];
+          const int small = it.nrows <= RT;
+          qb = small ? qb ^ 1 : 0;
+          const int behind = small && last_small ? piece - 2 : piece - 1;    // the piece that must be through
+          last_small = small;
+          ok = behind < 0 || wait(q_free, behind & 1);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&q_full[piece & 1], (unsigned)((small ? 1 : 2) * C::CHUNKS * RT * 128));
+          for (int x = 0; x < (small ? 1 : 2); ++x)
+#pragma unroll
+            for (int b = 0; b < C::CHUNKS; ++b)
+              tma_load_3d(smem + b * C::QCHUNK + (qb + x) * (128 * 128), &tmQ, b * 64, it.h * d.G,
+                          it.t0 + div_g(d, it.row0) + x * (RT / d.G), &q_full[piece & 1]);
         }
-        cp_async_commit();
-        cp_async_wait_all();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[piece & 1]);
+        // no load may still be on its way when the CTA exits
+        for (int i = max(0, piece - 2); i < piece; ++i) mbar_wait(&q_full[i & 1], (i >> 1) & 1, kDrainTimeoutNs);
       }
+      __syncwarp();
     } while (more());
-    cp_async_wait_all();
+  } else if (warp == 3) {
+    regs_dec<C::REGS_LOW>();
+    while (more()) {
+    }
   } else if (warp < 12) {
     // ------------------------------------------------------------------ softmax and output
     regs_inc<C::REGS_HIGH>();
@@ -387,14 +390,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
       for (int i = 0; i < cnt; ++i) {
         const Piece& it = pieces[i];
         const int n = it.n, nrows = it.nrows, j0 = it.j0;
-        const bool pair = nrows > 128;
-        const int r = pair ? g * 128 + lr : lr;                          // row of the item
-        const bool live = r < nrows;
+        const bool pair = nrows > RT;
+        const int r = pair ? g * RT + lr : lr;                           // row of the item
+        const bool live = lr < RT && r < nrows;
         const int row = it.row0 + r;
         // the keys this row sees, and those every row of this group sees
         int hi = live ? it.len : 0, lo = 0, first = 0, hi_all = it.len, lo_all = 0;
         if (seqs.causal) {
-          const int ra = it.row0 + (pair ? g * 128 : 0), rb = min(ra + 127, it.row0 + nrows - 1);
+          const int ra = it.row0 + (pair ? g * RT : 0), rb = min(ra + RT - 1, it.row0 + nrows - 1);
           const int p = it.p0 + div_g(d, row), pa = it.p0 + div_g(d, ra), pb = it.p0 + div_g(d, rb);
           hi = live ? max(0, p + 1) : 0;
           hi_all = max(0, pa + 1);
@@ -419,6 +422,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
             for (int w = 0; w < 4; ++w) {
               const int off = base + 32 * w;
               const uint32_t vis = bits_below(hi - off) & (~bits_below(lo - off) | bits_below(first - off));
+              if (__all_sync(0xffffffffu, vis == 0xffffffffu)) continue;
 #pragma unroll
               for (int i2 = 0; i2 < 32; ++i2)
                 if (!(vis & (1u << i2))) s[32 * w + i2] = -INFINITY;
@@ -529,6 +533,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
           RowOut ro = {0.f, 1.f, 0.f};
           if (whole && live) ro = row_out(o, has_prev, orow, m, l, d.v_scale);
           const bool has = l > 0.f;
+          const size_t to = whole ? orow : prow;             // this row's place among those written
+          const unsigned lives = __ballot_sync(0xffffffffu, live);
 #pragma unroll 1
           for (int c0 = ca; c0 < cb; c0 += 32) {
             float x[32];
@@ -541,31 +547,68 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QT>::THREADS, 1)
 #pragma unroll
               for (int i2 = 0; i2 < 32; ++i2) x[i2] += w1 > 0.f ? y[i2] * w1 : 0.f;
             }
-            if (!live) continue;
             if (whole) {
-              if (has_prev && ro.w_prev > 0.f) {       // the earlier call's row, all of it on its way at once
-                float4 z[8];
+              const bool prev = live && has_prev && ro.w_prev > 0.f;
+              float4 z[8];
 #pragma unroll
-                for (int i2 = 0; i2 < 8; ++i2) z[i2] = __ldg(reinterpret_cast<const float4*>(o.prev_out + orow * D + c0) + i2);
+              for (int i2 = 0; i2 < 8; ++i2)       // the earlier call's row, all of it on its way at once
+                z[i2] = prev ? __ldg(reinterpret_cast<const float4*>(o.prev_out + orow * D + c0) + i2) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int i2 = 0; i2 < 8; ++i2) {
-                  x[4 * i2] = (has ? x[4 * i2] * ro.w_new : 0.f) + ro.w_prev * z[i2].x;
-                  x[4 * i2 + 1] = (has ? x[4 * i2 + 1] * ro.w_new : 0.f) + ro.w_prev * z[i2].y;
-                  x[4 * i2 + 2] = (has ? x[4 * i2 + 2] * ro.w_new : 0.f) + ro.w_prev * z[i2].z;
-                  x[4 * i2 + 3] = (has ? x[4 * i2 + 3] * ro.w_new : 0.f) + ro.w_prev * z[i2].w;
-                }
-              } else {
-#pragma unroll
-                for (int i2 = 0; i2 < 32; ++i2) x[i2] = has ? x[i2] * ro.w_new : 0.f;
+              for (int i2 = 0; i2 < 8; ++i2) {
+                x[4 * i2] = (has ? x[4 * i2] * ro.w_new : 0.f) + ro.w_prev * z[i2].x;
+                x[4 * i2 + 1] = (has ? x[4 * i2 + 1] * ro.w_new : 0.f) + ro.w_prev * z[i2].y;
+                x[4 * i2 + 2] = (has ? x[4 * i2 + 2] * ro.w_new : 0.f) + ro.w_prev * z[i2].z;
+                x[4 * i2 + 3] = (has ? x[4 * i2 + 3] * ro.w_new : 0.f) + ro.w_prev * z[i2].w;
               }
+            } else if (!has) {
 #pragma unroll
-              for (int i2 = 0; i2 < 32; i2 += 4)
-                row_store4(o, orow * D + c0 + i2, make_float4(x[i2], x[i2 + 1], x[i2 + 2], x[i2 + 3]));
-            } else {
+              for (int i2 = 0; i2 < 32; ++i2) x[i2] = 0.f;
+            }
+            float* f32 = whole ? o.part_out : sc.o;
+            if constexpr (C::STAGE_OUT) {
+              // 64 bytes of each of the warp's 32 rows at a time: written by rows' threads, read back by four threads a row
+              unsigned char* st = smem + C::OFF_OUT + (warp - 4) * 2048;
 #pragma unroll
-              for (int i2 = 0; i2 < 32; i2 += 4)
-                *reinterpret_cast<float4*>(sc.o + prow * D + c0 + i2) =
-                    has ? make_float4(x[i2], x[i2 + 1], x[i2 + 2], x[i2 + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+              for (int half = 0; half < 2; ++half) {
+                if (!f32 && half) break;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  uint4 v;
+                  if (f32) {
+                    const int i2 = half * 16 + e * 4;
+                    v = make_uint4(__float_as_uint(x[i2]), __float_as_uint(x[i2 + 1]), __float_as_uint(x[i2 + 2]),
+                                   __float_as_uint(x[i2 + 3]));
+                  } else {
+                    v = make_uint4(pack_bf16x2(x[8 * e], x[8 * e + 1]), pack_bf16x2(x[8 * e + 2], x[8 * e + 3]),
+                                   pack_bf16x2(x[8 * e + 4], x[8 * e + 5]), pack_bf16x2(x[8 * e + 6], x[8 * e + 7]));
+                  }
+                  *reinterpret_cast<uint4*>(st + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) = v;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int rr = e * 8 + (lane >> 2), part = lane & 3;
+                  const uint4 v = *reinterpret_cast<const uint4*>(st + rr * 64 + ((part ^ ((rr >> 1) & 3)) << 4));
+                  const size_t at = (size_t)__shfl_sync(0xffffffffu, (unsigned long long)to, rr) * D + c0;
+                  if ((lives >> rr) & 1u) {
+                    if (f32) *reinterpret_cast<uint4*>(f32 + at + half * 16 + part * 4) = v;
+                    else *reinterpret_cast<uint4*>(o.out + at + part * 8) = v;
+                  }
+                }
+                __syncwarp();
+              }
+            } else if (live) {
+#pragma unroll
+              for (int i2 = 0; i2 < 32; i2 += 8) {
+                if (f32) {
+                  *reinterpret_cast<float4*>(f32 + to * D + c0 + i2) = make_float4(x[i2], x[i2 + 1], x[i2 + 2], x[i2 + 3]);
+                  *reinterpret_cast<float4*>(f32 + to * D + c0 + i2 + 4) = make_float4(x[i2 + 4], x[i2 + 5], x[i2 + 6], x[i2 + 7]);
+                } else {
+                  *reinterpret_cast<uint4*>(o.out + to * D + c0 + i2) =
+                      make_uint4(pack_bf16x2(x[i2], x[i2 + 1]), pack_bf16x2(x[i2 + 2], x[i2 + 3]),
+                                 pack_bf16x2(x[i2 + 4], x[i2 + 5]), pack_bf16x2(x[i2 + 6], x[i2 + 7]));
+                }
+              }
             }
           }
           if (live && (pair || g == 0)) {
@@ -701,22 +744,22 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   if (lane == 0) row_lse(o, orow, ro.lse2);
 }
 
-template <int D, bool FP8, int QT>
+template <int D, bool FP8>
 cudaError_t launch(const PoolDims& d, const CUtensorMap* tm, const __nv_bfloat16* q, long long q_stride,
                    const PoolSeqs& seqs, const PoolAttnOut& o, void* scratch, unsigned* err, cudaStream_t s) {
-  using C = Cfg<D, FP8, QT>;
-  auto kern = pool_attn_kernel<D, FP8, QT>;
-  const int smem = C::OFF_TAB + 4 * (seqs.n_seq + 1) + 1024;
+  using C = Cfg<D, FP8>;
+  auto kern = pool_attn_kernel<D, FP8>;
   cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), MAX_SMEM);
   if (e != cudaSuccess) return e;
-  Split sp;
-  sp.n_cta = device_sm_count();
-  sp.min_per = 2;
-  launch_pdl(kern, dim3(sp.n_cta), dim3(C::THREADS), smem, s, tm[0], tm[1], d, q, q_stride, seqs, o, scratch, sp, err);
+  CUtensorMap tmQ;
+  if (!make_pool_q_map(&tmQ, d, q, q_stride, seqs.n_tok)) return cudaErrorInvalidValue;
+  const Split sp = {device_sm_count(), 2};
+  launch_pdl(kern, dim3(sp.n_cta), dim3(C::THREADS), C::OFF_TAB + 4 * (seqs.n_seq + 1) + 1024, s, tm[0], tm[1], tmQ, d, seqs, o,
+             scratch, sp, err);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // an item has at most 128 * QT rows, and no more than the call has
-  return launch_pool_merge(d, o, scratch, sp.n_cta, (int)std::min<long long>(C::RB, (long long)seqs.n_tok * d.G), s);
+  // an item has at most two row tiles, and no more rows than the call
+  return launch_pool_merge(d, o, scratch, sp.n_cta, (int)std::min<long long>(2 * d.rt, (long long)seqs.n_tok * d.G), s);
 }
 
 }  // namespace pa
@@ -740,21 +783,14 @@ cudaError_t launch_pool_attn(const PoolDims& d, const unsigned char*, const unsi
                              void* scratch, unsigned* err, cudaStream_t s, int* n_launched) {
   using namespace pa;
   *n_launched = 2;
-  // rows per (sequence, head) on average: few take the products' column side, more than 128 pay for two row tiles per
-  // K/V tile
+  // rows per (sequence, head) on average: few take the products' column side
   const long long rows = ((long long)seqs.n_tok * d.G + seqs.n_seq - 1) / seqs.n_seq;
   if (rows <= (d.fp8 ? 32 : 64)) return launch_pool_decode(d, tm, q, q_stride, seqs, o, (int)rows, scratch, err, s, n_launched);
-  const bool two = (long long)seqs.n_tok * d.G > 128ll * seqs.n_seq;
-  if (d.d == 128) {
-    if (d.fp8) return two ? launch<128, true, 2>(d, tm, q, q_stride, seqs, o, scratch, err, s)
-                          : launch<128, true, 1>(d, tm, q, q_stride, seqs, o, scratch, err, s);
-    return two ? launch<128, false, 2>(d, tm, q, q_stride, seqs, o, scratch, err, s)
-               : launch<128, false, 1>(d, tm, q, q_stride, seqs, o, scratch, err, s);
-  }
-  if (d.fp8) return two ? launch<64, true, 2>(d, tm, q, q_stride, seqs, o, scratch, err, s)
-                        : launch<64, true, 1>(d, tm, q, q_stride, seqs, o, scratch, err, s);
-  return two ? launch<64, false, 2>(d, tm, q, q_stride, seqs, o, scratch, err, s)
-             : launch<64, false, 1>(d, tm, q, q_stride, seqs, o, scratch, err, s);
+  if (d.d == 128)
+    return d.fp8 ? launch<128, true>(d, tm, q, q_stride, seqs, o, scratch, err, s)
+                 : launch<128, false>(d, tm, q, q_stride, seqs, o, scratch, err, s);
+  return d.fp8 ? launch<64, true>(d, tm, q, q_stride, seqs, o, scratch, err, s)
+               : launch<64, false>(d, tm, q, q_stride, seqs, o, scratch, err, s);
 }
 
 }  // namespace kvs

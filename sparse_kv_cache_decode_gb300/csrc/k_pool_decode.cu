@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
   }
   if (warp == 1) tmem_alloc(tmem_slot, 256);
   kvs_pdl_entry();
-  cta_range<NB, false, C::THREADS>(d, seqs, tab, reinterpret_cast<long long*>(x_s), plan, sp, c, err);
+  cta_range<false, C::THREADS>(d, seqs, NB, tab, reinterpret_cast<long long*>(x_s), plan, sp, c, err);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -138,14 +138,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
   const uint64_t timeout_ns = (uint64_t)d.timeout_us * 1000ull;
   const Scratch sc = scratch_of(scratch, sp.n_cta);
   auto wait = [&](uint64_t* bar, unsigned parity) { return bounded_wait(bar, parity, timeout_ns, abort_flag); };
-  if (warp == 0) plan_pieces<NB, false>(d, seqs, tab, plan, pieces, sp.n_cta, err);
+  if (warp == 0) plan_pieces<false>(d, seqs, NB, tab, plan, pieces, sp.n_cta, err);
   __syncthreads();
   // Between two lists of pieces (long calls only): every role is done with the old one.
   auto more = [&]() {
     const int l = plan[2];
     __syncthreads();
     if (l <= 0) return false;
-    if (warp == 0) plan_pieces<NB, false>(d, seqs, tab, plan, pieces, sp.n_cta, err);
+    if (warp == 0) plan_pieces<false>(d, seqs, NB, tab, plan, pieces, sp.n_cta, err);
     __syncthreads();
     return true;
   };

@@ -16,7 +16,6 @@
 // Roles: warp 0 brings K tiles, warp 1 issues the products, warp 2 brings Q tiles (tensor loads), warp 3 their
 // log-sum-exps; warps 4-11 sum; with E4M3 pools warps 12-15 widen the codes.  Waits are bounded (KVS_ERR_TIMEOUT).
 #include <algorithm>
-#include <cudaTypedefs.h>
 
 #include "kvs_pool_dev.cuh"
 
@@ -102,14 +101,6 @@ __device__ __forceinline__ Piece item_at(const PoolDims& d, const PoolSeqs& q, c
   it.h = local - kp * d.Hkv;
   item_tiles(q, T, r, kp, it);
   return it;
-}
-
-__device__ __forceinline__ void tma_load_3d(void* dst, const void* tm, int x, int y, int z, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::
-          "r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
 }
 
 template <int D, bool FP8>
@@ -580,28 +571,6 @@ __global__ void __launch_bounds__(KEYS)
   *w = t >= r.len - (r.t1 - r.t0) ? sum : *w + sum;
 }
 
-// The query rows as [tokens][heads][64-dim boxes]: a box holds the group's G heads of T tokens.
-bool make_q_map(CUtensorMap* m, const PoolDims& d, const __nv_bfloat16* q, long long q_stride, int n_tok) {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-  if (!encode) {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess || !fn) {
-      cudaGetLastError();
-      return false;
-    }
-    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }
-  cuuint64_t dims[3] = {(cuuint64_t)d.d, (cuuint64_t)d.Hq, (cuuint64_t)n_tok};
-  cuuint64_t strides[2] = {(cuuint64_t)d.d * 2, (cuuint64_t)q_stride * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)d.G, (cuuint32_t)(TOK / d.G)};
-  cuuint32_t es[3] = {1, 1, 1};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(q), dims, strides, box, es,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, bool FP8>
 cudaError_t launch(const PoolDims& d, const CUtensorMap* tm, const CUtensorMap& tmQ, const PoolSeqs& seqs, const float* lse2,
                    float* weight, void* scratch, unsigned* err, cudaStream_t s) {
@@ -628,7 +597,7 @@ cudaError_t launch_pool_weight(const PoolDims& d, const CUtensorMap* tm, const _
                                cudaStream_t s, int* n_launched) {
   CUtensorMap tmQ;
   *n_launched = 0;
-  if (!pw::make_q_map(&tmQ, d, q, q_stride, seqs.n_tok)) return cudaErrorInvalidValue;
+  if (!make_pool_q_map(&tmQ, d, q, q_stride, seqs.n_tok)) return cudaErrorInvalidValue;
   *n_launched = 2;
   if (d.d == 128)
     return d.fp8 ? pw::launch<128, true>(d, tm, tmQ, seqs, lse2, weight, scratch, err, s)

@@ -213,6 +213,8 @@ cudaError_t launch_attention(const Dims& d, const Layer& L, const __nv_bfloat16*
                              const int* slot_of_sel, const int* nsel, const int* ctx_len, float* out,
                              cudaStream_t s);
 int attention_supported(const Dims& d);
+bool encode_tmap(CUtensorMap* m, void* base, int rank, const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                 int elem_bytes, bool swizzle);
 bool make_tmap_2d(CUtensorMap* m, void* base, uint64_t inner, uint64_t rows, uint32_t box_inner, uint32_t box_rows,
                   int elem_bytes = 2, bool swizzle = true);
 int score_tc_supported(const Dims& d, int nq);

@@ -50,6 +50,7 @@ bool pool_dims(const kvs_pool_config* c, PoolDims* d) {
   d->G = c->n_q_head / c->n_kv_head;
   d->d = c->head_dim;
   d->bs = c->block_size;
+  d->rt = 128 / d->G * d->G;
   d->g_magic = (unsigned)(((1ull << 32) + d->G - 1) / d->G);
   d->log2bs = 0;
   while ((1 << d->log2bs) < d->bs) ++d->log2bs;
@@ -102,6 +103,15 @@ bool query_ok(const kvs_pool* p, const void* q, long long q_stride, const int* c
 }
 
 }  // namespace
+
+namespace kvs {
+bool make_pool_q_map(CUtensorMap* m, const PoolDims& d, const __nv_bfloat16* q, long long q_stride, int n_tok) {
+  const uint64_t dims[3] = {(uint64_t)d.d, (uint64_t)d.Hq, (uint64_t)n_tok};
+  const uint64_t strides[2] = {(uint64_t)d.d * 2, (uint64_t)q_stride * 2};
+  const uint32_t box[3] = {64, (uint32_t)d.G, (uint32_t)(d.rt / d.G)};
+  return encode_tmap(m, const_cast<__nv_bfloat16*>(q), 3, dims, strides, box, 2, true);
+}
+}  // namespace kvs
 
 extern "C" {
 

@@ -10,6 +10,7 @@ constexpr int kPoolMaxReq = 2048;   // requests (or prefixes) per call
 struct PoolDims {
   int NL, n_slots;
   int Hq, Hkv, G, d, bs, log2bs;
+  int rt;                 // rows of a row tile: the heads of 128 / G whole query tokens
   unsigned g_magic;       // ceil(2^32 / G), for division by G (G > 1)
   int max_ctx, nb_max, max_req, max_tokens, max_prefix_tokens;
   int fp8, ebytes;
@@ -87,6 +88,8 @@ struct PoolAttnOut {
   const int* prev_req;  // prefix_req; its first and last entries bound the requests that have one
   int n_prev;
 };
+// The query rows as [tokens][heads][dims]; a box holds 64 dims of the group's G heads of 128 / G tokens.
+bool make_pool_q_map(CUtensorMap* m, const PoolDims& d, const __nv_bfloat16* q, long long q_stride, int n_tok);
 size_t pool_attn_scratch_bytes(const PoolDims& d);
 cudaError_t launch_pool_attn(const PoolDims& d, const unsigned char* k, const unsigned char* v, const CUtensorMap* tm,
                              const __nv_bfloat16* q, long long q_stride, const PoolSeqs& seqs, const PoolAttnOut& o,

@@ -55,6 +55,14 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tm, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::
+          "r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Zeroes, in a tile of 128-byte rows with `chunks` 64-dim chunks, those of the calling warp's 32 rows (from row0 on) whose bit
 // is set: 8 lanes a row, so that the stores of a step fill all banks.
 __device__ __forceinline__ void zero_rows(unsigned char* tile, int chunks, int row0, uint32_t rows) {

@@ -76,8 +76,7 @@ __device__ __forceinline__ void item_span(const PoolDims& d, const PoolSeqs& q, 
 }
 
 // Row block rb of a sequence: its rows and span.
-template <int RB>
-__device__ __forceinline__ void item_rows(const PoolDims& d, const PoolSeqs& q, const SeqInfo& r, int rb, Piece& it) {
+__device__ __forceinline__ void item_rows(const PoolDims& d, const PoolSeqs& q, const SeqInfo& r, int RB, int rb, Piece& it) {
   it.t0 = r.t0;
   it.len = r.len;
   it.p0 = r.len - (r.t1 - r.t0);
@@ -97,8 +96,7 @@ __device__ __forceinline__ int dealt(int p, int n_items, int n) {
 }
 
 // Item i: the sequences' items follow one another, row block by row block, head by head.
-template <int RB>
-__device__ __forceinline__ Piece item_at(const PoolDims& d, const PoolSeqs& q, const int* tab, int i, unsigned* err) {
+__device__ __forceinline__ Piece item_at(const PoolDims& d, const PoolSeqs& q, const int* tab, int RB, int i, unsigned* err) {
   // the last sequence with tab[s] <= i (empty sequences hold no items, so it is the one that does)
   int lo = 0, hi = q.n_seq;
   while (hi - lo > 1) {
@@ -110,7 +108,7 @@ __device__ __forceinline__ Piece item_at(const PoolDims& d, const PoolSeqs& q, c
   const SeqInfo r = pool_seq(d, q, lo, err);
   const int local = i - tab[lo], rb = local / d.Hkv;
   it.h = local - rb * d.Hkv;
-  item_rows<RB>(d, q, r, rb, it);
+  item_rows(d, q, r, RB, rb, it);
   return it;
 }
 
@@ -146,17 +144,11 @@ __device__ __forceinline__ void row_lse(const PoolAttnOut& o, size_t row, float 
   if (o.lse) o.lse[row] = lse2 * kLn2;
   if (o.lse2) o.lse2[row] = lse2;
 }
-// 4 columns of a finished row at element e of the output arrays
-__device__ __forceinline__ void row_store4(const PoolAttnOut& o, size_t e, float4 y) {
-  if (o.part_out) *reinterpret_cast<float4*>(o.part_out + e) = y;
-  else *reinterpret_cast<uint2*>(o.out + e) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-}
-
 // The CTA's range of the call's tiles: tab[s] = items before sequence s; plan[0..2] = its first item (position), that
 // item's first tile, its tiles; plan[4] = items, plan[5] = tiles per CTA.  DEALT: the tiles in the order of dealt().
 // Every thread of the CTA calls it; the caller synchronises behind it.  ws: 64 words of shared memory.
-template <int RB, bool DEALT, int THREADS>
-__device__ __forceinline__ void cta_range(const PoolDims& d, const PoolSeqs& seqs, int* tab, long long* ws, volatile int* plan,
+template <bool DEALT, int THREADS>
+__device__ __forceinline__ void cta_range(const PoolDims& d, const PoolSeqs& seqs, int RB, int* tab, long long* ws, volatile int* plan,
                                           const Split& sp, int c, unsigned* err) {
   constexpr int NW = THREADS / 32;
   const int tid = threadIdx.x;
@@ -166,13 +158,13 @@ __device__ __forceinline__ void cta_range(const PoolDims& d, const PoolSeqs& seq
   // items and, in the order of sequences, tiles of a sequence
   auto seq_work = [&](int s, int* items) {
     q1 = pool_seq(d, seqs, s, err);
-    const int n_rb = (int)(((long long)(q1.t1 - q1.t0) * d.G + RB - 1) / RB);
+    const int n_rb = ((q1.t1 - q1.t0) * d.G + RB - 1) / RB;
     *items = n_rb * d.Hkv;
     long long v = 0;
     if (!DEALT)
       for (int rb = 0; rb < n_rb; ++rb) {
         Piece it;
-        item_rows<RB>(d, seqs, q1, rb, it);
+        item_rows(d, seqs, q1, RB, rb, it);
         v += it.nt;
       }
     return v * d.Hkv;
@@ -204,7 +196,7 @@ __device__ __forceinline__ void cta_range(const PoolDims& d, const PoolSeqs& seq
     i0 = min(n_items, tid * per_i);
     i1 = min(n_items, i0 + per_i);
     tiles = 0;
-    for (int p = i0; p < i1; ++p) tiles += item_at<RB>(d, seqs, tab, dealt(p, n_items, sp.n_cta), err).nt;
+    for (int p = i0; p < i1; ++p) tiles += item_at(d, seqs, tab, RB, dealt(p, n_items, sp.n_cta), err).nt;
     r = block_scan(0, tiles, ws, NW);
   }
   const long long per = max((long long)sp.min_per, div_ll(r.v_all + sp.n_cta - 1, sp.n_cta));
@@ -213,8 +205,8 @@ __device__ __forceinline__ void cta_range(const PoolDims& d, const PoolSeqs& seq
     long long f = r.v;
     int p = -1, j = 0;
     if (DEALT) {
-      for (p = i0; p < i1; ++p) {
-        const int nt = item_at<RB>(d, seqs, tab, dealt(p, n_items, sp.n_cta), err).nt;
+      for (p = i0; p + 1 < i1; ++p) {
+        const int nt = item_at(d, seqs, tab, RB, dealt(p, n_items, sp.n_cta), err).nt;
         if (f0 < f + nt) break;
         f += nt;
       }
@@ -228,7 +220,7 @@ __device__ __forceinline__ void cta_range(const PoolDims& d, const PoolSeqs& seq
         }
         for (int rb = 0; p < 0; ++rb) {
           Piece it;
-          item_rows<RB>(d, seqs, q1, rb, it);
+          item_rows(d, seqs, q1, RB, rb, it);
           const long long w = (long long)it.nt * d.Hkv;
           if (f0 < f + w) {
             const int h = (int)div_ll(f0 - f, it.nt);
@@ -250,8 +242,8 @@ __device__ __forceinline__ void cta_range(const PoolDims& d, const PoolSeqs& seq
 }
 
 // Plans the CTA's next kPieces pieces (one warp, a lane per piece): pieces[0 .. plan[3]); plan[2] = tiles left.
-template <int RB, bool DEALT>
-__device__ __forceinline__ void plan_pieces(const PoolDims& d, const PoolSeqs& seqs, const int* tab, volatile int* plan,
+template <bool DEALT>
+__device__ __forceinline__ void plan_pieces(const PoolDims& d, const PoolSeqs& seqs, int RB, const int* tab, volatile int* plan,
                                             Piece* pieces, int n_cta, unsigned* err) {
   const int lane = threadIdx.x & 31;
   int pos = plan[0], j0 = plan[1], left = plan[2], cnt = 0;
@@ -259,7 +251,7 @@ __device__ __forceinline__ void plan_pieces(const PoolDims& d, const PoolSeqs& s
   for (int x = 0; x < kPieces && left > 0; x += 32) {
     Piece it;
     it.nt = 0;
-    if (pos + lane < n_items) it = item_at<RB>(d, seqs, tab, DEALT ? dealt(pos + lane, n_items, n_cta) : pos + lane, err);
+    if (pos + lane < n_items) it = item_at(d, seqs, tab, RB, DEALT ? dealt(pos + lane, n_items, n_cta) : pos + lane, err);
     it.j0 = lane == 0 ? j0 : 0;
     const long long w = it.nt - it.j0;
     long long incl = w;
