@@ -436,9 +436,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             }
           }
           const uint64_t sl22 = pack2(sl2, sl2);
-          bool fix = m == -INFINITY;       // this row's m has to be set from the tile's maximum
+          // this row's m has to be set from the tile's maximum (lanes without a row hold whatever Q's place held: never)
+          bool fix = live && m == -INFINITY;
 #pragma unroll 1
-          for (;;) {
+          for (int pass = 0;; ++pass) {          // twice at most
             if (__any_sync(0xffffffffu, fix)) {
               float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -485,9 +486,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             }
             float a, b;
             unpack2(add2(ps0, ps1), a, b);
-            // a row whose weights grew past the limit: set m anew and do the tile again (once: m is its maximum then)
-            fix = a + b > kMaxSum && !fix;
-            if (!__any_sync(0xffffffffu, fix)) {
+            // a row whose weights grew past the limit: set m anew and do the tile again (m is its maximum then)
+            fix = live && a + b > kMaxSum;
+            if (pass > 0 || !__any_sync(0xffffffffu, fix)) {
               l += a + b;
               break;
             }

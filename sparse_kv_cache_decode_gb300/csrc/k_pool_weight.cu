@@ -409,11 +409,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int row = e * 32 + lane;
-            v[e] = INFINITY;                       // a row that is not there weighs nothing
+            v[e] = -INFINITY;                      // (negated) a row that is not there weighs nothing
             if (row < nr) {
-              const int tok = row / d.G;
-              v[e] = lse2[(size_t)(it.t0 + tok0 + tok) * d.Hq + it.h * d.G + row - tok * d.G];
-              if (v[e] == -INFINITY) v[e] = INFINITY;   // a row that sees no key
+              const int tok = div_g(d, row);
+              v[e] = -lse2[(size_t)(it.t0 + tok0 + tok) * d.Hq + it.h * d.G + row - tok * d.G];
+              if (v[e] == INFINITY) v[e] = -INFINITY;   // nor does one that sees no key
             }
           }
           ok = J < LSE_STAGES || __all_sync(0xffffffffu, wait(&l_empty[s], ((J / LSE_STAGES) & 1) ^ 1));
@@ -436,50 +436,58 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     do {
       const int cnt = plan[3];
       for (int i = 0; i < cnt; ++i) {
-        const Piece& it = pieces[i];
+        const Piece it = pieces[i];
         const int n = it.n, k0 = it.k0 + g * TOK, t = k0 + lr, len = it.len, p0 = it.p0;
         const bool act = k0 < len;               // the group's tile holds keys
         const int k1 = min(len, k0 + TOK) - 1;   // its last key
+        const bool far = seqs.window && k1 >= seqs.n_sink;       // the window hides its keys from rows far behind them
         float sum = 0.f, low = 0.f;
-        for (int j = 0; j < n; ++j, ++J) {
+        int tok0 = (it.rt0 + it.j0) * T;
+        for (int j = 0; j < n; ++j, ++J, tok0 += T) {
           const int ls = J % LSE_STAGES;
+          wait(&l_full[ls], (J / LSE_STAGES) & 1);
           if (act) {
             const int b = ops & 1;
-            const int tok0 = (it.rt0 + it.j0 + j) * T, nr = min(T, it.R - tok0) * d.G;
-            const int pa = p0 + tok0, pb = pa + nr / d.G - 1;        // positions of the tile's first and last token
-            const bool whole = k1 <= pa && (!seqs.window || pb - k0 < seqs.window || k1 < seqs.n_sink) && nr == rows;
+            const int n_tok = min(T, it.R - tok0), nr = n_tok * d.G;
+            const int pa = p0 + tok0, pb = pa + n_tok - 1;           // positions of the tile's first and last token
+            const bool whole = k1 <= pa && n_tok == T && !(far && pb - k0 >= seqs.window);
             // the columns this key is seen by: rows from its own position on, to the window's end
             int ca = 0, cb = nr;
             if (!whole) {
-              ca = t > pa ? (int)min((long long)nr, (long long)(t - pa) * d.G) : 0;
-              if (seqs.window && t >= seqs.n_sink)
-                cb = (int)max(0ll, min((long long)nr, ((long long)t + seqs.window - pa) * d.G));
+              if (t > pa) ca = min(t - pa, T) * d.G;
+              if (seqs.window && t >= seqs.n_sink) cb = min(cb, min(max(t - pa + seqs.window, 0), T) * d.G);
               if (t >= len) cb = 0;
             }
-            wait(&l_full[ls], (J / LSE_STAGES) & 1);
             wait(&s_full[g * 2 + b], (ops >> 1) & 1);
             tc_fence_after();
             uint64_t a0 = 0, a1 = 0;
-#pragma unroll 1
-            for (int c0 = 0; c0 < nr; c0 += 32) {
+            const uint32_t ts = trow + b * 128;
+            const float4* lv = reinterpret_cast<const float4*>(lse_s + ls * TOK);
+            auto chunk = [&](int c0, bool part) {        // 32 columns
               float x[32];
-              tmem_ld32(trow + b * 128 + c0, x);
-              if (!(whole && c0 + 32 <= nr)) {
+              tmem_ld32(ts + c0, x);
+              if (part) {
                 const uint32_t vis = bits_below(cb - c0) & ~bits_below(ca - c0);
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
                   if (!(vis & (1u << e))) x[e] = -INFINITY;
               }
-              const float4* lv = reinterpret_cast<const float4*>(lse_s + ls * TOK + c0);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float4 z = lv[e];
+                const float4 z = lv[c0 / 4 + e];
                 float p, q2;
-                unpack2(fma2(pack2(x[4 * e], x[4 * e + 1]), sl22, pack2(-z.x, -z.y)), p, q2);
+                unpack2(fma2(pack2(x[4 * e], x[4 * e + 1]), sl22, pack2(z.x, z.y)), p, q2);
                 a0 = add2(a0, pack2(ex2(p), ex2(q2)));
-                unpack2(fma2(pack2(x[4 * e + 2], x[4 * e + 3]), sl22, pack2(-z.z, -z.w)), p, q2);
+                unpack2(fma2(pack2(x[4 * e + 2], x[4 * e + 3]), sl22, pack2(z.z, z.w)), p, q2);
                 a1 = add2(a1, pack2(ex2(p), ex2(q2)));
               }
+            };
+            if (whole && rows == TOK) {
+#pragma unroll
+              for (int c0 = 0; c0 < TOK; c0 += 32) chunk(c0, false);
+            } else {
+#pragma unroll 1
+              for (int c0 = 0; c0 < nr; c0 += 32) chunk(c0, true);
             }
             tc_fence_before();
             __syncwarp();
@@ -491,8 +499,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             const float v = x + y, nsum = __fadd_rn(sum, v), bv = __fsub_rn(nsum, sum);
             low = __fadd_rn(low, __fadd_rn(__fsub_rn(sum, __fsub_rn(nsum, bv)), __fsub_rn(v, bv)));
             sum = nsum;
-          } else {
-            wait(&l_full[ls], (J / LSE_STAGES) & 1);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&l_empty[ls]);

@@ -11,6 +11,8 @@ constexpr int TOK = 128;                      // tokens per K/V tile
 constexpr int MAX_SMEM = 227 * 1024;
 constexpr int kPieces = 64;                   // pieces of work a CTA plans at a time
 
+// n / G (n < 2^25)
+__device__ __forceinline__ int div_g(const PoolDims& d, int n) { return d.G == 1 ? n : (int)__umulhi((unsigned)n, d.g_magic); }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

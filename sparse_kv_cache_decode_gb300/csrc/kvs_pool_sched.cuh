@@ -39,8 +39,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
-// n / G (n < 2^25)
-__device__ __forceinline__ int div_g(const PoolDims& d, int n) { return d.G == 1 ? n : (int)__umulhi((unsigned)n, d.g_magic); }
 // a / b, in 32 bits where they do
 __device__ __forceinline__ long long div_ll(long long a, long long b) {
   return ((a | b) >> 31) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;

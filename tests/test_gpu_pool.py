@@ -66,6 +66,50 @@ def test_many_tiles_per_sm(m, d, kv):
 
 HEADS = [(8, 2, 128), (4, 4, 64), (12, 4, 128), (7, 1, 64), (16, 2, 64), (32, 2, 128)]
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("m,g", [(1, 4), (5, 3), (30, 4), (200, 3), (300, 4)])
+@pytest.mark.parametrize("shape", ["rising", "step", "falling"])
+def test_logits_that_outgrow_the_first_tile(shape, m, g, kv):
+    """Logits that rise (or fall) by hundreds over the context, smoothly or in one key: what a kernel takes for the
+    maximum of a row early on is passed by far later, and a weight of the first keys vanishes.  The queries have a
+    common component of 2, the keys one that moves from -2 to 2.5 (a logit moves by 4.5 * 2 * sqrt(d) = 102)."""
+    n, d = 900, 128
+    move = {"rising": lambda t: -2 + 4.5 * t / n, "step": lambda t: np.where(t == 700, 2.5, -2.0), "falling": lambda t: 2.5 - 4.5 * t / n}
+    c = PoolCase(m + g, [n, 400], [m, 1], 2 * g, 2, d, 32, kv, key_shift=move[shape], q_shift=2.0, heavy=0.0).cuda()
+    out, lse = c.out()
+    c.pool.attn(0, c.d_q, c.d_cu, c.d_ctx, c.d_table, out, lse=lse)
+    torch.cuda.synchronize()
+    assert c.pool.poll_error() == 0
+    got, lse = out.double().cpu().numpy(), lse.cpu().numpy()
+    for r in range(2):
+        ref, ref_lse, mag, _ = pool_attend(c.query(r), *c.rows[r], c.softmax_scale)
+        a, b = c.cu[r], c.cu[r + 1]
+        check_out(got[a:b], lse[a:b], ref, ref_lse, mag, d, f"request {r}", S=200)
+
+
+@pytest.mark.parametrize("m", [1, 3, 100, 700])
+def test_lanes_without_a_row(m):
+    """Groups of 3 and 7 heads leave places of a row tile empty, and what an earlier call left in them may be
+    anything: here the largest queries there are.  Results and running time do not depend on it."""
+    for g in (3, 7):
+        big = PoolCase(1, [700, 64], [700, 64], 8, 2, 128, 64).cuda()
+        big.d_q.copy_(torch.where(big.d_q > 0, 3e38, -3e38))
+        out, _ = big.out()
+        big.pool.attn(0, big.d_q, big.d_cu, big.d_ctx, big.d_table, out)
+        c = PoolCase(m + g, [900, 300], [m, 1], g, 1, 128, 64).cuda()
+        got, lse, _ = run_attn(c)
+        check_attn(c, got, lse)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_prompt_ranges(d, kv):
+    """Items of two row tiles, a dozen tiles and more of K and V per SM."""
+    c = PoolCase(d, [3000, 2500], [3000, 1200], 12, 4, d, 64, kv).cuda()
+    got, lse, _ = run_attn(c, 1500, 5)
+    check_attn(c, got, lse, 1500, 5)
+
+
 SINGLE = [  # contexts, window, sink, block size
     ([1], 0, 0, 16), ([0, 5, 0], 0, 0, 16), ([1, 15, 16, 17], 0, 0, 16), ([127, 128, 129, 130], 0, 0, 32), ([700], 0, 0, 128),
     ([700, 333], 100, 0, 16), ([700, 333, 90], 100, 4, 64), ([1000], 1, 0, 16), ([1000], 1, 1, 128), ([513], 128, 130, 32),
