@@ -130,16 +130,30 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
   }
   if (warp == 1) tmem_alloc(tmem_slot, 256);
   kvs_pdl_entry();
-  cta_range<false, C::THREADS>(d, seqs, NB, tab, reinterpret_cast<long long*>(x_s), plan, sp, c, err);
-  tc_fence_before();
-  __syncthreads();
+  volatile int* few = reinterpret_cast<volatile int*>(tmem_slot + 10);      // warp 0 has planned alone
+  if (seqs.n_seq <= 32) {
+    if (warp == 0) {
+      const bool done = plan_few(d, seqs, NB, tab, plan, pieces, sp, c, err);
+      if (lane == 0) *few = done;
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
+  const bool planned = seqs.n_seq <= 32 && *few;
+  if (!planned) {
+    cta_range<false, C::THREADS>(d, seqs, NB, tab, reinterpret_cast<long long*>(x_s), plan, sp, c, err);
+    tc_fence_before();
+    __syncthreads();
+  }
   tc_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
   const uint64_t timeout_ns = (uint64_t)d.timeout_us * 1000ull;
   const Scratch sc = scratch_of(scratch, sp.n_cta);
   auto wait = [&](uint64_t* bar, unsigned parity) { return bounded_wait(bar, parity, timeout_ns, abort_flag); };
-  if (warp == 0) plan_pieces<false>(d, seqs, NB, tab, plan, pieces, sp.n_cta, err);
-  __syncthreads();
+  if (!planned) {
+    if (warp == 0) plan_pieces<false>(d, seqs, NB, tab, plan, pieces, sp.n_cta, err);
+    __syncthreads();
+  }
   // Between two lists of pieces (long calls only): every role is done with the old one.
   auto more = [&]() {
     const int l = plan[2];

@@ -276,6 +276,73 @@ __device__ __forceinline__ void plan_pieces(const PoolDims& d, const PoolSeqs& s
   }
 }
 
+// The range and the first pieces of a CTA in one warp, for at most 32 sequences of at most RB rows each (a lane per sequence,
+// then a lane per piece); false where there are more rows, and nothing is planned.  (The general way through the block
+// took 3 us of a 9 us call.)
+__device__ __forceinline__ bool plan_few(const PoolDims& d, const PoolSeqs& seqs, int RB, int* tab, volatile int* plan,
+                                         Piece* pieces, const Split& sp, int c, unsigned* err) {
+  const int lane = threadIdx.x & 31;
+  SeqInfo q = {0, 0, 0};
+  if (lane < seqs.n_seq) q = pool_seq(d, seqs, lane, err);
+  const int R = (q.t1 - q.t0) * d.G;
+  Piece it;
+  item_rows(d, seqs, q, RB, 0, it);
+  const int nt = R > 0 ? it.nt : 0;
+  // tiles in 32 bits
+  if (__any_sync(0xffffffffu, R > RB || (long long)nt * d.Hkv > (1 << 25))) return false;
+  int incl = nt * d.Hkv;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  const unsigned some = __ballot_sync(0xffffffffu, nt > 0);
+  const int before = __popc(some & ((1u << lane) - 1)) * d.Hkv;      // items before this lane's sequence
+  if (lane < seqs.n_seq) tab[lane] = before;
+  const int total = __shfl_sync(0xffffffffu, incl, 31), n_items = __popc(some) * d.Hkv;
+  const int per = max(sp.min_per, (total + sp.n_cta - 1) / sp.n_cta);
+  const int f0 = per * c, f1 = min(total, f0 + per);
+  const unsigned at = __ballot_sync(0xffffffffu, f0 < f1 && f0 < incl);
+  int cnt = 0, left = max(0, f1 - f0), pos = 0;
+  if (at) {
+    const int s0 = __ffs(at) - 1;
+    const int off = f0 - __shfl_sync(0xffffffffu, incl - nt * d.Hkv, s0), nt0 = __shfl_sync(0xffffffffu, nt, s0);
+    const int h0 = off / nt0, j0 = off - h0 * nt0;
+    pos = __shfl_sync(0xffffffffu, before, s0) + h0;
+    // piece `lane`: item pos + lane
+    const int item = pos + lane, rank = item / d.Hkv;
+    const int s = item < n_items ? (int)__fns(some, 0, rank + 1) : 0;
+    const SeqInfo r = {__shfl_sync(0xffffffffu, q.t0, s), __shfl_sync(0xffffffffu, q.t1, s), __shfl_sync(0xffffffffu, q.len, s)};
+    item_rows(d, seqs, r, RB, 0, it);
+    it.s = s;
+    it.h = item - rank * d.Hkv;
+    it.j0 = lane == 0 ? j0 : 0;
+    const int w = item < n_items ? it.nt - it.j0 : 0;
+    int sum = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    it.n = max(0, min(w, left - (sum - w)));
+    if (it.n > 0) pieces[lane] = it;
+    cnt = __popc(__ballot_sync(0xffffffffu, it.n > 0));
+    left = max(0, left - __shfl_sync(0xffffffffu, sum, 31));
+    pos += cnt;
+  }
+  __syncwarp();
+  if (lane == 0) {
+    tab[seqs.n_seq] = n_items;
+    plan[0] = pos;
+    plan[1] = 0;
+    plan[2] = pos < n_items ? left : 0;
+    plan[3] = cnt;
+    plan[4] = n_items;
+    plan[5] = per;
+  }
+  return true;
+}
+
 }  // namespace pdev
 
 // The merge kernel behind an attention kernel: items of at most `rows` rows.
