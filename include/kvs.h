@@ -393,7 +393,7 @@ typedef struct kvs_pool kvs_pool;
 /* Device bytes the workspace of `cfg` needs (0 when cfg is invalid or not supported). */
 size_t kvs_pool_workspace_bytes(const kvs_pool_config* cfg);
 
-/* Bind a pool to its K/V memory (256-byte aligned device pointers, both of n_layer * n_slots * H_kv *
+/* Bind a pool to its K/V memory (256-byte aligned device pointers, apart, both of n_layer * n_slots * H_kv *
  * block_size * head_dim elements; never written but by kvs_pool_append and kvs_pool_evict) and to a
  * workspace (>= kvs_pool_workspace_bytes, 256-byte aligned).  Synchronous; on the current device. */
 kvs_status kvs_pool_create(const kvs_pool_config* cfg, void* d_k, void* d_v, void* d_workspace,
@@ -419,7 +419,7 @@ kvs_status kvs_pool_append(kvs_pool* pool, int layer, const void* d_k_new, const
  * d_lse may be NULL.  d_weight (may be NULL) accumulates the softmax weight of each key over the rows
  * and heads of the call: weight[r][h][t] of a key before the request's query tokens is added to, that
  * of the query tokens themselves (positions ctx_len - q_r and up) is set; entries >= ctx_len are left.
- * q_stride: a multiple of 8, >= H_q * d; d_q and d_out 16-byte aligned. */
+ * q_stride: a multiple of 8, >= H_q * d; d_q and d_out 16-byte aligned, not overlapping. */
 kvs_status kvs_pool_attn(kvs_pool* pool, int layer, const void* d_q, long long q_stride, const int* d_cu_q,
                          const int* d_ctx_len, const int* d_block2slot, int n_req, int n_tok, int window, int n_sink,
                          void* d_out, float* d_lse, float* d_weight, kvs_stream_t stream);
@@ -428,8 +428,8 @@ kvs_status kvs_pool_attn(kvs_pool* pool, int layer, const void* d_q, long long q
  * see all prefix_len[i] tokens of prefix i (its blocks in prefix2slot [n_prefix][nb_max], once in
  * the pool), then their own context causally as kvs_pool_attn without a window (ctx_len and positions
  * count a request's own tokens only).  Requests before prefix_req[0] or from prefix_req[n_prefix] on
- * have no prefix.  prefix_req [n_prefix + 1], ascending within [0, n_req]; n_prefix <= max_req; n_tok <=
- * max_prefix_tokens.  A prefix's K/V is read once for all its requests. */
+ * have no prefix.  prefix_req [n_prefix + 1], ascending within [0, n_req]; n_prefix <= max_req (0: no prefixes,
+ * their pointers may be NULL); n_tok <= max_prefix_tokens.  A prefix's K/V is read once for all its requests. */
 kvs_status kvs_pool_prefix_attn(kvs_pool* pool, int layer, const void* d_q, long long q_stride, const int* d_cu_q,
                                 const int* d_ctx_len, const int* d_block2slot, int n_req, int n_tok,
                                 const int* d_prefix_req, const int* d_prefix_len, const int* d_prefix2slot, int n_prefix,
@@ -440,7 +440,7 @@ kvs_status kvs_pool_prefix_attn(kvs_pool* pool, int layer, const void* d_q, long
  * the earlier token; NaN lowest), in their order, and gather their K/V rows into the blocks of
  * dst2slot [n_req][nb_max], which must be disjoint from every block the call reads.
  *   kept [n_req][H_kv][keep]   the kept tokens' indices, ascending (entries past n_kept are left)
- *   n_kept [n_req]             min(keep, ctx_len): the new context length
+ *   n_kept [n_req]             min(keep, ctx_len): the new context length (another buffer than ctx_len)
  *   weight_out [n_req][H_kv][max_ctx], another buffer than weight: the kept tokens' weights, in order
  * n_sink + n_recent <= keep <= max_ctx. */
 kvs_status kvs_pool_evict(kvs_pool* pool, int layer, const float* d_weight, const int* d_ctx_len,

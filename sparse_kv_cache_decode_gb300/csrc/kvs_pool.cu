@@ -24,6 +24,11 @@ namespace {
 
 constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+// [a, a + na) and [b, b + nb) share a byte
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool pool_dims(const kvs_pool_config* c, PoolDims* d) {
@@ -97,9 +102,12 @@ bool call_ok(const kvs_pool* p, int layer, int n_req) {
 }
 
 bool query_ok(const kvs_pool* p, const void* q, long long q_stride, const int* cu_q, const int* ctx_len,
-              const int* table, const void* out) {
+              const int* table, const void* out, int n_tok) {
   if (!q || !cu_q || !ctx_len || !table || !out) return false;
-  return aligned16(q) && aligned16(out) && q_stride % 8 == 0 && q_stride >= (long long)p->d.Hq * p->d.d;
+  const size_t row = (size_t)p->d.Hq * p->d.d;
+  if (!aligned16(q) || !aligned16(out) || q_stride % 8 || q_stride < (long long)row) return false;
+  // a row split over several CTAs is written while others may still read its q
+  return !overlap(q, ((size_t)(n_tok - 1) * q_stride + row) * 2, out, n_tok * row * 2);
 }
 
 }  // namespace
@@ -142,6 +150,9 @@ kvs_status kvs_pool_create(const kvs_pool_config* cfg, void* d_k, void* d_v, voi
       return KVS_ERR_INVALID_ARG;
     }
   }
+  const size_t bytes = (size_t)d.NL * d.n_slots * d.Hkv * d.bs * d.d * d.ebytes;
+  if (overlap(d_k, bytes, d_v, bytes) || overlap(d_k, bytes, d_workspace, p.total) || overlap(d_v, bytes, d_workspace, p.total))
+    return KVS_ERR_INVALID_ARG;
   kvs_pool* c = new (std::nothrow) kvs_pool();
   if (!c) return KVS_ERR_INVALID_ARG;
   c->maps = new (std::nothrow) CUtensorMap[2 * (size_t)d.NL];
@@ -223,7 +234,7 @@ kvs_status kvs_pool_attn(kvs_pool* c, int layer, const void* d_q, long long q_st
   const PoolDims& d = c->d;
   if (n_tok < 0 || n_tok > d.max_tokens) return KVS_ERR_INVALID_ARG;
   if (n_req == 0 || n_tok == 0) return KVS_OK;
-  if (!query_ok(c, d_q, q_stride, d_cu_q, d_ctx_len, d_block2slot, d_out)) return KVS_ERR_INVALID_ARG;
+  if (!query_ok(c, d_q, q_stride, d_cu_q, d_ctx_len, d_block2slot, d_out, n_tok)) return KVS_ERR_INVALID_ARG;
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(d_q);
   if (window >= d.max_ctx) window = 0;           // no key is that far away (and position + window stays in 32 bits)
   if (n_sink > d.max_ctx) n_sink = d.max_ctx;
@@ -250,7 +261,7 @@ kvs_status kvs_pool_prefix_attn(kvs_pool* c, int layer, const void* d_q, long lo
   const PoolDims& d = c->d;
   if (n_tok < 0 || n_tok > d.max_prefix_tokens) return KVS_ERR_INVALID_ARG;
   if (n_req == 0 || n_tok == 0) return KVS_OK;
-  if (!query_ok(c, d_q, q_stride, d_cu_q, d_ctx_len, d_block2slot, d_out)) return KVS_ERR_INVALID_ARG;
+  if (!query_ok(c, d_q, q_stride, d_cu_q, d_ctx_len, d_block2slot, d_out, n_tok)) return KVS_ERR_INVALID_ARG;
   if (n_prefix > 0 && (!d_prefix_req || !d_prefix_len || !d_prefix2slot)) return KVS_ERR_INVALID_ARG;
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(d_q);
   const unsigned char *k = c->k + layer * c->layer_bytes, *v = c->v + layer * c->layer_bytes;
@@ -264,8 +275,9 @@ kvs_status kvs_pool_prefix_attn(kvs_pool* c, int layer, const void* d_q, long lo
   }
   if (e == cudaSuccess) {
     const PoolSeqs own = {d_cu_q, nullptr, d_ctx_len, d_block2slot, n_req, n_req, n_tok, 1, 0, 0};
-    const PoolAttnOut o = {static_cast<__nv_bfloat16*>(d_out), d_lse, nullptr, nullptr, c->prev_out, c->prev_lse2,
-                           d_prefix_req, n_prefix};
+    // without prefixes there are no earlier rows, and d_prefix_req may be NULL
+    const PoolAttnOut o = {static_cast<__nv_bfloat16*>(d_out), d_lse, nullptr, nullptr, n_prefix > 0 ? c->prev_out : nullptr,
+                           c->prev_lse2, d_prefix_req, n_prefix};
     e = launch_pool_attn(d, k, v, &c->maps[2 * layer], q, q_stride, own, o, c->scratch, c->err, S(stream), &n);
     c->launches += n;
   }
@@ -281,7 +293,11 @@ kvs_status kvs_pool_evict(kvs_pool* c, int layer, const float* d_weight, const i
     return KVS_ERR_INVALID_ARG;
   if (n_req == 0) return KVS_OK;
   if (!d_weight || !d_ctx_len || !d_block2slot || !d_dst2slot || !d_kept || !d_n_kept || !d_weight_out) return KVS_ERR_INVALID_ARG;
-  if (d_weight == d_weight_out) return KVS_ERR_INVALID_ARG;
+  // what the call reads it may not write: other CTAs still read it
+  const size_t weights = (size_t)n_req * d.Hkv * d.max_ctx * 4;
+  if (overlap(d_weight, weights, d_weight_out, weights) || d_block2slot == d_dst2slot ||
+      overlap(d_ctx_len, (size_t)n_req * 4, d_n_kept, (size_t)n_req * 4))
+    return KVS_ERR_INVALID_ARG;
   c->launches += 2;
   return cuda_status(launch_pool_evict(d, c->k + layer * c->layer_bytes, c->v + layer * c->layer_bytes, d_weight, d_ctx_len,
                                        d_block2slot, n_req, keep, n_sink, n_recent, d_dst2slot, d_kept, d_n_kept,

@@ -77,7 +77,7 @@ cudaError_t launch_pool_append(const PoolDims& d, unsigned char* k, unsigned cha
                                cudaStream_t s);
 // Attention of the sequences' rows.  Exactly one of out (bf16) and part_out (fp32, with part_lse) is
 // written; with prev_out / prev_lse (fp32 rows and log2-sum-exps of an earlier call over other keys, for
-// the tokens of requests [*prev_req0, *prev_req1)) the result joins both.  lse: natural log, may be nullptr.
+// the tokens of requests [prev_req[0], prev_req[n_prev])) the result joins both.  lse: natural log, may be nullptr.
 struct PoolAttnOut {
   __nv_bfloat16* out;
   float* lse;         // [n_tok][Hq] natural log, or nullptr
