@@ -197,14 +197,19 @@ def test_prefix(i, kv):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
-@pytest.mark.parametrize("i", range(9))
+@pytest.mark.parametrize("i", range(12))
 def test_evict(i, kv):
     ctx, keep, sink, recent, bs, kind = [
         ([100, 64, 33, 0], 64, 4, 8, 16, "plain"), ([1], 1, 0, 0, 16, "plain"), ([300], 299, 0, 299, 32, "plain"),
         ([1000, 999, 200], 128, 0, 0, 64, "ties"), ([513, 700], 65, 1, 64, 128, "plain"), ([2000], 1000, 4, 100, 16, "nan"),
         ([40000], 3000, 4, 32, 128, "plain"), ([3000, 100], 7, 7, 0, 16, "zeros"),
-        ([60000], 2500, 3, 60, 64, "ties")][i]
-    hq, hk, d = HEADS[i % len(HEADS)]
+        ([60000], 2500, 3, 60, 64, "ties"),
+        ([45000] + [3, 70] * 80, 61, 2, 3, 128, "ties"),              # many units: one CTA each
+        ([340000, 20], 1500, 4, 64, 128, "plain"),                    # runs longer than shared memory holds
+        ([9000, 33, 8193, 4097], 4000, 3990, 5, 16, "zeros")][i]   # runs without a token to choose from
+    hq, hk, d = HEADS[i % len(HEADS)] if i < 10 else HEADS[0]
+    if i in (9, 10):
+        hq, hk, d = 2, 1, 64
     need = [-(-min(n, keep) // bs) for n in ctx]
     c = PoolCase(900 + i, ctx, [0] * len(ctx), hq, hk, d, bs, kv, spare=sum(need)).cuda()
     w = c.rng.exponential(1.0, (len(ctx), hk, c.max_ctx)).astype(np.float32)
