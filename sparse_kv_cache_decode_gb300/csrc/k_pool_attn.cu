@@ -651,7 +651,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             constexpr int VEC = D / 16;              // 16-code vectors of a row
 #pragma unroll 4
             for (int y = tid - 384; y < TOK * VEC; y += 128) {
-              const int row = y / VEC, v = y - row * VEC;
+              int row, v;
+              widen_place<VEC>(y, row, v);
               uint4 w = *reinterpret_cast<const uint4*>(src + row * D + v * 16);
               if (x && part && !key_seen(it, base + row)) w = make_uint4(0, 0, 0, 0);
               widen16(w, dst + row * 128, TOK * 128, row, v);

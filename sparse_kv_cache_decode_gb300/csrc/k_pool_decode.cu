@@ -547,20 +547,28 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
           const unsigned char* src = stg + rs * C::CODES;
           uint4 w[PER];
 #pragma unroll
-          for (int e = 0; e < PER; ++e) w[e] = *reinterpret_cast<const uint4*>(src + (th + e * 128) * 16);
+          for (int e = 0; e < PER; ++e) {
+            int row, v;
+            widen_place<VEC>(th + e * 128, row, v);
+            w[e] = *reinterpret_cast<const uint4*>(src + row * D + v * 16);
+          }
           const int base = tile_base(it, j);
           if (x && !tile_whole(it, base)) {
 #pragma unroll
-            for (int e = 0; e < PER; ++e)
-              if (!key_seen(it, base + (th + e * 128) / VEC)) w[e] = make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < PER; ++e) {
+              int row, v;
+              widen_place<VEC>(th + e * 128, row, v);
+              if (!key_seen(it, base + row)) w[e] = make_uint4(0, 0, 0, 0);
+            }
           }
           ok = k < S || __all_sync(0xffffffffu, wait(&kv_empty[s], par));
           if (!ok) break;
           unsigned char* dst = ring + s * C::TILE;
 #pragma unroll
           for (int e = 0; e < PER; ++e) {
-            const int y = th + e * 128, row = y / VEC;
-            widen16(w[e], dst + row * 128, TOK * 128, row, y - row * VEC);
+            int row, v;
+            widen_place<VEC>(th + e * 128, row, v);
+            widen16(w[e], dst + row * 128, TOK * 128, row, v);
           }
           fence_proxy_async_smem();
           __syncwarp();

@@ -537,7 +537,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
           constexpr int VEC = D / 16;
 #pragma unroll 4
           for (int y = tid - 384; y < TOK * VEC; y += 128) {
-            const int row = y / VEC, v = y - row * VEC;
+            int row, v;
+            widen_place<VEC>(y, row, v);
             widen16(*reinterpret_cast<const uint4*>(stg + rs * C::CODES + row * D + v * 16), kring + s * C::TILE + row * 128,
                     TOK * 128, row, v);
           }

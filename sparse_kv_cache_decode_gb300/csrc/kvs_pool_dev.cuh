@@ -180,6 +180,20 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(0x7b807b80u));           // 0x7b80: 2^120
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(0x7b807b80u));
 }
+// Row and vector (16 codes) that place y of a code tile is widened by.  At 8 vectors a row, 8 lanes take half of a row and
+// the other half of the next: their 16-byte loads and stores then fill all banks (a row's two 64-dim chunks of bf16 are
+// 16 KiB apart, on the same banks, and its own 8 vectors would meet there in pairs).
+template <int VEC>
+__device__ __forceinline__ void widen_place(int y, int& row, int& v) {
+  if (VEC == 8) {
+    const int sub = (y >> 2) & 1;
+    row = (y >> 4) * 2 + sub;
+    v = (y & 3) + 4 * (sub ^ ((y >> 3) & 1));
+  } else {
+    row = y / VEC;
+    v = y - row * VEC;
+  }
+}
 // 16 E4M3 codes (vector v of a row) as bf16 into the row of a K-major 128-byte-swizzled tile: `p` the row in its first
 // 64-dim chunk, chunks `chunk` bytes apart.
 __device__ __forceinline__ void widen16(const uint4& w, unsigned char* p, int chunk, int row, int v) {
