@@ -11,11 +11,18 @@
 //
 // The tiles of all items form one sequence that is cut into equal ranges, one per CTA (one per SM), as in the kernel
 // for many rows; the same merge kernel joins the items that a cut splits.  (Joining them in the last of an item's CTAs to
-// finish saves a launch, but its fences and serial loads cost more: 16.7 us against 13.3 for one request's token.)
+// finish saves a launch, but its fences and serial loads cost more: 16.7 us against 13.3 for one request's token; planned by one warp it now takes 12.0.)
+//
+// E4M3 pools.  S^T is a product of the K codes as they are with Q in E4M3: a row of Q is scaled by a power of two, so that its
+// largest element lies in [2^7, 2^8), and split into two codes, q = hi + lo, in columns of their own.  The 8 bits of a bf16
+// significand are 4 + 4, so the split is exact for elements down to 2^-10 of the row's largest; below that it is off by
+// at most 2^-18 of it (half a step of E4M3's subnormals).  V is widened to bf16
+// tiles, whose product takes P^T in bf16 (P has no room in E4M3: its rounding would be an output's error).  Widening K as
+// well was the kernel's bound: 2650 clocks a tile, 87 us for 32 requests' windows of 4096 tokens, against 67.
 //
 // Roles: warp 0 brings K/V tiles, warp 1 issues the products (S^T of a tile before O^T of the tile before it, across
-// pieces), warp 2 loads Q, warps 4-7 are the softmax; with E4M3 pools warps 8-11 (K) and 12-15 (V)
-// widen the codes to bf16 tiles.
+// pieces), warp 2 loads Q, warps 4-7 are the softmax; with E4M3 pools warps 8-11 and 12-15 widen V's codes, every other
+// tile each.
 // Value rows that no row of the item sees are zeroed before their product.  All waits are bounded.
 #include <algorithm>
 
@@ -34,28 +41,50 @@ template <int D, bool FP8, int NB>
 struct Cfg {
   static constexpr int CHUNKS = D / 64;
   static constexpr int NQ = NB < 16 ? 16 : NB;                // columns of the products
-  static constexpr int QCHUNK = NQ * 128;                     // 64 dims of the rows
-  static constexpr int QBUF = CHUNKS * QCHUNK;                // one item's Q
-  static constexpr int QB = FP8 && NB == 32 ? 1 : 2;          // items whose Q is held
+  static constexpr int NS = FP8 ? 2 * NB : NQ;                // of S^T: the rows' high and low codes
+  static constexpr int QCHUNK = NQ * 128;                     // 64 dims of the rows (bf16)
+  static constexpr int QBUF = FP8 ? NS * D : CHUNKS * QCHUNK; // one item's Q
   // P^T: 128 tokens of 128 bytes, 64 columns of room: two tiles of up to 32 columns side by side, or one of 64
   static constexpr int PBYTES = (NB == 64 ? 2 : 1) * TOK * 128;
   static constexpr int PSTEP = NB == 64 ? TOK * 128 : 64;     // bytes from one tile's P^T to the other's
   static constexpr int TILE = TOK * D * 2;
   static constexpr int CODES = TOK * D;
   static constexpr int THREADS = FP8 ? 512 : 256;
-  static constexpr int ROOM = MAX_SMEM - 3072 - 512 - 2048 - 4 * (kPoolMaxReq + 1) - kPieces * 64 - QB * QBUF - PBYTES;
-  // bf16 tiles; with E4M3 pools two of K and two of V, widened by warps of their own
-  static constexpr int STAGES = FP8 ? 4 : ROOM / TILE > 8 ? 8 : ROOM / TILE;
-  static constexpr int OFF_P = QB * QBUF;
+  static constexpr int ROOM = MAX_SMEM - 3072 - 512 - 2048 - 4 * (kPoolMaxReq + 1) - kPieces * 64 - 2 * QBUF - PBYTES;
+  // bf16 tiles, K's and V's in turn; with E4M3 pools three of V's, three of K's codes, and two of V's codes, each for the warps
+  // that widen it
+  static constexpr int STAGES = FP8 ? 3 : ROOM / TILE > 8 ? 8 : ROOM / TILE;
+  static constexpr int OFF_P = 2 * QBUF;
   static constexpr int OFF_RING = OFF_P + PBYTES;
-  static constexpr int OFF_ML = OFF_RING + STAGES * TILE;     // m, l, factors, maxima by warp, places: 3 KiB
+  static constexpr int OFF_K = OFF_RING + STAGES * TILE;      // codes of K (E4M3)
+  static constexpr int OFF_RAW = OFF_K + (FP8 ? 3 * CODES : 0);      // codes of V (E4M3)
+  static constexpr int OFF_ML = OFF_RAW + (FP8 ? 2 * CODES : 0);     // m, l, factors, scales of Q, maxima by warp, places: 3 KiB
   static constexpr int OFF_BAR = OFF_ML + 3072;
   static constexpr int OFF_PIECES = OFF_BAR + 512;
-  static constexpr int OFF_STG = (OFF_PIECES + kPieces * 64 + 1023) / 1024 * 1024;   // code tiles (E4M3), then the table
-  // shared memory with `staging` code tiles
-  static int bytes(int staging, int n_seq) { return OFF_STG + staging * CODES + 4 * (n_seq + 1) + 1024; }
-  static_assert(STAGES >= 3 && OFF_STG + (FP8 ? 2 * CODES : 0) + 4 * (kPoolMaxReq + 1) + 1024 <= MAX_SMEM, "shared memory plan");
+  static constexpr int OFF_TAB = OFF_PIECES + kPieces * 64;
+  static int bytes(int n_seq) { return OFF_TAB + 4 * (n_seq + 1) + 1024; }
+  static_assert(STAGES >= 3 && OFF_TAB + 4 * (kPoolMaxReq + 1) + 1024 <= MAX_SMEM, "shared memory plan");
 };
+
+// Products of E4M3 codes, both operands K-major with rows of D bytes: swizzled by as many bytes, 8-row groups 8 D bytes apart.
+template <int D, bool ACC>
+__device__ __forceinline__ void mma_codes(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+  constexpr uint32_t kHi = (8u * D >> 4) | (1u << 14) | ((D == 128 ? 2u : 4u) << 29);
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.u32 p, %5, 0;\n mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(kHi), "r"(idesc), "n"(ACC ? 1 : 0)
+      : "memory");
+}
+// byte offset of 16-byte chunk c of row r in such an operand
+template <int D>
+__device__ __forceinline__ int code_chunk(int r, int c) { return r * D + ((c ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4); }
+// two fp32 that two E4M3 codes stand for (exact)
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)codes));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
 
 __device__ __forceinline__ float warp_max(float x) {
   float y;
@@ -66,23 +95,29 @@ template <int D, bool FP8, int NB>
 __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
     pool_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, PoolDims d,
                        const __nv_bfloat16* __restrict__ q, long long q_stride, PoolSeqs seqs, PoolAttnOut o, void* scratch,
-                       Split sp, int staging, unsigned* err) {
+                       Split sp, unsigned* err) {
   using C = Cfg<D, FP8, NB>;
   constexpr int S = C::STAGES, NQ = C::NQ;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* ring = smem + C::OFF_RING;
-  unsigned char* stg = smem + C::OFF_STG;
+  unsigned char* raw = smem + C::OFF_RAW;
   float* m_s = reinterpret_cast<float*>(smem + C::OFF_ML);            // [64] m of the rows, -inf: none yet
   float* l_s = m_s + 64;                                              // [64] sums at a piece's end
   float* f_s = m_s + 128;                                             // [64] factors of a new m
+  float* nm_s = m_s + 192;                                            // [64] -m as the exponents take it: 0 without m, -inf without a row
+  // [4][32] softmax scale and scale of a row's codes of Q (E4M3), by piece: the softmax is done with piece p when Q of piece p + 4 is
+  // loaded, as S^T of piece p + 2 has been issued over the tile before last
+  float* q_s = m_s + 640;
   float* x_s = m_s + 256;                                             // [4][64] maxima or sums by warp
   long long* at_s = reinterpret_cast<long long*>(m_s + 512);          // [64] places of the output rows
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* kv_full = bars;             // [8]
+  uint64_t* kv_full = bars;             // [8] (E4M3: V's widened tiles)
   uint64_t* kv_empty = bars + 8;        // [8]
-  uint64_t* raw_full = bars + 16;       // [8] code tiles
-  uint64_t* raw_empty = bars + 24;      // [8]
+  uint64_t* k_full = bars + 16;         // [4] K's codes
+  uint64_t* k_empty = bars + 20;        // [4]
+  uint64_t* raw_full = bars + 24;       // [2] V's codes
+  uint64_t* raw_empty = bars + 26;      // [2]
   uint64_t* s_full = bars + 32;         // [2]
   uint64_t* s_free = bars + 34;         // [2]
   uint64_t* p_full = bars + 36;         // [2]
@@ -98,7 +133,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
   volatile int* plan = reinterpret_cast<volatile int*>(tmem_slot + 2);
   volatile int* outgrown = reinterpret_cast<volatile int*>(tmem_slot + 8);     // [2] a weight has outgrown m
   Piece* pieces = reinterpret_cast<Piece*>(smem + C::OFF_PIECES);
-  int* tab = reinterpret_cast<int*>(smem + C::OFF_STG + staging * C::CODES);
+  int* tab = reinterpret_cast<int*>(smem + C::OFF_TAB);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x;
 
@@ -106,8 +141,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
     for (int i = 0; i < 8; ++i) {
       mbar_init(&kv_full[i], FP8 ? 4 : 1);
       mbar_init(&kv_empty[i], 1);
-      mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 4);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
@@ -119,6 +156,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
       mbar_init(&o_full[i], 1);
       mbar_init(&o_free[i], 4);
       mbar_init(&vote[i], 4);
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
       outgrown[i] = 0;
     }
     mbar_init(drained, 1);
@@ -170,12 +209,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
   if (warp == 0) {
     // ------------------------------------------------------------------ K/V tiles: a lane per block of a tile
     constexpr int BOXES = FP8 ? 1 : C::CHUNKS;
-    const int SLOTS = FP8 ? staging : S;
-    uint64_t* full = FP8 ? raw_full : kv_full;
-    uint64_t* empty = FP8 ? raw_empty : kv_empty;
     const int pages = TOK >> d.log2bs;
     const int box_bytes = d.bs * (FP8 ? D : 128);
-    int k = 0, s = 0;
+    int k = 0, s = 0, T = 0;          // tiles of the ring (bf16: K's and V's in turn; E4M3: K's), V's code tiles
     unsigned par = 1;                 // of the slot's last release (the first round is free)
     bool ok = true;
     do {
@@ -199,19 +235,27 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
             else row = (now * d.Hkv + it.h) * d.bs;
           }
           const int n_load = __popc(__ballot_sync(0xffffffffu, row >= 0));
-          for (int x = 0; x < 2; ++x, ++k) {
-            ok = k < SLOTS || __all_sync(0xffffffffu, wait(&empty[s], par));
+          for (int x = 0; x < 2; ++x) {
+            const bool raw_v = FP8 && x;
+            if (raw_v) ok = T < 2 || __all_sync(0xffffffffu, wait(&raw_empty[T & 1], ((T >> 1) - 1) & 1));
+            else ok = k < S || __all_sync(0xffffffffu, wait(FP8 ? &k_empty[s] : &kv_empty[s], par));
             if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&full[s], (unsigned)(n_load * BOXES * box_bytes));
+            uint64_t* full = raw_v ? &raw_full[T & 1] : FP8 ? &k_full[s] : &kv_full[s];
+            if (lane == 0) mbar_arrive_expect_tx(full, (unsigned)(n_load * BOXES * box_bytes));
             __syncwarp();
             if (row >= 0) {
-              unsigned char* dst = FP8 ? stg + s * C::CODES + lane * box_bytes : ring + s * C::TILE + lane * box_bytes;
+              unsigned char* dst = (raw_v ? raw + (T & 1) * C::CODES : FP8 ? smem + C::OFF_K + s * C::CODES : ring + s * C::TILE) + lane * box_bytes;
 #pragma unroll
-              for (int b = 0; b < BOXES; ++b) tma_load_2d(dst + b * (TOK * 128), x ? &tmV : &tmK, b * 64, row, &full[s]);
+              for (int b = 0; b < BOXES; ++b) tma_load_2d(dst + b * (TOK * 128), x ? &tmV : &tmK, b * 64, row, full);
             }
-            if (++s == SLOTS) {
-              s = 0;
-              par ^= 1;
+            if (raw_v) {
+              ++T;
+            } else {
+              ++k;
+              if (++s == S) {
+                s = 0;
+                par ^= 1;
+              }
             }
           }
         }
@@ -219,12 +263,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
     } while (more());
     __syncwarp();
     // no tensor load may still be writing this CTA's shared memory when it exits
-    for (int i = max(0, k - SLOTS); i < k; ++i) mbar_wait(&full[i % SLOTS], (i / SLOTS) & 1, kDrainTimeoutNs);
+    for (int i = max(0, k - S); i < k; ++i) mbar_wait(FP8 ? &k_full[i % S] : &kv_full[i % S], (i / S) & 1, kDrainTimeoutNs);
+    if (FP8)
+      for (int i = max(0, T - 2); i < T; ++i) mbar_wait(&raw_full[i & 1], (i >> 1) & 1, kDrainTimeoutNs);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ products
-    const uint32_t id_s = idesc_bf16_f32(128, NQ);
+    // S^T: bf16, or E4M3 codes (whose format fields are 0)
+    const uint32_t id_s = FP8 ? idesc_bf16_f32(128, C::NS) & ~((1u << 7) | (1u << 10)) : idesc_bf16_f32(128, NQ);
     const uint32_t id_o = idesc_bf16_f32(128, NQ) | (1u << 15) | (1u << 16);      // V and P^T are read MN-major
     const uint32_t aq = smem_u32(smem) >> 4, ap = smem_u32(smem + C::OFF_P) >> 4, ar = smem_u32(ring) >> 4;
+    const uint32_t ak = smem_u32(smem + C::OFF_K) >> 4;
     // V^T: 64-dim blocks of a tile 16 KiB apart; at d = 64 the second block gives lanes 64-127, which are not used: it is
     // read 1 KiB on, still inside this CTA's shared memory
     constexpr uint32_t kV = (uint32_t)((D == 128 ? TOK * 128 : 1024) >> 4) << 16;
@@ -237,19 +285,27 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
         int is = 0, js = 0, io = 0, jo = 0;      // the same within this list of pieces
         int n_s = cnt > 0 ? pieces[0].n : 0, n_o = n_s;
         auto s_t = [&]() {
-          const int s = (2 * T) % S, b = T & 1;
+          const int n = FP8 ? T : 2 * T, s = n % S, b = T & 1;      // K's place in the ring
           if (js == 0) ok = wait(&q_full[pc & 1], (pc >> 1) & 1);
-          ok = ok && wait(&kv_full[s], ((2 * T) / S) & 1) && (T < 2 || wait(&s_free[b], ((T >> 1) - 1) & 1));
+          ok = ok && wait(FP8 ? &k_full[s] : &kv_full[s], (n / S) & 1) && (T < 2 || wait(&s_free[b], ((T >> 1) - 1) & 1));
           if (!ok) return;
           tc_fence_after();
-          const uint32_t k0 = ar + s * (C::TILE >> 4), q0 = aq + (pc % C::QB) * (C::QBUF >> 4), t = tS(b);
-          mma_ss<false>(t, k0, q0, id_s);
+          const uint32_t q0 = aq + (pc & 1) * (C::QBUF >> 4), t = tS(b);
+          if constexpr (FP8) {
+            const uint32_t k0 = ak + s * (C::CODES >> 4);
+            mma_codes<D, false>(t, k0, q0, id_s);
 #pragma unroll
-          for (int k16 = 1; k16 < D / 16; ++k16)
-            mma_ss<true>(t, k0 + (((k16 >> 2) * (TOK * 128) + (k16 & 3) * 32) >> 4),
-                         q0 + (((k16 >> 2) * C::QCHUNK + (k16 & 3) * 32) >> 4), id_s);
+            for (int k32 = 1; k32 < D / 32; ++k32) mma_codes<D, true>(t, k0 + k32 * 2, q0 + k32 * 2, id_s);
+          } else {
+            const uint32_t k0 = ar + s * (C::TILE >> 4);
+            mma_ss<false>(t, k0, q0, id_s);
+#pragma unroll
+            for (int k16 = 1; k16 < D / 16; ++k16)
+              mma_ss<true>(t, k0 + (((k16 >> 2) * (TOK * 128) + (k16 & 3) * 32) >> 4),
+                           q0 + (((k16 >> 2) * C::QCHUNK + (k16 & 3) * 32) >> 4), id_s);
+          }
           tc_commit(&s_full[b]);
-          tc_commit(&kv_empty[s]);
+          tc_commit(FP8 ? &k_empty[s] : &kv_empty[s]);
           ++T;
           if (++js == n_s) {
             tc_commit(&q_free[pc & 1]);
@@ -259,8 +315,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
           }
         };
         auto o_t = [&]() {
-          const int s = (2 * To + 1) % S, b = To & 1;
-          ok = wait(&kv_full[s], ((2 * To + 1) / S) & 1) && wait(&p_full[b], (To >> 1) & 1) &&
+          const int n = FP8 ? To : 2 * To + 1, s = n % S, b = To & 1;      // V's
+          ok = wait(&kv_full[s], (n / S) & 1) && wait(&p_full[b], (To >> 1) & 1) &&
                (jo > 0 || po < 2 || wait(&o_free[po & 1], ((po >> 1) - 1) & 1));
           if (!ok) return;
           tc_fence_after();
@@ -300,18 +356,62 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
       for (int i = 0; i < cnt && ok; ++i, ++piece) {
         const Piece& it = pieces[i];
         const int nrows = it.nrows, row0 = it.row0, t0 = it.t0, h = it.h;
-        const int behind = piece - C::QB;      // the piece whose Q is there
-        ok = behind < 0 || __all_sync(0xffffffffu, wait(&q_free[behind & 1], (behind >> 1) & 1));
+        ok = piece < 2 || __all_sync(0xffffffffu, wait(&q_free[piece & 1], ((piece >> 1) - 1) & 1));
         if (!ok) break;
         constexpr int VEC = D / 8;       // 16-byte vectors of a row
-        unsigned char* buf = smem + (piece % C::QB) * C::QBUF;
-        for (int x = lane; x < nrows * VEC; x += 32) {
-          const int r = x / VEC, v = x - r * VEC, row = row0 + r, tok = div_g(d, row), g = row - tok * d.G;
-          cp_async16(buf + (v >> 3) * C::QCHUNK + r * 128 + (((v & 7) ^ (r & 7)) << 4),
-                     q + (t0 + tok) * q_stride + (h * d.G + g) * D + v * 8, 16);
+        unsigned char* buf = smem + (piece & 1) * C::QBUF;
+        if constexpr (!FP8) {
+          for (int x = lane; x < nrows * VEC; x += 32) {
+            const int r = x / VEC, v = x - r * VEC, row = row0 + r, tok = div_g(d, row), g = row - tok * d.G;
+            cp_async16(buf + (v >> 3) * C::QCHUNK + r * 128 + (((v & 7) ^ (r & 7)) << 4),
+                       q + (t0 + tok) * q_stride + (h * d.G + g) * D + v * 8, 16);
+          }
+          cp_async_commit();
+          cp_async_wait_all();
+        } else {
+          // a step takes 32 / VEC rows, a vector per lane; up to 8 steps' loads in flight
+          const float sl2 = d.scale * d.k_scale * kLog2e;
+          constexpr int PER = 32 / VEC, DEEP = NB / PER < 8 ? NB / PER : 8;
+          const int sub = lane / VEC, v = lane % VEC;
+#pragma unroll 1
+          for (int r0 = 0; r0 < nrows; r0 += PER * DEEP) {
+            uint4 w[DEEP];
+#pragma unroll
+            for (int e = 0; e < DEEP; ++e) {
+              const int r = r0 + e * PER + sub, row = row0 + r, tok = div_g(d, row), g = row - tok * d.G;
+              w[e] = r < nrows ? *reinterpret_cast<const uint4*>(q + (t0 + tok) * q_stride + (h * d.G + g) * D + v * 8)
+                               : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int e = 0; e < DEEP; ++e) {
+              const int r = r0 + e * PER + sub;
+              const uint32_t u[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+              // the exponent field of the row's largest element (as bit patterns: magnitudes of bf16 compare as integers)
+              uint32_t top = 0;
+#pragma unroll
+              for (int i2 = 0; i2 < 4; ++i2) top = max(top, max(u[i2] & 0x7fffu, (u[i2] >> 16) & 0x7fffu));
+#pragma unroll
+              for (int o2 = VEC / 2; o2; o2 >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o2));
+              const uint32_t field = min(max(top >> 7, 8u), 254u);
+              const float mult = __uint_as_float((261u - field) << 23);       // 2^7 / 2^exponent
+              uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+              for (int i2 = 0; i2 < 4; ++i2) {
+                const float a = bf16_lo(u[i2]) * mult, b2 = bf16_hi(u[i2]) * mult;
+                const uint32_t c2 = f32x2_to_e4m3x2(a, b2);
+                const float2 back = e4m3x2_to_f32(c2);
+                hi[i2 >> 1] |= c2 << ((i2 & 1) * 16);
+                lo[i2 >> 1] |= (uint32_t)f32x2_to_e4m3x2(a - back.x, b2 - back.y) << ((i2 & 1) * 16);
+              }
+              if (r < nrows) {
+                *reinterpret_cast<uint2*>(buf + code_chunk<D>(r, v >> 1) + (v & 1) * 8) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2*>(buf + code_chunk<D>(NB + r, v >> 1) + (v & 1) * 8) = make_uint2(lo[0], lo[1]);
+                // (infinities and NaN in a row leave it NaN)
+                if (v == 0) q_s[(piece & 3) * 32 + r] = top >= 0x7f80u ? __int_as_float(0x7fc00000) : __uint_as_float((field - 7u) << 23) * sl2;
+              }
+            }
+          }
         }
-        cp_async_commit();
-        cp_async_wait_all();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[piece & 1]);
@@ -342,6 +442,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
         }
         const int ja = it.ns + (lo_all + TOK - 1) / TOK - it.lo_tile - it.j0;
         const unsigned n_whole = (unsigned)max(0, it.ns + hi_all / TOK - it.lo_tile - it.j0 - ja);
+        const float* qs = q_s + (piece & 3) * 32;
         float l[NB];
 #pragma unroll
         for (int x = 0; x < NB; ++x) l[x] = 0.f;
@@ -377,7 +478,24 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
           float x[NB];
 #pragma unroll 1
           for (bool first = true;; first = false) {
-            if constexpr (NB == 8) tmem_ld8(tS(b) + lanes, x);
+            if constexpr (FP8) {
+              // the products with the rows' high and low codes
+              if constexpr (NB == 8) {
+                float w[16];
+                tmem_ld16(tS(b) + lanes, w);
+#pragma unroll
+                for (int y = 0; y < 8; ++y) x[y] = w[y] + w[8 + y];
+              } else {
+#pragma unroll
+                for (int y0 = 0; y0 < NB; y0 += 16) {
+                  float w[16], z[16];
+                  tmem_ld16(tS(b) + lanes + y0, w);
+                  tmem_ld16(tS(b) + lanes + NB + y0, z);
+#pragma unroll
+                  for (int y = 0; y < 16; ++y) x[y0 + y] = w[y] + z[y];
+                }
+              }
+            } else if constexpr (NB == 8) tmem_ld8(tS(b) + lanes, x);
             else if constexpr (NB == 16) tmem_ld16(tS(b) + lanes, x);
             else if constexpr (NB == 32) tmem_ld32(tS(b) + lanes, x);
             else tmem_ld64(tS(b) + lanes, x);
@@ -396,10 +514,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
               }
               named_bar_sync(2, 128);
               if (lr < NB) {
-                const float v = fmaxf(fmaxf(x_s[lr], x_s[64 + lr]), fmaxf(x_s[128 + lr], x_s[192 + lr])) * sl2, m = m_s[lr];
+                const float v = fmaxf(fmaxf(x_s[lr], x_s[64 + lr]), fmaxf(x_s[128 + lr], x_s[192 + lr])) * (FP8 ? qs[lr] : sl2), m = m_s[lr];
                 const float m2 = m == -INFINITY || v > m + kMaxArg ? v : m;
                 f_s[lr] = m == -INFINITY || m2 == m ? 1.f : ex2(m - m2);
                 m_s[lr] = m2;
+                nm_s[lr] = lr >= nrows ? -INFINITY : m2 == -INFINITY ? 0.f : -m2;
               }
               if (lr == 0) outgrown[b] = 0;
               named_bar_sync(2, 128);
@@ -434,10 +553,17 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
 #pragma unroll
             for (int y = 0; y < NB; y += 8) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float m = m_s[y + e], arg = fmaf(x[y + e], sl2, m == -INFINITY ? 0.f : -m);
-                if (y + e < nrows) top = fmaxf(top, arg);
-                x[y + e] = ex2(arg);
+              for (int e = 0; e < 8; e += 4) {
+                const float4 z = *reinterpret_cast<const float4*>(nm_s + y + e);
+                const float4 f = FP8 ? *reinterpret_cast<const float4*>(qs + y + e) : make_float4(sl2, sl2, sl2, sl2);
+                float a0, a1, a2, a3;
+                unpack2(fma2(pack2(x[y + e], x[y + e + 1]), pack2(f.x, f.y), pack2(z.x, z.y)), a0, a1);
+                unpack2(fma2(pack2(x[y + e + 2], x[y + e + 3]), pack2(f.z, f.w), pack2(z.z, z.w)), a2, a3);
+                top = max3(max3(top, a0, a1), a2, a3);      // (columns without a row: -inf, or NaN, which a maximum skips)
+                x[y + e] = ex2(a0);
+                x[y + e + 1] = ex2(a1);
+                x[y + e + 2] = ex2(a2);
+                x[y + e + 3] = ex2(a3);
               }
               *reinterpret_cast<uint4*>(pr + (((pc0 + (y >> 3)) ^ (lr & 7)) << 4)) =
                   make_uint4(pack_bf16x2(x[y], x[y + 1]), pack_bf16x2(x[y + 2], x[y + 3]), pack_bf16x2(x[y + 4], x[y + 5]),
@@ -460,7 +586,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_free[b]);
 #pragma unroll
-          for (int y = 0; y < NB; ++y) l[y] += x[y];
+          for (int y = 0; y < NB; y += 2) unpack2(add2(pack2(l[y], l[y + 1]), pack2(x[y], x[y + 1])), l[y], l[y + 1]);
           fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
@@ -529,22 +655,23 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
       }
     } while (more());
   } else if constexpr (FP8) {
-    // ------------------------------------------------------------------ E4M3 codes -> bf16 tiles: K (warps 8-11), V (12-15)
-    // Each has every other slot of both rings to itself, so its waits never look two phases ahead.
+    // ------------------------------------------------------------------ V's codes -> bf16 tiles: warps 8-11 and 12-15 in turn
+    // Each four have a code tile of their own.  The ring's slots are shared; a wait for slot T % 3 never looks two phases
+    // ahead, as these warps have waited for the product of tile T - 5 before.
     const int x = (warp - 8) >> 2, th = tid & 127;
-    int k = x, s = x, rs = x;
-    unsigned par = 1, rpar = 0;       // of the slot's last release, of the codes
+    int T = 0;
     bool ok = true;
     do {
       const int cnt = plan[3];
       for (int i = 0; i < cnt && ok; ++i) {
         const Piece& it = pieces[i];
         const int j1 = it.j0 + it.n;
-        for (int j = it.j0; j < j1 && ok; ++j, k += 2) {
-          ok = __all_sync(0xffffffffu, wait(&raw_full[rs], rpar));
+        for (int j = it.j0; j < j1 && ok; ++j, ++T) {
+          if ((T & 1) != x) continue;
+          ok = __all_sync(0xffffffffu, wait(&raw_full[x], (T >> 1) & 1));
           if (!ok) break;
           constexpr int VEC = D / 16, PER = TOK * VEC / 128;              // 16-code vectors of a row, of a thread
-          const unsigned char* src = stg + rs * C::CODES;
+          const unsigned char* src = raw + x * C::CODES;
           uint4 w[PER];
 #pragma unroll
           for (int e = 0; e < PER; ++e) {
@@ -552,8 +679,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
             widen_place<VEC>(th + e * 128, row, v);
             w[e] = *reinterpret_cast<const uint4*>(src + row * D + v * 16);
           }
-          const int base = tile_base(it, j);
-          if (x && !tile_whole(it, base)) {
+          // the codes are in registers: the next ones may come (their load's latency is longer than the widening)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&raw_empty[x]);
+          const int base = tile_base(it, j), s = T % S;
+          if (!tile_whole(it, base)) {
 #pragma unroll
             for (int e = 0; e < PER; ++e) {
               int row, v;
@@ -561,7 +691,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
               if (!key_seen(it, base + row)) w[e] = make_uint4(0, 0, 0, 0);
             }
           }
-          ok = k < S || __all_sync(0xffffffffu, wait(&kv_empty[s], par));
+          ok = T < S || __all_sync(0xffffffffu, wait(&kv_empty[s], ((T / S) - 1) & 1));
           if (!ok) break;
           unsigned char* dst = ring + s * C::TILE;
 #pragma unroll
@@ -572,20 +702,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&kv_full[s]);
-            mbar_arrive(&raw_empty[rs]);
-          }
-          s += 2;
-          if (s >= S) {
-            s = x;
-            par ^= 1;
-          }
-          rs += 2;
-          if (rs >= staging) {
-            rs = x;
-            rpar ^= 1;
-          }
+          if (lane == 0) mbar_arrive(&kv_full[s]);
         }
       }
     } while (more());
@@ -607,10 +724,8 @@ cudaError_t launch(const PoolDims& d, const CUtensorMap* tm, const __nv_bfloat16
   cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), MAX_SMEM);
   if (e != cudaSuccess) return e;
   const Split sp = {device_sm_count(), 2};
-  // code tiles in flight: as many as fit beside the table of the sequences
-  const int staging = !FP8 ? 0 : C::bytes(8, seqs.n_seq) <= MAX_SMEM ? 8 : C::bytes(4, seqs.n_seq) <= MAX_SMEM ? 4 : 2;
-  launch_pdl(kern, dim3(sp.n_cta), dim3(C::THREADS), C::bytes(staging, seqs.n_seq), s, tm[0], tm[1], d, q, q_stride, seqs, o,
-             scratch, sp, staging, err);
+  launch_pdl(kern, dim3(sp.n_cta), dim3(C::THREADS), C::bytes(seqs.n_seq), s, FP8 ? tm[2] : tm[0], tm[1], d, q, q_stride, seqs, o,
+             scratch, sp, err);
   e = cudaGetLastError();
   *n_launched = 1;
   if (e != cudaSuccess) return e;

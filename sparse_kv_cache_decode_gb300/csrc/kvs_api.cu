@@ -250,7 +250,7 @@ namespace kvs {
 // Tiled tensor map of bf16 (elem_bytes 2) or bytes (1): dims and box innermost first, strides in bytes of the outer
 // dimensions; 128-byte swizzle or none.
 bool encode_tmap(CUtensorMap* m, void* base, int rank, const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
-                 int elem_bytes, bool swizzle) {
+                 int elem_bytes, int swizzle) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if (!encode) {
     void* fn = nullptr;
@@ -265,15 +265,15 @@ bool encode_tmap(CUtensorMap* m, void* base, int rank, const uint64_t* dims, con
   const cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = encode(m, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
                       base, reinterpret_cast<const cuuint64_t*>(dims), reinterpret_cast<const cuuint64_t*>(strides), box, estr,
-                      CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
 // 2D tensor map over a row-major matrix [rows][inner] of bf16 (elem_bytes 2) or bytes (1), boxes of
-// box_inner x box_rows with the 128-byte swizzle (box_inner * elem_bytes must be 128), or none.
+// box_inner x box_rows swizzled by 128 or 64 bytes (box_inner * elem_bytes at most that), or not (0).
 bool make_tmap_2d(CUtensorMap* m, void* base, uint64_t inner, uint64_t rows, uint32_t box_inner, uint32_t box_rows,
-                  int elem_bytes, bool swizzle) {
+                  int elem_bytes, int swizzle) {
   const uint64_t dims[2] = {inner, rows}, strides[1] = {inner * elem_bytes};
   const uint32_t box[2] = {box_inner, box_rows};
   return encode_tmap(m, base, 2, dims, strides, box, elem_bytes, swizzle);

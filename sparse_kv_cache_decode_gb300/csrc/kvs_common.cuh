@@ -214,9 +214,9 @@ cudaError_t launch_attention(const Dims& d, const Layer& L, const __nv_bfloat16*
                              cudaStream_t s);
 int attention_supported(const Dims& d);
 bool encode_tmap(CUtensorMap* m, void* base, int rank, const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
-                 int elem_bytes, bool swizzle);
+                 int elem_bytes, int swizzle);
 bool make_tmap_2d(CUtensorMap* m, void* base, uint64_t inner, uint64_t rows, uint32_t box_inner, uint32_t box_rows,
-                  int elem_bytes = 2, bool swizzle = true);
+                  int elem_bytes = 2, int swizzle = 128);
 int score_tc_supported(const Dims& d, int nq);
 cudaError_t launch_score_tc(const Dims& d, const __nv_bfloat16* index, const __nv_bfloat16* q, int nq,
                             const int* ctx_len, float* scores, unsigned* err, cudaStream_t s);

@@ -16,7 +16,7 @@ struct kvs_pool {
   unsigned* err;
   float *lse2, *prev_lse2, *prev_out;
   void* scratch;
-  CUtensorMap* maps;        // per layer: K, V
+  CUtensorMap* maps;        // per layer: K, V, and K as the products read its codes (E4M3)
   unsigned long long launches;
 };
 
@@ -117,7 +117,7 @@ bool make_pool_q_map(CUtensorMap* m, const PoolDims& d, const __nv_bfloat16* q, 
   const uint64_t dims[3] = {(uint64_t)d.d, (uint64_t)d.Hq, (uint64_t)n_tok};
   const uint64_t strides[2] = {(uint64_t)d.d * 2, (uint64_t)q_stride * 2};
   const uint32_t box[3] = {64, (uint32_t)d.G, (uint32_t)(d.rt / d.G)};
-  return encode_tmap(m, const_cast<__nv_bfloat16*>(q), 3, dims, strides, box, 2, true);
+  return encode_tmap(m, const_cast<__nv_bfloat16*>(q), 3, dims, strides, box, 2, 128);
 }
 }  // namespace kvs
 
@@ -155,7 +155,7 @@ kvs_status kvs_pool_create(const kvs_pool_config* cfg, void* d_k, void* d_v, voi
     return KVS_ERR_INVALID_ARG;
   kvs_pool* c = new (std::nothrow) kvs_pool();
   if (!c) return KVS_ERR_INVALID_ARG;
-  c->maps = new (std::nothrow) CUtensorMap[2 * (size_t)d.NL];
+  c->maps = new (std::nothrow) CUtensorMap[3 * (size_t)d.NL];
   if (!c->maps) {
     delete c;
     return KVS_ERR_INVALID_ARG;
@@ -176,10 +176,11 @@ kvs_status kvs_pool_create(const kvs_pool_config* cfg, void* d_k, void* d_v, voi
   // swizzled as the products read them), or all dims of E4M3 codes, as they are
   const uint64_t rows = (uint64_t)d.n_slots * d.Hkv * d.bs;
   const uint32_t inner = (uint32_t)(d.fp8 ? d.d : 64);
+  // (E4M3's third map: the same boxes of K, swizzled)
   for (int l = 0; l < d.NL; ++l)
-    for (int x = 0; x < 2; ++x)
-      if (!make_tmap_2d(&c->maps[2 * l + x], (x ? c->v : c->k) + l * c->layer_bytes, (uint64_t)d.d, rows, inner,
-                        (uint32_t)d.bs, d.ebytes, !d.fp8)) {
+    for (int x = 0; x < (d.fp8 ? 3 : 2); ++x)
+      if (!make_tmap_2d(&c->maps[3 * l + x], (x == 1 ? c->v : c->k) + l * c->layer_bytes, (uint64_t)d.d, rows, inner,
+                        (uint32_t)d.bs, d.ebytes, !d.fp8 ? 128 : x == 2 ? d.d : 0)) {
         kvs_pool_destroy(c);
         return KVS_ERR_CUDA;
       }
@@ -243,11 +244,11 @@ kvs_status kvs_pool_attn(kvs_pool* c, int layer, const void* d_q, long long q_st
   const PoolAttnOut o = {static_cast<__nv_bfloat16*>(d_out), d_lse, d_weight ? c->lse2 : nullptr, nullptr, nullptr, nullptr,
                          nullptr, 0};
   int n = 0;
-  cudaError_t e = launch_pool_attn(d, k, c->v + layer * c->layer_bytes, &c->maps[2 * layer], q, q_stride, seqs, o,
+  cudaError_t e = launch_pool_attn(d, k, c->v + layer * c->layer_bytes, &c->maps[3 * layer], q, q_stride, seqs, o,
                                    c->scratch, c->err, S(stream), &n);
   c->launches += n;
   if (e == cudaSuccess && d_weight) {
-    e = launch_pool_weight(d, &c->maps[2 * layer], q, q_stride, seqs, c->lse2, d_weight, c->scratch, c->err, S(stream), &n);
+    e = launch_pool_weight(d, &c->maps[3 * layer], q, q_stride, seqs, c->lse2, d_weight, c->scratch, c->err, S(stream), &n);
     c->launches += n;
   }
   return cuda_status(e);
@@ -270,7 +271,7 @@ kvs_status kvs_pool_prefix_attn(kvs_pool* c, int layer, const void* d_q, long lo
   if (n_prefix > 0) {
     const PoolSeqs pre = {d_cu_q, d_prefix_req, d_prefix_len, d_prefix2slot, n_prefix, n_req, n_tok, 0, 0, 0};
     const PoolAttnOut o = {nullptr, nullptr, c->prev_lse2, c->prev_out, nullptr, nullptr, nullptr, 0};
-    e = launch_pool_attn(d, k, v, &c->maps[2 * layer], q, q_stride, pre, o, c->scratch, c->err, S(stream), &n);
+    e = launch_pool_attn(d, k, v, &c->maps[3 * layer], q, q_stride, pre, o, c->scratch, c->err, S(stream), &n);
     c->launches += n;
   }
   if (e == cudaSuccess) {
@@ -278,7 +279,7 @@ kvs_status kvs_pool_prefix_attn(kvs_pool* c, int layer, const void* d_q, long lo
     // without prefixes there are no earlier rows, and d_prefix_req may be NULL
     const PoolAttnOut o = {static_cast<__nv_bfloat16*>(d_out), d_lse, nullptr, nullptr, n_prefix > 0 ? c->prev_out : nullptr,
                            c->prev_lse2, d_prefix_req, n_prefix};
-    e = launch_pool_attn(d, k, v, &c->maps[2 * layer], q, q_stride, own, o, c->scratch, c->err, S(stream), &n);
+    e = launch_pool_attn(d, k, v, &c->maps[3 * layer], q, q_stride, own, o, c->scratch, c->err, S(stream), &n);
     c->launches += n;
   }
   return cuda_status(e);

@@ -118,6 +118,28 @@ SINGLE = [  # contexts, window, sink, block size
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m", [1, 3, 7])
+def test_query_rows_of_every_size(m, d, kv):
+    """Rows whose elements differ by many powers of two, rows of zeros, rows far larger or smaller than their neighbours.
+
+    With an E4M3 pool a row of Q may be held to 2^-18 of its largest element (4 here) wherever an element is 2^-10 of that
+    or smaller.  A key's |k| sum to less than 128 * 4 (4 times a normal's mean of 0.8 for heavy keys), so a logit is off by at
+    most 512 * 4 * 2^-18 / sqrt(128) = 7e-4 by it, inside the logit error that check_out allows (1.3e-3 at d = 128, and half
+    the sum and 0.7e-3 / sqrt(2) at d = 64)."""
+    c = PoolCase(40 + m + d, [700, 129, 64], [m] * 3, 8, 2, d, 32, kv)
+    q = c.q.float()
+    t = torch.arange(c.n_tok * 8).view(c.n_tok, 8, 1) % 5
+    spike = torch.zeros(d)
+    spike[d // 3] = 4.0
+    q = torch.where(t == 0, q * 2.0 ** -11 + spike, torch.where(t == 1, q * 0, torch.where(t == 2, q * 2.0 ** -30, torch.where(t == 3, q * 2.0 ** -125, q * 1.5))))
+    c.q = q.to(torch.bfloat16)
+    c.cuda()
+    got, lse, _ = run_attn(c)
+    check_attn(c, got, lse)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
 @pytest.mark.parametrize("i", range(len(SINGLE)))
 def test_single_tokens(i, kv):
     ctx, window, sink, bs = SINGLE[i]
