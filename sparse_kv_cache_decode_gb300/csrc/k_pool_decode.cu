@@ -451,8 +451,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
         for (int j = 0; j < n; ++j, ++T) {
           const int b = T & 1;
           wait(&s_full[b], (T >> 1) & 1);
-          // P's room: free once the product of the tile before last has read it
-          if (T >= 2) wait(&p_free[b], ((T >> 1) - 1) & 1);
+          // P's room is free as well: the product of the tile before last was issued before this S^T, whose commit covers it
           tc_fence_after();
           const bool edge = (unsigned)(j - ja) >= n_whole;
           const int base = tile_base(it, it.j0 + j), t = base + lr;
@@ -551,23 +550,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
             }
             float top = -INFINITY;
 #pragma unroll
-            for (int y = 0; y < NB; y += 8) {
-#pragma unroll
-              for (int e = 0; e < 8; e += 4) {
-                const float4 z = *reinterpret_cast<const float4*>(nm_s + y + e);
-                const float4 f = FP8 ? *reinterpret_cast<const float4*>(qs + y + e) : make_float4(sl2, sl2, sl2, sl2);
-                float a0, a1, a2, a3;
-                unpack2(fma2(pack2(x[y + e], x[y + e + 1]), pack2(f.x, f.y), pack2(z.x, z.y)), a0, a1);
-                unpack2(fma2(pack2(x[y + e + 2], x[y + e + 3]), pack2(f.z, f.w), pack2(z.z, z.w)), a2, a3);
-                top = max3(max3(top, a0, a1), a2, a3);      // (columns without a row: -inf, or NaN, which a maximum skips)
-                x[y + e] = ex2(a0);
-                x[y + e + 1] = ex2(a1);
-                x[y + e + 2] = ex2(a2);
-                x[y + e + 3] = ex2(a3);
-              }
-              *reinterpret_cast<uint4*>(pr + (((pc0 + (y >> 3)) ^ (lr & 7)) << 4)) =
-                  make_uint4(pack_bf16x2(x[y], x[y + 1]), pack_bf16x2(x[y + 2], x[y + 3]), pack_bf16x2(x[y + 4], x[y + 5]),
-                             pack_bf16x2(x[y + 6], x[y + 7]));
+            for (int y = 0; y < NB; y += 4) {
+              const float4 z = *reinterpret_cast<const float4*>(nm_s + y);
+              const float4 f = FP8 ? *reinterpret_cast<const float4*>(qs + y) : make_float4(sl2, sl2, sl2, sl2);
+              unpack2(fma2(pack2(x[y], x[y + 1]), pack2(f.x, f.y), pack2(z.x, z.y)), x[y], x[y + 1]);
+              unpack2(fma2(pack2(x[y + 2], x[y + 3]), pack2(f.z, f.w), pack2(z.z, z.w)), x[y + 2], x[y + 3]);
+              // (columns without a row: -inf, or NaN, which a maximum skips)
+              top = max3(max3(top, x[y], x[y + 1]), x[y + 2], x[y + 3]);
             }
             // a weight that outgrows m: the warps vote (once a tile, so that the phases follow T), and all do the tile
             // again with a new m
@@ -578,19 +567,27 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
                 mbar_arrive(&vote[b]);
               }
             }
+#pragma unroll
+            for (int y = 0; y < NB; y += 8) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[y + e] = ex2(x[y + e]);
+              *reinterpret_cast<uint4*>(pr + (((pc0 + (y >> 3)) ^ (lr & 7)) << 4)) =
+                  make_uint4(pack_bf16x2(x[y], x[y + 1]), pack_bf16x2(x[y + 2], x[y + 3]), pack_bf16x2(x[y + 4], x[y + 5]),
+                             pack_bf16x2(x[y + 6], x[y + 7]));
+            }
+            fence_proxy_async_smem();
             if (set) break;
             wait(&vote[b], (T >> 1) & 1);
             if (!outgrown[b]) break;
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s_free[b]);
+          if (lane == 0) {
+            mbar_arrive(&s_free[b]);
+            mbar_arrive(&p_full[b]);
+          }
 #pragma unroll
           for (int y = 0; y < NB; y += 2) unpack2(add2(pack2(l[y], l[y + 1]), pack2(x[y], x[y + 1])), l[y], l[y + 1]);
-          fence_proxy_async_smem();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[b]);
         }
         // -------------------------------------------------------------- the piece's end: sums, then O^T, a dim per thread
 #pragma unroll
