@@ -311,7 +311,11 @@ __device__ __forceinline__ bool plan_few(const PoolDims& d, const PoolSeqs& seqs
     pos = __shfl_sync(0xffffffffu, before, s0) + h0;
     // piece `lane`: item pos + lane
     const int item = pos + lane, rank = item / d.Hkv;
-    const int s = item < n_items ? (int)__fns(some, 0, rank + 1) : 0;
+    int s = 0;                             // the rank-th of the lanes in `some`
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+      if (__popc(some & ((1u << (s + o)) - 1)) <= rank) s += o;
+    if (item >= n_items) s = 0;
     const SeqInfo r = {__shfl_sync(0xffffffffu, q.t0, s), __shfl_sync(0xffffffffu, q.t1, s), __shfl_sync(0xffffffffu, q.len, s)};
     item_rows(d, seqs, r, RB, 0, it);
     it.s = s;
