@@ -1,7 +1,7 @@
 // Device-resident pools: attention for few rows per (sequence, kv head) on the 5th-generation tensor cores.
 //
 // A decode step has G rows (a group's heads) per K/V row, drafts a few times that: far fewer than a product's 128-row
-// side.  Here the tokens take that side, and the rows the columns (NB = 8, 16, 32 or, with bf16 pools, 64 of them):
+// side.  Here the tokens take that side, and the rows the columns (NB = 8, 16 or 32 of them):
 //   S^T = K Q^T (128 tokens x NB),   P^T = 2^(S^T scale log2 e - m) in bf16,   O^T += V^T P^T (d x NB)
 // so that a tile of 128 tokens costs two products of 16 x (d / 16 + 8) small columns, and the 128 threads of the softmax
 // share its exponentials, a token each: the kernel is bound by the K/V bytes.  V is read as the product's A operand with
@@ -14,7 +14,7 @@
 // finish saves a launch, but its fences and serial loads cost more: 16.7 us against 13.3 for one request's token; planned by one warp it now takes 12.0.)
 //
 // E4M3 pools.  S^T is a product of the K codes as they are with Q in E4M3: a row of Q is scaled by a power of two, so that its
-// largest element lies in [2^7, 2^8), and split into two codes, q = hi + lo, in columns of their own.  The 8 bits of a bf16
+// largest element lies in [2^7, 2^8), and split into two codes, q = hi + lo, whose products add up.  The 8 bits of a bf16
 // significand are 4 + 4, so the split is exact for elements down to 2^-10 of the row's largest; below that it is off by
 // at most 2^-18 of it (half a step of E4M3's subnormals).  V is widened to bf16
 // tiles, whose product takes P^T in bf16 (P has no room in E4M3: its rounding would be an output's error).  Widening K as
@@ -41,12 +41,11 @@ template <int D, bool FP8, int NB>
 struct Cfg {
   static constexpr int CHUNKS = D / 64;
   static constexpr int NQ = NB < 16 ? 16 : NB;                // columns of the products
-  static constexpr int NS = FP8 ? 2 * NB : NQ;                // of S^T: the rows' high and low codes
   static constexpr int QCHUNK = NQ * 128;                     // 64 dims of the rows (bf16)
-  static constexpr int QBUF = FP8 ? NS * D : CHUNKS * QCHUNK; // one item's Q
-  // P^T: 128 tokens of 128 bytes, 64 columns of room: two tiles of up to 32 columns side by side, or one of 64
-  static constexpr int PBYTES = (NB == 64 ? 2 : 1) * TOK * 128;
-  static constexpr int PSTEP = NB == 64 ? TOK * 128 : 64;     // bytes from one tile's P^T to the other's
+  static constexpr int QBUF = CHUNKS * QCHUNK;                // one item's Q: bf16, or its high codes and behind them its low ones
+  // P^T: 128 tokens of 128 bytes, 64 columns of room: two tiles of up to 32 columns side by side
+  static constexpr int PBYTES = TOK * 128;
+  static constexpr int PSTEP = 64;                            // bytes from one tile's P^T to the other's
   static constexpr int TILE = TOK * D * 2;
   static constexpr int CODES = TOK * D;
   static constexpr int THREADS = FP8 ? 512 : 256;
@@ -269,7 +268,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------------ products
     // S^T: bf16, or E4M3 codes (whose format fields are 0)
-    const uint32_t id_s = FP8 ? idesc_bf16_f32(128, C::NS) & ~((1u << 7) | (1u << 10)) : idesc_bf16_f32(128, NQ);
+    const uint32_t id_s = idesc_bf16_f32(128, NQ) & ~(FP8 ? (1u << 7) | (1u << 10) : 0u);
     const uint32_t id_o = idesc_bf16_f32(128, NQ) | (1u << 15) | (1u << 16);      // V and P^T are read MN-major
     const uint32_t aq = smem_u32(smem) >> 4, ap = smem_u32(smem + C::OFF_P) >> 4, ar = smem_u32(ring) >> 4;
     const uint32_t ak = smem_u32(smem + C::OFF_K) >> 4;
@@ -296,6 +295,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
             mma_codes<D, false>(t, k0, q0, id_s);
 #pragma unroll
             for (int k32 = 1; k32 < D / 32; ++k32) mma_codes<D, true>(t, k0 + k32 * 2, q0 + k32 * 2, id_s);
+#pragma unroll
+            for (int k32 = 0; k32 < D / 32; ++k32) mma_codes<D, true>(t, k0 + k32 * 2, q0 + (NQ * D >> 4) + k32 * 2, id_s);
           } else {
             const uint32_t k0 = ar + s * (C::TILE >> 4);
             mma_ss<false>(t, k0, q0, id_s);
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
               }
               if (r < nrows) {
                 *reinterpret_cast<uint2*>(buf + code_chunk<D>(r, v >> 1) + (v & 1) * 8) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2*>(buf + code_chunk<D>(NB + r, v >> 1) + (v & 1) * 8) = make_uint2(lo[0], lo[1]);
+                *reinterpret_cast<uint2*>(buf + NQ * D + code_chunk<D>(r, v >> 1) + (v & 1) * 8) = make_uint2(lo[0], lo[1]);
                 // (infinities and NaN in a row leave it NaN)
                 if (v == 0) q_s[(piece & 3) * 32 + r] = top >= 0x7f80u ? __int_as_float(0x7fc00000) : __uint_as_float((field - 7u) << 23) * sl2;
               }
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
           tc_fence_after();
           const bool edge = (unsigned)(j - ja) >= n_whole;
           const int base = tile_base(it, it.j0 + j), t = base + lr;
-          uint32_t v0 = 0xffffffffu, v1 = 0xffffffffu;
+          uint32_t vis = 0xffffffffu;
           if (edge) {
             // the columns that see this token: rows from its own position on, to the window's end
             int ca = 0, cb = t < it.len ? nrows : 0;
@@ -463,8 +464,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
               if (t > pa) ca = min(t - pa, NB + 1) * d.G - pa_row;
               if (seqs.window && t >= seqs.n_sink) cb = min(cb, min(max(t - pa + seqs.window, 0), NB + 1) * d.G - pa_row);
             }
-            v0 = bits_below(cb) & ~bits_below(ca);
-            v1 = bits_below(cb - 32) & ~bits_below(ca - 32);
+            vis = bits_below(cb) & ~bits_below(ca);
             if (!FP8 && !tile_whole(it, base)) {
               // value rows that no row of the item sees
               const int slot = 2 * T + 1;
@@ -472,36 +472,18 @@ __global__ void __launch_bounds__(Cfg<D, FP8, NB>::THREADS, 1)
               zero_rows(ring + (slot % S) * C::TILE, C::CHUNKS, lr & ~31, __ballot_sync(0xffffffffu, !key_seen(it, t)));
             }
           }
-          unsigned char* pr = smem + C::OFF_P + (NB == 64 ? b * C::PSTEP : 0) + lr * 128;
-          const int pc0 = NB == 64 ? 0 : b * 4;        // its first 16-byte chunk
+          unsigned char* pr = smem + C::OFF_P + lr * 128;
+          const int pc0 = b * 4;        // its first 16-byte chunk
           float x[NB];
 #pragma unroll 1
           for (bool first = true;; first = false) {
-            if constexpr (FP8) {
-              // the products with the rows' high and low codes
-              if constexpr (NB == 8) {
-                float w[16];
-                tmem_ld16(tS(b) + lanes, w);
-#pragma unroll
-                for (int y = 0; y < 8; ++y) x[y] = w[y] + w[8 + y];
-              } else {
-#pragma unroll
-                for (int y0 = 0; y0 < NB; y0 += 16) {
-                  float w[16], z[16];
-                  tmem_ld16(tS(b) + lanes + y0, w);
-                  tmem_ld16(tS(b) + lanes + NB + y0, z);
-#pragma unroll
-                  for (int y = 0; y < 16; ++y) x[y0 + y] = w[y] + z[y];
-                }
-              }
-            } else if constexpr (NB == 8) tmem_ld8(tS(b) + lanes, x);
+            if constexpr (NB == 8) tmem_ld8(tS(b) + lanes, x);
             else if constexpr (NB == 16) tmem_ld16(tS(b) + lanes, x);
-            else if constexpr (NB == 32) tmem_ld32(tS(b) + lanes, x);
-            else tmem_ld64(tS(b) + lanes, x);
+            else tmem_ld32(tS(b) + lanes, x);
             if (edge) {
 #pragma unroll
               for (int y = 0; y < NB; ++y)
-                if (!((y < 32 ? v0 : v1) & (1u << (y & 31)))) x[y] = -INFINITY;
+                if (!(vis & (1u << y))) x[y] = -INFINITY;
             }
             const bool set = fresh || !first;
             if (set) {
@@ -735,8 +717,6 @@ cudaError_t launch_nb(int nb, const PoolDims& d, const CUtensorMap* tm, const __
                       const PoolSeqs& seqs, const PoolAttnOut& o, void* scratch, unsigned* err, cudaStream_t s, int* n_launched) {
   if (nb <= 8) return launch<D, FP8, 8>(d, tm, q, q_stride, seqs, o, scratch, err, s, n_launched);
   if (nb <= 16) return launch<D, FP8, 16>(d, tm, q, q_stride, seqs, o, scratch, err, s, n_launched);
-  if constexpr (!FP8)
-    if (nb > 32) return launch<D, FP8, 64>(d, tm, q, q_stride, seqs, o, scratch, err, s, n_launched);
   return launch<D, FP8, 32>(d, tm, q, q_stride, seqs, o, scratch, err, s, n_launched);
 }
 

@@ -94,8 +94,7 @@ size_t pool_attn_scratch_bytes(const PoolDims& d);
 cudaError_t launch_pool_attn(const PoolDims& d, const unsigned char* k, const unsigned char* v, const CUtensorMap* tm,
                              const __nv_bfloat16* q, long long q_stride, const PoolSeqs& seqs, const PoolAttnOut& o,
                              void* scratch, unsigned* err, cudaStream_t s, int* n_launched);
-// The kernel for few rows per (sequence, kv head): row blocks of nb rows (up to 64;
-// 32 with E4M3 pools).
+// The kernel for few rows per (sequence, kv head): row blocks of nb rows (up to 32).
 cudaError_t launch_pool_decode(const PoolDims& d, const CUtensorMap* tm, const __nv_bfloat16* q, long long q_stride,
                                const PoolSeqs& seqs, const PoolAttnOut& o, int nb, void* scratch, unsigned* err,
                                cudaStream_t s, int* n_launched);
