@@ -367,7 +367,8 @@ kvs_status kvs_quantize_e4m3(const void* d_src_bf16, void* d_dst, size_t n, floa
  * never used and may hold anything; keys that some row sees must be finite.
  *
  * Supported: head dim 64 or 128; block_size 16, 32, 64 or 128; 1 to 128 query heads per kv head;
- * max_req <= 2048 with max_req * n_kv_head <= 65535; max_tokens * (H_q / H_kv) <= 2^25.
+ * max_req <= 2048 with max_req * n_kv_head <= 65535; max_tokens * (H_q / H_kv) <= 2^25;
+ * max_req * max_tokens * H_q <= 2^37.
  * Calls are asynchronous on `stream` and capturable; the workspace is scratch of one call at a time,
  * so calls on one kvs_pool must not overlap on the GPU, captured graphs that hold them included
  * (a second kvs_pool over the same K/V memory, with a workspace of its own, may run beside it).
@@ -438,7 +439,7 @@ kvs_status kvs_pool_prefix_attn(kvs_pool* pool, int layer, const void* d_q, long
 /* Cut caches down to the tokens that matter: per request and kv head keep the first n_sink and the last
  * n_recent tokens and, of the others, those with the largest weight, min(keep, ctx_len) in all (ties:
  * the earlier token; NaN lowest), in their order, and gather their K/V rows into the blocks of
- * dst2slot [n_req][nb_max], which must be disjoint from every block the call reads.
+ * dst2slot [n_req][nb_max], which must be distinct and disjoint from every block the call reads.
  *   kept [n_req][H_kv][keep]   the kept tokens' indices, ascending (entries past n_kept are left)
  *   n_kept [n_req]             min(keep, ctx_len): the new context length (another buffer than ctx_len)
  *   weight_out [n_req][H_kv][max_ctx], another buffer than weight: the kept tokens' weights, in order

@@ -40,6 +40,7 @@ constexpr float kMaxArg = 40.f;     // log2 of the largest weight before m is se
 template <int D, bool FP8, int NB>
 struct Cfg {
   static constexpr int CHUNKS = D / 64;
+  static constexpr int ML = 3 * 1024;
   static constexpr int NQ = NB < 16 ? 16 : NB;                // columns of the products
   static constexpr int QCHUNK = NQ * 128;                     // 64 dims of the rows (bf16)
   static constexpr int QBUF = CHUNKS * QCHUNK;                // one item's Q: bf16, or its high codes and behind them its low ones
@@ -49,7 +50,7 @@ struct Cfg {
   static constexpr int TILE = TOK * D * 2;
   static constexpr int CODES = TOK * D;
   static constexpr int THREADS = FP8 ? 512 : 256;
-  static constexpr int ROOM = MAX_SMEM - 3072 - 512 - 2048 - 4 * (kPoolMaxReq + 1) - kPieces * 64 - 2 * QBUF - PBYTES;
+  static constexpr int ROOM = MAX_SMEM - ML - 512 - 2048 - 4 * (kPoolMaxReq + 1) - kPieces * 64 - 2 * QBUF - PBYTES;
   // bf16 tiles, K's and V's in turn; with E4M3 pools three of V's, three of K's codes, and two of V's codes, each for the warps
   // that widen it
   static constexpr int STAGES = FP8 ? 3 : ROOM / TILE > 8 ? 8 : ROOM / TILE;
@@ -57,8 +58,8 @@ struct Cfg {
   static constexpr int OFF_RING = OFF_P + PBYTES;
   static constexpr int OFF_K = OFF_RING + STAGES * TILE;      // codes of K (E4M3)
   static constexpr int OFF_RAW = OFF_K + (FP8 ? 3 * CODES : 0);      // codes of V (E4M3)
-  static constexpr int OFF_ML = OFF_RAW + (FP8 ? 2 * CODES : 0);     // m, l, factors, scales of Q, maxima by warp, places: 3 KiB
-  static constexpr int OFF_BAR = OFF_ML + 3072;
+  static constexpr int OFF_ML = OFF_RAW + (FP8 ? 2 * CODES : 0);     // m, l, factors, scales of Q, maxima by warp, places
+  static constexpr int OFF_BAR = OFF_ML + ML;
   static constexpr int OFF_PIECES = OFF_BAR + 512;
   static constexpr int OFF_TAB = OFF_PIECES + kPieces * 64;
   static int bytes(int n_seq) { return OFF_TAB + 4 * (n_seq + 1) + 1024; }

@@ -48,6 +48,8 @@ bool pool_dims(const kvs_pool_config* c, PoolDims* d) {
   // rows of a layer are tensor-load coordinates (32 bits), and rows of a (request, kv head) are divided by G through 2^32 / G
   if ((long long)c->n_slots * c->n_kv_head * c->block_size > 0x7fff0000ll) return false;
   if ((long long)c->max_tokens * (c->n_q_head / c->n_kv_head) > (1 << 25)) return false;
+  // row blocks of a call are counted in 32 bits, for any offsets: each request may be given all tokens
+  if ((long long)c->max_req * c->max_tokens > (1ll << 37) / c->n_q_head) return false;
   d->NL = c->n_layer;
   d->n_slots = c->n_slots;
   d->Hq = c->n_q_head;
@@ -130,7 +132,7 @@ size_t kvs_pool_workspace_bytes(const kvs_pool_config* cfg) {
 }
 
 kvs_status kvs_pool_create(const kvs_pool_config* cfg, void* d_k, void* d_v, void* d_workspace,
-                           size_t workspace_bytes, kvs_pool** out) {
+                           size_t workspace_bytes, kvs_pool** out) try {
   if (!out) return KVS_ERR_INVALID_ARG;
   *out = nullptr;
   PoolDims d;
@@ -190,6 +192,8 @@ kvs_status kvs_pool_create(const kvs_pool_config* cfg, void* d_k, void* d_v, voi
   }
   *out = c;
   return KVS_OK;
+} catch (...) {      // out of host memory
+  return KVS_ERR_CUDA;
 }
 
 kvs_status kvs_pool_destroy(kvs_pool* c) {
@@ -214,7 +218,7 @@ unsigned long long kvs_pool_launch_count(kvs_pool* c) { return c ? c->launches :
 
 kvs_status kvs_pool_append(kvs_pool* c, int layer, const void* d_k_new, const void* d_v_new, long long kv_stride,
                            const int* d_cu_q, const int* d_ctx_len, const int* d_block2slot, int n_req, int n_tok,
-                           kvs_stream_t stream) {
+                           kvs_stream_t stream) try {
   if (!call_ok(c, layer, n_req) || n_tok < 0 || n_tok > c->d.max_tokens) return KVS_ERR_INVALID_ARG;
   const PoolDims& d = c->d;
   if (n_req == 0 || n_tok == 0) return KVS_OK;
@@ -226,11 +230,13 @@ kvs_status kvs_pool_append(kvs_pool* c, int layer, const void* d_k_new, const vo
   return cuda_status(launch_pool_append(d, c->k + layer * c->layer_bytes, c->v + layer * c->layer_bytes,
                                         static_cast<const __nv_bfloat16*>(d_k_new),
                                         static_cast<const __nv_bfloat16*>(d_v_new), kv_stride, q, c->err, S(stream)));
+} catch (...) {      // out of host memory
+  return KVS_ERR_CUDA;
 }
 
 kvs_status kvs_pool_attn(kvs_pool* c, int layer, const void* d_q, long long q_stride, const int* d_cu_q,
                          const int* d_ctx_len, const int* d_block2slot, int n_req, int n_tok, int window, int n_sink,
-                         void* d_out, float* d_lse, float* d_weight, kvs_stream_t stream) {
+                         void* d_out, float* d_lse, float* d_weight, kvs_stream_t stream) try {
   if (!call_ok(c, layer, n_req) || window < 0 || n_sink < 0) return KVS_ERR_INVALID_ARG;
   const PoolDims& d = c->d;
   if (n_tok < 0 || n_tok > d.max_tokens) return KVS_ERR_INVALID_ARG;
@@ -252,12 +258,14 @@ kvs_status kvs_pool_attn(kvs_pool* c, int layer, const void* d_q, long long q_st
     c->launches += n;
   }
   return cuda_status(e);
+} catch (...) {      // out of host memory
+  return KVS_ERR_CUDA;
 }
 
 kvs_status kvs_pool_prefix_attn(kvs_pool* c, int layer, const void* d_q, long long q_stride, const int* d_cu_q,
                                 const int* d_ctx_len, const int* d_block2slot, int n_req, int n_tok,
                                 const int* d_prefix_req, const int* d_prefix_len, const int* d_prefix2slot, int n_prefix,
-                                void* d_out, float* d_lse, kvs_stream_t stream) {
+                                void* d_out, float* d_lse, kvs_stream_t stream) try {
   if (!call_ok(c, layer, n_req) || n_prefix < 0 || n_prefix > c->d.max_req) return KVS_ERR_INVALID_ARG;
   const PoolDims& d = c->d;
   if (n_tok < 0 || n_tok > d.max_prefix_tokens) return KVS_ERR_INVALID_ARG;
@@ -283,11 +291,13 @@ kvs_status kvs_pool_prefix_attn(kvs_pool* c, int layer, const void* d_q, long lo
     c->launches += n;
   }
   return cuda_status(e);
+} catch (...) {      // out of host memory
+  return KVS_ERR_CUDA;
 }
 
 kvs_status kvs_pool_evict(kvs_pool* c, int layer, const float* d_weight, const int* d_ctx_len,
                           const int* d_block2slot, int n_req, int keep, int n_sink, int n_recent, const int* d_dst2slot,
-                          int* d_kept, int* d_n_kept, float* d_weight_out, kvs_stream_t stream) {
+                          int* d_kept, int* d_n_kept, float* d_weight_out, kvs_stream_t stream) try {
   if (!call_ok(c, layer, n_req)) return KVS_ERR_INVALID_ARG;
   const PoolDims& d = c->d;
   if (keep < 1 || keep > d.max_ctx || n_sink < 0 || n_recent < 0 || n_sink > keep || n_recent > keep - n_sink)
@@ -303,6 +313,8 @@ kvs_status kvs_pool_evict(kvs_pool* c, int layer, const float* d_weight, const i
   return cuda_status(launch_pool_evict(d, c->k + layer * c->layer_bytes, c->v + layer * c->layer_bytes, d_weight, d_ctx_len,
                                        d_block2slot, n_req, keep, n_sink, n_recent, d_dst2slot, d_kept, d_n_kept,
                                        d_weight_out, c->err, S(stream)));
+} catch (...) {      // out of host memory
+  return KVS_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -32,7 +32,8 @@ def make_pool_config(n_layer: int, n_slots: int, n_q_head: int, n_kv_head: int, 
 
 
 class Pool:
-    """A kvs_pool over K and V tensors of the caller, with its device workspace (allocated through torch)."""
+    """A kvs_pool over K and V tensors of the caller, with its device workspace (allocated through torch): keep it, and every
+    tensor of a call, until the calls on them are through."""
 
     def __init__(self, cfg: KvsPoolConfig, k: torch.Tensor, v: torch.Tensor):
         self.h = None

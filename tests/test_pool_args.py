@@ -25,7 +25,8 @@ def _bytes(K, **over):
 @pytest.mark.parametrize("over", [
     dict(), dict(head_dim=64), dict(block_size=128), dict(n_q_head=128, n_kv_head=1), dict(n_q_head=2), dict(n_q_head=6),
     dict(max_ctx=1), dict(max_ctx=1 << 30), dict(max_req=2048), dict(max_req=1, n_kv_head=1024, n_q_head=1024),
-    dict(max_prefix_tokens=0), dict(max_prefix_tokens=64), dict(kv_dtype="fp8", k_scale=0.0), dict(max_tokens=1 << 23, max_prefix_tokens=0)])
+    dict(max_prefix_tokens=0), dict(max_prefix_tokens=64), dict(kv_dtype="fp8", k_scale=0.0), dict(max_tokens=1 << 23, max_prefix_tokens=0),
+    dict(max_req=2048, n_kv_head=8, n_q_head=64, max_tokens=1 << 20)])
 def test_supported_configurations_size_a_workspace(K, over):
     n = _bytes(K, **over)
     c = OK | over
@@ -39,7 +40,7 @@ def test_supported_configurations_size_a_workspace(K, over):
     dict(max_req=0), dict(max_req=2049), dict(max_req=2048, n_kv_head=32, n_q_head=32), dict(max_tokens=0), dict(max_tokens=-5),
     dict(max_tokens=1 << 24, n_q_head=8), dict(max_prefix_tokens=65), dict(max_prefix_tokens=-1), dict(k_scale=-1.0),
     dict(v_scale=float("inf")), dict(k_scale=float("nan")), dict(softmax_scale=-1.0), dict(softmax_scale=float("nan")),
-    dict(n_slots=(1 << 31) - 1)])
+    dict(n_slots=(1 << 31) - 1), dict(max_req=2048, n_kv_head=16, n_q_head=128, max_tokens=1 << 20)])
 def test_other_configurations_are_refused(K, over):
     assert _bytes(K, **over) == 0
     cfg = K.make_pool_config(**(OK | over))
