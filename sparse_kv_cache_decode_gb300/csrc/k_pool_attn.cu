@@ -692,24 +692,32 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   if (r >= mt.nrows) return;
   const int n = mt.c1 - c + 1;                           // pieces: (c, 1), (c + 1, 0) .. (c1, 0)
   auto place = [&](int i) { return ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * 256 + r; };
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, sc.ml[place(i)].x);
+  constexpr int E = D / 32;
+  const int row = mt.row0 + r;
+  const size_t orow = (size_t)(mt.t0 + div_g(d, row)) * d.Hq + mt.head0 + row - div_g(d, row) * d.G, at = orow * D + lane * E;
+  const float2 ml0 = lane < n ? sc.ml[place(lane)] : make_float2(-INFINITY, 0.f);
+  // the earlier call's row, on its way while the parts are joined
+  const bool has_prev = o.prev_out && mt.seq >= o.prev_req[0] && mt.seq < o.prev_req[o.n_prev];
+  float prev[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) prev[e] = has_prev ? o.prev_out[at + e] : 0.f;
+  float M = ml0.x;
+  for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, sc.ml[place(i)].x);
 #pragma unroll
   for (int w = 16; w; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
   float l = 0.f;
-  constexpr int E = D / 32;
   float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   for (int i0 = 0; i0 < n; i0 += 32) {
     float w = 0.f;
     if (i0 + lane < n) {
-      const float2 v = sc.ml[place(i0 + lane)];
+      const float2 v = i0 == 0 ? ml0 : sc.ml[place(i0 + lane)];
       w = v.x == -INFINITY ? 0.f : ex2(v.x - M);
       l += w * v.y;
     }
     const int cnt = min(32, n - i0);
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i < cnt; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
       const float* p = sc.o + place(i0 + i) * D + lane * E;
@@ -728,16 +736,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   }
 #pragma unroll
   for (int w = 16; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-  const int row = mt.row0 + r;
-  const size_t orow = (size_t)(mt.t0 + div_g(d, row)) * d.Hq + mt.head0 + row % d.G;
-  const bool has_prev = o.prev_out && mt.seq >= o.prev_req[0] && mt.seq < o.prev_req[o.n_prev];
   const RowOut ro = row_out(o, has_prev, orow, M, l, d.v_scale);
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     acc[e] *= ro.w_new;
-    if (has_prev && ro.w_prev > 0.f) acc[e] += ro.w_prev * o.prev_out[orow * D + lane * E + e];
+    if (has_prev && ro.w_prev > 0.f) acc[e] += ro.w_prev * prev[e];
   }
-  const size_t at = orow * D + lane * E;
 #pragma unroll
   for (int e = 0; e < E; e += 2) {
     if (o.part_out) *reinterpret_cast<float2*>(o.part_out + at + e) = make_float2(acc[e], acc[e + 1]);
