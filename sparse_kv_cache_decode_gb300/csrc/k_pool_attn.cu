@@ -95,9 +95,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
   uint64_t* p_full = bars + 26;         // [2]
   uint64_t* o_full = bars + 30;         // [2]
   uint64_t* q_full = bars + 32;         // [2] by piece parity
-  uint64_t* q_free = bars + 34;
-  uint64_t* drained = bars + 35;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 36);
+  uint64_t* q_free = bars + 34;         // [2] by piece parity
+  uint64_t* drained = bars + 36;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 37);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   // position and first tile of the CTA's next piece, its tiles still to plan, pieces planned, items, tiles per CTA
   volatile int* plan = reinterpret_cast<volatile int*>(tmem_slot + 2);
@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     }
     mbar_init(&q_full[0], 1);
     mbar_init(&q_full[1], 1);
-    mbar_init(q_free, 1);
+    mbar_init(&q_free[0], 1);
+    mbar_init(&q_free[1], 1);
     mbar_init(drained, 1);
     *abort_flag = 0;
     plan[0] = plan[1] = plan[2] = 0;
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
               tc_commit(&kv_empty[s1]);
             }
             if (!ok) break;
-            tc_commit(q_free);
+            tc_commit(&q_free[piece & 1]);
             pv(0, sv, n == 1, par0);
             if (!ok) break;
             tc_commit(&o_full[0]);
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
               tc_fence_after();
               qk(g, s, qb * 128);
               tc_commit(&kv_empty[s]);
-              if (x == n - 1) tc_commit(q_free);
+              if (x == n - 1) tc_commit(&q_free[piece & 1]);
               const int info = tile * 4 + (x + 2 >= n ? 2 : 0) + (x < 2 ? 1 : 0);
               if (g) pend1 = info; else pend0 = info;
               if ((g ? pend0 : pend1) < 0) older = g;
@@ -345,7 +346,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------------ Q: whole tokens, so one load per row tile and chunk
-    // Two items of at most one row tile each use the two places; otherwise Q waits for the last item's products.
+    // Two items of at most one row tile each use the two places: piece p's Q waits for the products of piece p - 2, and
+    // where one of p - 1 and p has two row tiles, for those of p - 1 as well.  A parity tells phases apart only while the one
+    // waited for is the barrier's last: q_free[p & 1] completes phase p / 2 with piece p's products, which need the Q that
+    // waits here for phase p / 2 - 1, and every phase is waited for, so none is passed unseen.  (With one barrier for all
+    // pieces, phase p - 1 may be complete as well, and is at a new list of pieces: the wait for p - 2 would not end.)
     regs_dec<C::REGS_LOW>();
     int piece = 0, qb = 0, last_small = 1;
     bool ok = true;
@@ -356,9 +361,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
           const Piece& it = pieces[i];
           const int small = it.nrows <= RT;
           qb = small ? qb ^ 1 : 0;
-          const int behind = small && last_small ? piece - 2 : piece - 1;    // the piece that must be through
+          if (piece >= 2) ok = wait(&q_free[piece & 1], ((piece >> 1) - 1) & 1);
+          if (ok && piece >= 1 && !(small && last_small)) ok = wait(&q_free[(piece - 1) & 1], ((piece - 1) >> 1) & 1);
           last_small = small;
-          ok = behind < 0 || wait(q_free, behind & 1);
           if (!ok) break;
           mbar_arrive_expect_tx(&q_full[piece & 1], (unsigned)((small ? 1 : 2) * C::CHUNKS * RT * 128));
           for (int x = 0; x < (small ? 1 : 2); ++x)
