@@ -409,7 +409,8 @@ unsigned long long kvs_pool_launch_count(kvs_pool* pool);
 
 /* Write the K/V rows of every request's query tokens to their positions in the pool: k_new, v_new
  * [n_tok] tokens of [H_kv][d] bf16, kv_stride elements apart (a multiple of 8, 16-byte aligned);
- * E4M3 pools quantise them with the rule of kvs_quantize_e4m3. */
+ * E4M3 pools quantise them with the rule of kvs_quantize_e4m3.  Query tokens at a position p < 0 (a free place of the
+ * batch, whose context is empty) have no place in the pool and are passed over. */
 kvs_status kvs_pool_append(kvs_pool* pool, int layer, const void* d_k_new, const void* d_v_new, long long kv_stride,
                            const int* d_cu_q, const int* d_ctx_len, const int* d_block2slot, int n_req, int n_tok,
                            kvs_stream_t stream);

@@ -27,10 +27,7 @@ __global__ void __launch_bounds__(kAppendThreads)
   const SeqInfo r = pool_seq(d, seqs, s, err);
   if (tok < r.t0 || tok >= r.t1) return;
   const int pos = r.len - (r.t1 - tok);
-  if (pos < 0) {   // more query tokens than the context holds
-    set_error(err, KVS_ERR_BAD_INDEX);
-    return;
-  }
+  if (pos < 0) return;   // a free place of the batch, or more query tokens than the context holds: no place, as no keys in attention
   const int slot = seqs.table[(size_t)s * d.nb_max + (pos >> d.log2bs)];
   if (slot < 0 || slot >= d.n_slots) {
     set_error(err, KVS_ERR_BAD_INDEX);
