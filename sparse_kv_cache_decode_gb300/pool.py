@@ -22,13 +22,23 @@ _FP8 = (torch.float8_e4m3fn, torch.uint8)
 _I32, _F32 = (torch.int32,), (torch.float32,)
 
 
+def _int(x: int, name: str) -> int:
+    """x, if the ABI's 32 bits hold it (ctypes would cut it to its low bits)."""
+    if -0x80000000 <= x < 0x80000000:
+        return x
+    raise ValueError(f"{name}: {x} does not fit 32 bits")
+
+
 def make_pool_config(n_layer: int, n_slots: int, n_q_head: int, n_kv_head: int, head_dim: int, block_size: int,
                      max_ctx: int, max_req: int, max_tokens: int, max_prefix_tokens: int = 0, kv_dtype: str = "bf16",
                      k_scale: float = 1.0, v_scale: float = 1.0, softmax_scale: float = 0.0,
                      wait_timeout_us: int = 0) -> KvsPoolConfig:
-    return KvsPoolConfig(n_layer, n_slots, n_q_head, n_kv_head, head_dim, block_size, max_ctx, max_req, max_tokens,
-                         max_prefix_tokens, KV_DTYPE[kv_dtype], float(k_scale), float(v_scale), float(softmax_scale),
-                         wait_timeout_us)
+    ints = dict(n_layer=n_layer, n_slots=n_slots, n_q_head=n_q_head, n_kv_head=n_kv_head, head_dim=head_dim, block_size=block_size,
+                max_ctx=max_ctx, max_req=max_req, max_tokens=max_tokens, max_prefix_tokens=max_prefix_tokens)
+    if not 0 <= wait_timeout_us < 1 << 32:
+        raise ValueError(f"wait_timeout_us: {wait_timeout_us} does not fit 32 bits")
+    return KvsPoolConfig(*(_int(x, name) for name, x in ints.items()), KV_DTYPE[kv_dtype], float(k_scale), float(v_scale),
+                         float(softmax_scale), wait_timeout_us)
 
 
 class Pool:
@@ -133,18 +143,20 @@ class Pool:
         if n_v != n_tok or ks != vs:
             raise ValueError("k_new and v_new: different numbers or strides of tokens")
         n_req, cu, ctx, tab = self._batch(ctx_len, block2slot, cu_q)
-        self._call(self.L.kvs_pool_append, "kvs_pool_append", layer, kp, vp, ks, cu, ctx, tab, n_req, n_tok, self._stream(stream))
+        self._call(self.L.kvs_pool_append, "kvs_pool_append", _int(layer, "layer"), kp, vp, ks, cu, ctx, tab, n_req, n_tok, self._stream(stream))
 
     def attn(self, layer, q, cu_q, ctx_len, block2slot, out, window=0, n_sink=0, lse=None, weight=None, stream=None):
         """kvs_pool_attn: causal attention (window, n_sink: a sliding window and first tokens that stay visible);
         weight accumulates each key's softmax weight."""
         c = self.cfg
+        # no key is further away than the longest context
+        window, n_sink = _int(min(window, c.max_ctx), "window"), _int(min(n_sink, c.max_ctx), "n_sink")
         qp, qs, n_tok = self._tokens(q, "q", c.n_q_head)
         n_req, cu, ctx, tab = self._batch(ctx_len, block2slot, cu_q)
         o = self._whole(out, "out", _BF16, (n_tok, c.n_q_head, c.head_dim))
         ls = None if lse is None else self._whole(lse, "lse", _F32, (n_tok, c.n_q_head))
         w = None if weight is None else self._whole(weight, "weight", _F32, (n_req, c.n_kv_head, c.max_ctx))
-        self._call(self.L.kvs_pool_attn, "kvs_pool_attn", layer, qp, qs, cu, ctx, tab, n_req, n_tok, window, n_sink, o, ls, w,
+        self._call(self.L.kvs_pool_attn, "kvs_pool_attn", _int(layer, "layer"), qp, qs, cu, ctx, tab, n_req, n_tok, window, n_sink, o, ls, w,
                    self._stream(stream))
 
     def prefix_attn(self, layer, q, cu_q, ctx_len, block2slot, prefix_req, prefix_len, prefix2slot, out, lse=None,
@@ -159,7 +171,7 @@ class Pool:
         pt = self._whole(prefix2slot, "prefix2slot", _I32, (n_pre, self.nb_max))
         o = self._whole(out, "out", _BF16, (n_tok, c.n_q_head, c.head_dim))
         ls = None if lse is None else self._whole(lse, "lse", _F32, (n_tok, c.n_q_head))
-        self._call(self.L.kvs_pool_prefix_attn, "kvs_pool_prefix_attn", layer, qp, qs, cu, ctx, tab, n_req, n_tok, pr, pl, pt,
+        self._call(self.L.kvs_pool_prefix_attn, "kvs_pool_prefix_attn", _int(layer, "layer"), qp, qs, cu, ctx, tab, n_req, n_tok, pr, pl, pt,
                    n_pre, o, ls, self._stream(stream))
 
     def evict(self, layer, weight, ctx_len, block2slot, keep, n_sink, n_recent, dst2slot, kept, n_kept, weight_out,
@@ -172,8 +184,8 @@ class Pool:
         kp = self._whole(kept, "kept", _I32, (n_req, c.n_kv_head, keep))
         nk = self._whole(n_kept, "n_kept", _I32, (n_req,))
         wo = self._whole(weight_out, "weight_out", _F32, (n_req, c.n_kv_head, c.max_ctx))
-        self._call(self.L.kvs_pool_evict, "kvs_pool_evict", layer, w, ctx, tab, n_req, keep, n_sink, n_recent, dst, kp, nk, wo,
-                   self._stream(stream))
+        self._call(self.L.kvs_pool_evict, "kvs_pool_evict", _int(layer, "layer"), w, ctx, tab, n_req, keep, _int(n_sink, "n_sink"),
+                   _int(n_recent, "n_recent"), dst, kp, nk, wo, self._stream(stream))
 
     def launch_count(self) -> int:
         return int(self.L.kvs_pool_launch_count(self.h))
