@@ -346,8 +346,9 @@ kvs_status kvs_quantize_e4m3(const void* d_src_bf16, void* d_dst, size_t n, floa
 /* ------------------------------------------------------------------ caches resident in device memory
  * A kvs_pool is a paged KV cache that stays whole in device memory (no host history): the layers,
  * requests or prompt prefixes whose K/V need no offloading.  It lives beside a kvs_ctx in a model
- * whose other layers decode sparsely from host memory, and shares its terms: blocks of block_size
- * tokens, slots that hold a block, and block2slot tables.
+ * whose other layers decode sparsely from host memory, and uses its words (blocks of block_size
+ * tokens, slots that hold a block, block2slot tables) for layouts of its own, below: a slot here holds
+ * all kv heads of a block and a table has a row per request.  Nothing moves a request from one to the other.
  *
  * Layouts (row-major):
  *   K pool, V pool [n_layer][n_slots][H_kv][block_size][d]  bf16 or E4M3 codes, caller-owned
@@ -364,7 +365,8 @@ kvs_status kvs_quantize_e4m3(const void* d_src_bf16, void* d_dst, size_t n, floa
  * puts their K/V there).  A row that sees no key (p < 0, an empty context) gives zeros and lse -inf.
  * Rows of `out` and `lse` that belong to no request are left as they are.  K/V of keys that no row of the
  * call sees (past the context end, outside every window, in blocks whose table entry is -1) are
- * never used and may hold anything; keys that some row sees must be finite.
+ * never used and may hold anything; keys that some row sees must be finite, their logits finite in fp32, and V
+ * below 2^57 in magnitude (weights of up to 2^40 are summed before they are divided by their sum).
  *
  * Supported: head dim 64 or 128; block_size 16, 32, 64 or 128; 1 to 128 query heads per kv head;
  * max_req <= 2048 with max_req * n_kv_head <= 65535; max_tokens * (H_q / H_kv) <= 2^25;
@@ -421,6 +423,8 @@ kvs_status kvs_pool_append(kvs_pool* pool, int layer, const void* d_k_new, const
  * d_lse may be NULL.  d_weight (may be NULL) accumulates the softmax weight of each key over the rows
  * and heads of the call: weight[r][h][t] of a key before the request's query tokens is added to, that
  * of the query tokens themselves (positions ctx_len - q_r and up) is set; entries >= ctx_len are left.
+ * One kernel serves a call, chosen by its average rows (query tokens * heads of a kv head) per request: over E4M3 pools, a
+ * prompt's chunk and single tokens behind long contexts are faster in a call each.
  * q_stride: a multiple of 8, >= H_q * d; d_q and d_out 16-byte aligned, not overlapping. */
 kvs_status kvs_pool_attn(kvs_pool* pool, int layer, const void* d_q, long long q_stride, const int* d_cu_q,
                          const int* d_ctx_len, const int* d_block2slot, int n_req, int n_tok, int window, int n_sink,
@@ -431,7 +435,9 @@ kvs_status kvs_pool_attn(kvs_pool* pool, int layer, const void* d_q, long long q
  * the pool), then their own context causally as kvs_pool_attn without a window (ctx_len and positions
  * count a request's own tokens only).  Requests before prefix_req[0] or from prefix_req[n_prefix] on
  * have no prefix.  prefix_req [n_prefix + 1], ascending within [0, n_req]; n_prefix <= max_req (0: no prefixes,
- * their pointers may be NULL); n_tok <= max_prefix_tokens.  A prefix's K/V is read once for all its requests. */
+ * their pointers may be NULL); n_tok <= max_prefix_tokens.  A prefix's K/V is read once for every block of its
+ * requests' rows (query tokens * heads of a kv head): blocks of up to 256 rows, or of 8 to 32 where a prefix has at most 32 rows
+ * on average. */
 kvs_status kvs_pool_prefix_attn(kvs_pool* pool, int layer, const void* d_q, long long q_stride, const int* d_cu_q,
                                 const int* d_ctx_len, const int* d_block2slot, int n_req, int n_tok,
                                 const int* d_prefix_req, const int* d_prefix_len, const int* d_prefix2slot, int n_prefix,
