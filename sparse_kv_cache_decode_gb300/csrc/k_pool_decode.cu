@@ -12,7 +12,7 @@
 // The tiles of all items form one sequence that is cut into equal ranges, one per CTA (one per SM), as in the kernel
 // for many rows; the same merge kernel joins the items that a cut splits.  (Joining them in the last of an item's CTAs to
 // finish saves a launch, but its fences and serial loads cost more: 16.7 us against 13.3 for one request's token, both before
-// one warp planned a CTA's work, which took the form kept to 11.9.)
+// one warp planned a CTA's work, which took the form kept to 12.0.)
 //
 // E4M3 pools.  S^T is a product of the K codes as they are with Q in E4M3: a row of Q is scaled by a power of two, so that its
 // largest element lies in [2^7, 2^8), and split into two codes, q = hi + lo, whose products add up.  The 8 bits of a bf16
