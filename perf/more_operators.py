@@ -209,7 +209,8 @@ def prepare(c, seed):
               "place": torch.empty(n_tok, dtype=torch.int64, device="cuda"), "pos": torch.empty(n_tok, dtype=torch.int32, device="cuda")}
         if own:
             shape = (1, n_slots, cfg["n_kv_head"], bs, cfg["head_dim"])
-            s["pool"] = K.Pool(K.make_pool_config(**cfg), *(torch.zeros(shape, dtype=torch.bfloat16, device="cuda") for _ in range(2)))
+            pool = K.Pool(K.make_pool_config(**cfg), *(torch.zeros(shape, dtype=torch.bfloat16, device="cuda") for _ in range(2)))
+            s["tables"] = K.BlockTables(pool, s["table"], s["held"], s["ring"], s["state"])
         return s
     hq, hk, d = c["heads"], c["kv_heads"], c["dim"]
     s["freq"] = c["theta"] ** (-torch.arange(0, c["rot"], 2, dtype=torch.float64, device="cuda") / c["rot"])
@@ -353,9 +354,8 @@ def run(s):
     c = s["case"]
     if c["op"] == "tables":
         if own:
-            p = s["pool"]
-            p.reserve(s["ctx"], s["held"], s["table"], s["ring"], s["state"], s["cu"], s["place"], s["pos"], pos_delta=s["delta"])
-            p.reserve(s["before"], s["held"], s["table"], s["ring"], s["state"])
+            s["tables"].reserve(s["ctx"], s["cu"], s["place"], s["pos"], pos_delta=s["delta"])
+            s["tables"].reserve(s["before"])
         else:
             _plain_tables(s, s["ctx"], True)
             _plain_tables(s, s["before"], False)
