@@ -455,6 +455,89 @@ kvs_status kvs_pool_evict(kvs_pool* pool, int layer, const float* d_weight, cons
                           const int* d_block2slot, int n_req, int keep, int n_sink, int n_recent, const int* d_dst2slot,
                           int* d_kept, int* d_n_kept, float* d_weight_out, kvs_stream_t stream);
 
+/* ------------------------------------------------------------------ from a projection to a pool
+ * What a model does between its projections and the attention over a pool: whose block is where, and the
+ * norms and rotation of queries and keys.
+ *
+ * Block tables.  The free slots of a pool are a ring: ring [n_slots] int32 and ring_state [3] int32 = {first entry,
+ * free slots, blocks that were lacking}; the free slots are the entries ring_state[0], ... (mod n_slots), in the order in which
+ * they will be taken.  A pool with all slots free: ring = 0, 1, ..., n_slots - 1 and ring_state = {0, n_slots, 0}.
+ * n_held [n_req] int32 counts the blocks each row of the table owns (0 to begin with).
+ *
+ * kvs_pool_reserve makes every row hold the ceil(ctx_len[r] / block_size) blocks of its new length: rows that hold more (a
+ * request that is through, with ctx_len 0; drafts that were refused) give their last blocks back to the ring's end,
+ * request by request, blocks ascending; then rows that hold fewer take theirs from its front in the same order, those
+ * given back in this call last.  Entries of block2slot past a row's blocks are left as they were.  When the ring runs short
+ * nothing changes but ring_state[2], the number of blocks lacking (0 otherwise), and KVS_ERR_CAPACITY is reported.
+ * With cu_q (NULL: no tokens; n_tok is then 0) it also says where the call's query tokens (as in kvs_pool_attn) go:
+ *   place [n_tok] int64   slot * block_size + offset of the token's K/V rows; -1: none (a position p < 0, a token of no
+ *                         request, a block that was lacking)
+ *   pos [n_tok] int32     p + pos_delta[r] (pos_delta may be NULL: 0); 0 for tokens of no request.  May be NULL
+ * These serve every layer of the step.  A length outside [0, max_ctx], a count outside [0, nb_max], a ring state or
+ * offsets that cannot be, or a slot outside the pool is reported as KVS_ERR_BAD_INDEX; the row keeps its blocks and its
+ * tokens get no place (a ring state that cannot be changes nothing at all).  Buffers must not overlap.
+ *
+ * kvs_pool_places is the second half alone, for tables that are kept in another way. */
+kvs_status kvs_pool_reserve(kvs_pool* pool, const int* d_ctx_len, int* d_n_held, int* d_block2slot, int* d_ring, int* d_ring_state,
+                            int n_req, const int* d_cu_q, const int* d_pos_delta, int n_tok, long long* d_place, int* d_pos,
+                            kvs_stream_t stream);
+kvs_status kvs_pool_places(kvs_pool* pool, const int* d_cu_q, const int* d_ctx_len, const int* d_block2slot, int n_req, int n_tok,
+                           const int* d_pos_delta, long long* d_place, int* d_pos, kvs_stream_t stream);
+
+/* Norms and rotation.  A row x of head_dim elements of one head becomes, in fp32 and rounded once,
+ *   y = x / sqrt(mean(x^2) + norm_eps) * w          (with a norm weight w [head_dim] fp32; else y = x)
+ *   (y_a, y_b) -> rot_scale (y_a cos t - y_b sin t, y_b cos t + y_a sin t),   t = pos[axis[i]] * inv_freq[i]
+ * for the pairs i = 0 .. rot_dim / 2 - 1 of its first rot_dim elements: (a, b) = (2 i, 2 i + 1) if adjacent, else
+ * (i, i + rot_dim / 2).  A token has a position on each of n_axis axes (time, height and width of an image's patch, say), and each pair
+ * turns by one of them.  Positions are any int32; the angle is exact to 2^-31 turns and 2^-52 of its size.  The sum of a normed
+ * row's squares must be finite in fp32. */
+typedef struct {
+  int head_dim;                 /* 64, 128 or 256 (a pool's own for the calls on a pool) */
+  int rot_dim;                  /* a multiple of 16, at most head_dim; 0: no rotation */
+  int adjacent;                 /* 0 or 1 */
+  int n_axis;                   /* 1 to 8 */
+  const unsigned char* axis;    /* host, [rot_dim / 2], each < n_axis; NULL: 0 (n_axis 1) */
+  const double* inv_freq;       /* host, [rot_dim / 2], radians per position; NULL: theta^(-2 i / rot_dim) */
+  double theta;                 /* > 0 (unused with inv_freq) */
+  float rot_scale;              /* 0 -> 1 */
+  float norm_eps;               /* >= 0 */
+} kvs_rope_config;
+
+typedef struct kvs_rope kvs_rope;
+
+/* A handle of host memory only: it serves any device, stream and number of calls at once.  The arrays of cfg are copied. */
+kvs_status kvs_rope_create(const kvs_rope_config* cfg, kvs_rope** out);
+kvs_status kvs_rope_destroy(kvs_rope* rope);
+
+/* The heads of queries and of keys of n_tok tokens, as above: for kvs_decode_step (its q and k_new), an index of one's own,
+ * or the part of a latent row that turns.  Token t's head h is at d_x + t * x_stride + h * x_head_stride (elements: multiples of 8;
+ * rows 16-byte aligned, not overlapping); norms [head_dim] fp32, 16-byte aligned, or NULL; n_q_head or n_k_head may be 0 (its pointers
+ * are not used), at most 1024.  pos: n_axis rows of [n_tok] int32, pos_stride apart (0: one row for all axes).  Outputs are
+ * written in place (the same pointer and strides) or apart from the inputs and from one another. */
+kvs_status kvs_rotate(const kvs_rope* rope, const void* d_q, long long q_stride, long long q_head_stride, int n_q_head,
+                      const float* d_q_norm, void* d_q_out, long long q_out_stride, long long q_out_head_stride, const void* d_k,
+                      long long k_stride, long long k_head_stride, int n_k_head, const float* d_k_norm, void* d_k_out,
+                      long long k_out_stride, long long k_out_head_stride, const int* d_pos, long long pos_stride, int n_tok,
+                      kvs_stream_t stream);
+
+/* The same with K and V on their way into a pool, in one pass: d_q [n_tok] tokens of [H_q][d], q_stride elements apart, is normed and
+ * rotated into d_q_out (q_out_stride; in place, or apart from q, k and v), d_k and d_v [n_tok] tokens of [H_kv][d],
+ * kv_stride apart, go to place[t] (of kvs_pool_reserve, distinct), k normed and rotated, v as it is.  E4M3 pools round k's fp32 values
+ * and v's bf16 ones once, by the rule of kvs_quantize_e4m3.  A token without a place (-1) has its q written and its K/V passed
+ * over; a place outside the pool is reported as KVS_ERR_BAD_INDEX and passed over. */
+kvs_status kvs_pool_rotate_append(kvs_pool* pool, const kvs_rope* rope, int layer, const void* d_q, long long q_stride,
+                                  const void* d_k, const void* d_v, long long kv_stride, const float* d_q_norm,
+                                  const float* d_k_norm, const int* d_pos, long long pos_stride, const long long* d_place,
+                                  int n_tok, void* d_q_out, long long q_out_stride, kvs_stream_t stream);
+
+/* Keys that kvs_pool_evict kept, from their old positions to their new ones: row i of request r and kv head h (in the blocks
+ * of block2slot, evict's dst2slot) is rotated, in place, by i - kept[r][h][i] positions, i < n_kept[r] <= keep, without rot_scale.  So that a
+ * cache that was cut down goes on at position n_kept[r], as lengths count.  kept [n_req][H_kv][keep]; the rope has one axis.  Slots of
+ * different (request, block) are distinct.  Rows that stay at their position are not written.  A count
+ * outside [0, keep] or a slot outside the pool is reported as KVS_ERR_BAD_INDEX and passed over. */
+kvs_status kvs_pool_reposition(kvs_pool* pool, const kvs_rope* rope, int layer, const int* d_kept, const int* d_n_kept,
+                               const int* d_block2slot, int n_req, int keep, kvs_stream_t stream);
+
 /* Library version string. */
 const char* kvs_version(void);
 

@@ -29,6 +29,8 @@ What it computes, written plainly (numpy, fp64 where the arithmetic is floating 
                HiSparse page, insight 1: outputs identical to full KV in HBM).
   pool         attention over one request's cached tokens (window, first tokens, shared prefix, summed
                weights) and the eviction rule of the device-resident pools.
+  rope         norms and rotation of query and key rows by their positions (pairs as complex numbers).
+  tables       block tables over a ring of free slots, and where a call's tokens go.
   step         one decode step over all layers: append, score, select, update, prefetch,
                attend -- sync mode and lookahead-draft mode.
 
@@ -45,11 +47,13 @@ from .cache import (UnitCache, UpdateResult, PrefetchResult, cache_restore, cach
                     layer_prefetch)
 from .attention import attend
 from .pool import pool_attend, pool_kept
+from .rope import rope_freqs, rope_rows
+from .tables import TableOracle
 from .step import OracleDecoder, UnitRecord
 
 __all__ = [
     "bf16_to_f32", "bf16_to_f64", "f32_to_bf16_rne", "kv_cache_bytes", "kv_cache_bytes_variant",
     "index_keys", "index_key_block", "index_minmax", "index_minmax_block", "block_scores", "block_scores_bound", "forced_blocks", "select_blocks", "UnitCache",
     "UpdateResult", "PrefetchResult", "cache_update", "cache_restore", "importance_key", "layer_prefetch", "attend", "OracleDecoder",
-    "UnitRecord", "pool_attend", "pool_kept",
+    "UnitRecord", "pool_attend", "pool_kept", "rope_freqs", "rope_rows", "TableOracle",
 ]

@@ -54,6 +54,12 @@ class KvsPoolConfig(ctypes.Structure):
                 ("wait_timeout_us", ctypes.c_uint)]
 
 
+class KvsRopeConfig(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int), ("rot_dim", ctypes.c_int), ("adjacent", ctypes.c_int), ("n_axis", ctypes.c_int),
+                ("axis", ctypes.POINTER(ctypes.c_ubyte)), ("inv_freq", ctypes.POINTER(ctypes.c_double)),
+                ("theta", ctypes.c_double), ("rot_scale", ctypes.c_float), ("norm_eps", ctypes.c_float)]
+
+
 STATS_FIELDS = [f[0] for f in KvsStats._fields_]
 
 _lib = None
@@ -97,6 +103,13 @@ _SIGS = {
     "kvs_pool_attn": (_I, [_P, _I, _P, _LL, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P]),
     "kvs_pool_prefix_attn": (_I, [_P, _I, _P, _LL, _P, _P, _P, _I, _I, _P, _P, _P, _I, _P, _P, _P]),
     "kvs_pool_evict": (_I, [_P, _I, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "kvs_pool_reserve": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _P, _P, _P]),
+    "kvs_pool_places": (_I, [_P, _P, _P, _P, _I, _I, _P, _P, _P, _P]),
+    "kvs_rope_create": (_I, [ctypes.POINTER(KvsRopeConfig), ctypes.POINTER(_P)]),
+    "kvs_rope_destroy": (_I, [_P]),
+    "kvs_rotate": (_I, [_P, _P, _LL, _LL, _I, _P, _P, _LL, _LL, _P, _LL, _LL, _I, _P, _P, _LL, _LL, _P, _LL, _I, _P]),
+    "kvs_pool_rotate_append": (_I, [_P, _P, _I, _P, _LL, _P, _P, _LL, _P, _P, _P, _LL, _P, _I, _P, _LL, _P]),
+    "kvs_pool_reposition": (_I, [_P, _P, _I, _P, _P, _P, _I, _I, _P]),
 }
 
 KERNEL_IDS = {"score": 1, "topk": 2, "update": 3, "fetch": 4, "attn": 5, "prefetch": 6, "append": 7, "index": 8}
@@ -485,7 +498,10 @@ def version() -> str:
 
 
 def __getattr__(name):   # the pool binding imports torch: on first use
-    if name in ("Pool", "make_pool_config"):
+    if name in ("Pool", "make_pool_config", "BlockTables"):
         from . import pool
         return getattr(pool, name)
+    if name in ("Rope", "make_rope_config", "rope_axes"):
+        from . import rope
+        return getattr(rope, name)
     raise AttributeError(name)

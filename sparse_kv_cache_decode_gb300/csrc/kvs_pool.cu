@@ -4,7 +4,7 @@
 #include <algorithm>
 #include <new>
 
-#include "kvs_pool.cuh"
+#include "kvs_rope.cuh"
 
 using namespace kvs;
 
@@ -23,6 +23,7 @@ struct kvs_pool {
 namespace {
 
 constexpr size_t kAlign = 256;
+constexpr int kTicketWord = 16;     // a counter of CTAs beside the status word, 0 between calls
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 // [a, a + na) and [b, b + nb) share a byte
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -80,7 +81,7 @@ struct PoolPlan {
 };
 PoolPlan pool_plan(const PoolDims& d) {
   PoolPlan p;
-  p.err = align_up(16);
+  p.err = align_up((kTicketWord + 1) * 4);
   p.lse2 = align_up((size_t)d.max_tokens * d.Hq * 4);
   p.prev_lse2 = align_up((size_t)d.max_prefix_tokens * d.Hq * 4);
   p.prev_out = align_up((size_t)d.max_prefix_tokens * d.Hq * d.d * 4);
@@ -313,6 +314,95 @@ kvs_status kvs_pool_evict(kvs_pool* c, int layer, const float* d_weight, const i
   return cuda_status(launch_pool_evict(d, c->k + layer * c->layer_bytes, c->v + layer * c->layer_bytes, d_weight, d_ctx_len,
                                        d_block2slot, n_req, keep, n_sink, n_recent, d_dst2slot, d_kept, d_n_kept,
                                        d_weight_out, c->err, S(stream)));
+} catch (...) {      // out of host memory
+  return KVS_ERR_CUDA;
+}
+
+kvs_status kvs_pool_reserve(kvs_pool* c, const int* d_ctx_len, int* d_n_held, int* d_block2slot, int* d_ring, int* d_ring_state,
+                            int n_req, const int* d_cu_q, const int* d_pos_delta, int n_tok, long long* d_place, int* d_pos,
+                            kvs_stream_t stream) try {
+  if (!call_ok(c, 0, n_req) || n_tok < 0 || n_tok > c->d.max_tokens) return KVS_ERR_INVALID_ARG;
+  if (n_req == 0) return KVS_OK;
+  if (!d_ctx_len || !d_n_held || !d_block2slot || !d_ring || !d_ring_state || d_ctx_len == d_n_held) return KVS_ERR_INVALID_ARG;
+  if (n_tok == 0) d_cu_q = nullptr;
+  if (n_tok > 0 && (!d_cu_q || !d_place)) return KVS_ERR_INVALID_ARG;
+  const PoolTables t = {d_ctx_len, d_n_held, d_block2slot, d_ring, d_ring_state, d_cu_q, d_pos_delta, d_place, d_pos, n_req, n_tok};
+  c->launches += 1;
+  return cuda_status(launch_pool_tables(c->d, t, c->err + kTicketWord, c->err, S(stream)));
+} catch (...) {      // out of host memory
+  return KVS_ERR_CUDA;
+}
+
+kvs_status kvs_pool_places(kvs_pool* c, const int* d_cu_q, const int* d_ctx_len, const int* d_block2slot, int n_req, int n_tok,
+                           const int* d_pos_delta, long long* d_place, int* d_pos, kvs_stream_t stream) try {
+  if (!call_ok(c, 0, n_req) || n_tok < 0 || n_tok > c->d.max_tokens) return KVS_ERR_INVALID_ARG;
+  if (n_req == 0 || n_tok == 0) return KVS_OK;
+  if (!d_cu_q || !d_ctx_len || !d_block2slot || !d_place) return KVS_ERR_INVALID_ARG;
+  const PoolTables t = {d_ctx_len, nullptr, const_cast<int*>(d_block2slot), nullptr, nullptr, d_cu_q, d_pos_delta, d_place, d_pos, n_req, n_tok};
+  c->launches += 1;
+  return cuda_status(launch_pool_tables(c->d, t, c->err + kTicketWord, c->err, S(stream)));
+} catch (...) {      // out of host memory
+  return KVS_ERR_CUDA;
+}
+
+kvs_status kvs_pool_rotate_append(kvs_pool* c, const kvs_rope* rope, int layer, const void* d_q, long long q_stride,
+                                  const void* d_k, const void* d_v, long long kv_stride, const float* d_q_norm,
+                                  const float* d_k_norm, const int* d_pos, long long pos_stride, const long long* d_place,
+                                  int n_tok, void* d_q_out, long long q_out_stride, kvs_stream_t stream) try {
+  if (!call_ok(c, layer, 0) || !rope || n_tok < 0 || n_tok > c->d.max_tokens || pos_stride < 0) return KVS_ERR_INVALID_ARG;
+  const PoolDims& d = c->d;
+  if (rope->d.d != d.d) return KVS_ERR_INVALID_ARG;
+  if (n_tok == 0) return KVS_OK;
+  if (!d_q || !d_k || !d_v || !d_pos || !d_place || !d_q_out) return KVS_ERR_INVALID_ARG;
+  const long long q_row = (long long)d.Hq * d.d, kv_row = (long long)d.Hkv * d.d;
+  if (q_stride % 8 || kv_stride % 8 || q_out_stride % 8 || q_stride < q_row || kv_stride < kv_row || q_out_stride < q_row)
+    return KVS_ERR_INVALID_ARG;
+  for (const void* x : {d_q, d_k, d_v, static_cast<const void*>(d_q_out), static_cast<const void*>(d_q_norm), static_cast<const void*>(d_k_norm)})
+    if (!aligned16(x)) return KVS_ERR_INVALID_ARG;
+  // rows are written while others are still read: q in place, or apart from q, k and v (columns of the same rows may be)
+  const bool in_place = d_q == d_q_out && q_stride == q_out_stride;
+  auto meets = [&](const void* x, long long stride, long long row) {
+    const size_t more = (size_t)(n_tok - 1) * 2;
+    if (!overlap(x, more * stride + row * 2, d_q_out, more * q_out_stride + q_row * 2)) return false;
+    if (stride != q_out_stride || n_tok == 1) return true;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(d_q_out);
+    const uintptr_t off = (a < b ? b - a : a - b) % (stride * 2), wa = (a < b ? row : q_row) * 2, wb = (a < b ? q_row : row) * 2;
+    return !(off >= wa && off + wb <= (uintptr_t)stride * 2);
+  };
+  if ((!in_place && meets(d_q, q_stride, q_row)) || meets(d_k, kv_stride, kv_row) || meets(d_v, kv_stride, kv_row)) return KVS_ERR_INVALID_ARG;
+  RopeRows a = {};
+  const long long head = d.d;
+  a.q = {static_cast<const __nv_bfloat16*>(d_q), static_cast<__nv_bfloat16*>(d_q_out), q_stride, head, q_out_stride, head, d_q_norm, d.Hq};
+  a.k = {static_cast<const __nv_bfloat16*>(d_k), nullptr, kv_stride, head, 0, 0, d_k_norm, d.Hkv};
+  a.v = {static_cast<const __nv_bfloat16*>(d_v), nullptr, kv_stride, head, 0, 0, nullptr, d.Hkv};
+  a.pos = d_pos;
+  a.pos_stride = pos_stride;
+  a.place = d_place;
+  a.kpool = c->k + layer * c->layer_bytes;
+  a.vpool = c->v + layer * c->layer_bytes;
+  a.n_slots = d.n_slots;
+  a.bs = d.bs;
+  a.log2bs = d.log2bs;
+  a.fp8 = d.fp8;
+  a.k_scale = d.k_scale;
+  a.v_scale = d.v_scale;
+  a.err = c->err;
+  a.n_tok = n_tok;
+  c->launches += 1;
+  return cuda_status(launch_rope_rows(rope->d, a, S(stream)));
+} catch (...) {      // out of host memory
+  return KVS_ERR_CUDA;
+}
+
+kvs_status kvs_pool_reposition(kvs_pool* c, const kvs_rope* rope, int layer, const int* d_kept, const int* d_n_kept,
+                               const int* d_block2slot, int n_req, int keep, kvs_stream_t stream) try {
+  if (!call_ok(c, layer, n_req) || !rope || rope->d.d != c->d.d || rope->d.n_axis != 1) return KVS_ERR_INVALID_ARG;
+  if (keep < 1 || keep > c->d.max_ctx) return KVS_ERR_INVALID_ARG;
+  if (n_req == 0) return KVS_OK;
+  if (!d_kept || !d_n_kept || !d_block2slot) return KVS_ERR_INVALID_ARG;
+  c->launches += 1;
+  return cuda_status(launch_pool_reposition(c->d, rope->d, c->k + layer * c->layer_bytes, d_kept, d_n_kept, d_block2slot, n_req, keep,
+                                            c->err, S(stream)));
 } catch (...) {      // out of host memory
   return KVS_ERR_CUDA;
 }

@@ -8,6 +8,9 @@ what the tensors are (ValueError) and forward to the C ABI (KvsError).  Tensors:
   q            [n_tok][H_q][d] bf16, contiguous within a token (a slice of a fused projection will do)
   cu_q         [n_req + 1] int32;  ctx_len [n_req] int32;  block2slot [n_req][nb_max] int32
   out          [n_tok][H_q][d] bf16;  lse [n_tok][H_q] fp32;  weight [n_req][H_kv][max_ctx] fp32
+  place        [n_tok] int64;  pos [n_axis][n_tok] or [n_tok] int32;  norms [d] fp32
+
+`BlockTables` keeps the block table of a batch over a pool and the ring of its free slots.
 """
 from __future__ import annotations
 
@@ -16,10 +19,11 @@ import ctypes
 import torch
 
 from . import KV_DTYPE, KvsError, KvsPoolConfig, _check, lib
+from .rope import Rope, _norm, _positions
 
 _BF16 = (torch.bfloat16, torch.int16)
 _FP8 = (torch.float8_e4m3fn, torch.uint8)
-_I32, _F32 = (torch.int32,), (torch.float32,)
+_I32, _I64, _F32 = (torch.int32,), (torch.int64,), (torch.float32,)
 
 
 def _int(x: int, name: str) -> int:
@@ -187,6 +191,47 @@ class Pool:
         self._call(self.L.kvs_pool_evict, "kvs_pool_evict", _int(layer, "layer"), w, ctx, tab, n_req, keep, _int(n_sink, "n_sink"),
                    _int(n_recent, "n_recent"), dst, kp, nk, wo, self._stream(stream))
 
+    def places(self, cu_q, ctx_len, block2slot, place, pos=None, pos_delta=None, stream=None):
+        """kvs_pool_places: where the call's tokens go (place [n_tok]) and their positions, from tables kept by the caller."""
+        n_req, cu, ctx, tab = self._batch(ctx_len, block2slot, cu_q)
+        n_tok, pl, po, de = self._tokens_out(n_req, place, pos, pos_delta)
+        self._call(self.L.kvs_pool_places, "kvs_pool_places", cu, ctx, tab, n_req, n_tok, de, pl, po, self._stream(stream))
+
+    def _tokens_out(self, n_req, place, pos, pos_delta):
+        n_tok = place.shape[0]
+        pl = self._whole(place, "place", _I64, (n_tok,))
+        po = None if pos is None else self._whole(pos, "pos", _I32, (n_tok,))
+        return n_tok, pl, po, None if pos_delta is None else self._whole(pos_delta, "pos_delta", _I32, (n_req,))
+
+    def _rope(self, rope):
+        if not isinstance(rope, Rope) or rope.h is None:
+            raise ValueError("rope: not an open Rope")
+        return rope.h
+
+    def rotate_append(self, layer, rope, q, k, v, pos, place, q_out, q_norm=None, k_norm=None, stream=None):
+        """kvs_pool_rotate_append: q [n_tok][H_q][d] normed and rotated into q_out; k and v [n_tok][H_kv][d] to their places, k normed and
+        rotated as well."""
+        c = self.cfg
+        qp, qs, n_tok = self._tokens(q, "q", c.n_q_head)
+        kp, ks, n_k = self._tokens(k, "k", c.n_kv_head)
+        vp, vs, n_v = self._tokens(v, "v", c.n_kv_head)
+        op, os, n_o = self._tokens(q_out, "q_out", c.n_q_head)
+        if n_k != n_tok or n_v != n_tok or n_o != n_tok or ks != vs:
+            raise ValueError("q, k, v and q_out: different numbers of tokens, or k and v of different strides")
+        h = self._rope(rope)
+        pp, ps = _positions(pos, rope.n_axis, n_tok, self.index)
+        pl = self._whole(place, "place", _I64, (n_tok,))
+        qn, kn = _norm(q_norm, "q_norm", c.head_dim, self.index), _norm(k_norm, "k_norm", c.head_dim, self.index)
+        self._call(self.L.kvs_pool_rotate_append, "kvs_pool_rotate_append", h, _int(layer, "layer"), qp, qs, kp, vp, ks, qn, kn, pp, ps, pl,
+                   n_tok, op, os, self._stream(stream))
+
+    def reposition(self, layer, rope, kept, n_kept, block2slot, stream=None):
+        """kvs_pool_reposition: the keys that `evict` kept (its kept, n_kept and dst2slot), rotated to their new positions."""
+        n_req, nk, tab = self._batch(n_kept, block2slot)
+        kp = self._whole(kept, "kept", _I32, (n_req, self.cfg.n_kv_head, kept.shape[-1]))
+        self._call(self.L.kvs_pool_reposition, "kvs_pool_reposition", self._rope(rope), _int(layer, "layer"), kp, nk, tab, n_req, kept.shape[-1],
+                   self._stream(stream))
+
     def launch_count(self) -> int:
         return int(self.L.kvs_pool_launch_count(self.h))
 
@@ -195,3 +240,41 @@ class Pool:
         with torch.cuda.device(self.device):
             _check(self.L.kvs_pool_poll_error(self.h, ctypes.byref(st)), "kvs_pool_poll_error")
         return st.value
+
+
+class BlockTables:
+    """The block table of a batch over a pool and the ring of the pool's free slots, kept in the caller's tensors:
+
+      block2slot [n_req][nb_max] int32;  n_held [n_req] int32, the blocks each row owns;  ring [n_slots] int32;  ring_state [3] int32
+
+    Several may share a ring (a batch, its shared prefixes, the blocks that an eviction gathers into)."""
+
+    def __init__(self, pool: Pool, block2slot, n_held, ring, ring_state):
+        self.pool, self.n_req = pool, block2slot.shape[0]
+        self._ptrs = (pool._whole(n_held, "n_held", _I32, (self.n_req,)),
+                      pool._whole(block2slot, "block2slot", _I32, (self.n_req, pool.nb_max)),
+                      pool._whole(ring, "ring", _I32, (pool.cfg.n_slots,)), pool._whole(ring_state, "ring_state", _I32, (3,)))
+        self.block2slot, self.n_held, self.ring, self.ring_state = block2slot, n_held, ring, ring_state
+
+    @classmethod
+    def empty(cls, pool: Pool, n_req: int, like: BlockTables | None = None):
+        """Rows without blocks over a pool whose slots are all free, or over the ring of `like`."""
+        i32 = dict(dtype=torch.int32, device=pool.device)
+        n = pool.cfg.n_slots
+        ring, state = (like.ring, like.ring_state) if like is not None else (torch.arange(n, **i32), torch.tensor([0, n, 0], **i32))
+        return cls(pool, torch.full((n_req, pool.nb_max), -1, **i32), torch.zeros(n_req, **i32), ring, state)
+
+    def reserve(self, ctx_len, cu_q=None, place=None, pos=None, pos_delta=None, stream=None):
+        """kvs_pool_reserve: every row gets the blocks of its new length, or gives back those past it; with cu_q and place also where the
+        call's tokens go, and their positions."""
+        p, n_req = self.pool, self.n_req
+        ctx = p._whole(ctx_len, "ctx_len", _I32, (n_req,))
+        cu = pl = po = de = None
+        n_tok = 0
+        if cu_q is not None and place is not None:
+            cu = p._whole(cu_q, "cu_q", _I32, (n_req + 1,))
+            n_tok, pl, po, de = p._tokens_out(n_req, place, pos, pos_delta)
+        elif cu_q is not None or place is not None or pos is not None or pos_delta is not None:
+            raise ValueError("cu_q and place: one without the other")
+        held, tab, ring, state = self._ptrs
+        p._call(p.L.kvs_pool_reserve, "kvs_pool_reserve", ctx, held, tab, ring, state, n_req, cu, de, n_tok, pl, po, p._stream(stream))
