@@ -4,6 +4,8 @@
 // rotated pair are in one lane: no exchange but the norm's sum.  Pair i of a row turns by pos * f_i.  The angle is kept in
 // turns, as an integer multiple of 2^-64: pos * f_i wraps around at whole turns by itself, exactly, for any 32-bit position
 // (fp32 products lose the angle beyond some thousand positions); its upper 32 bits are off by less than 2^-32 turns.
+#include <cuda_fp16.h>
+
 #include <algorithm>
 
 #include "kvs_ptx.cuh"
@@ -13,32 +15,43 @@ namespace kvs {
 
 namespace {
 
-// cos and sin of pos * f turns
-__device__ __forceinline__ void turn_cos_sin(int pos, unsigned long long f, float& c, float& s) {
-  const int t = (int)((unsigned long long)((long long)pos * (long long)f) >> 32);
-  sincospif((float)t * 0x1p-31f, &s, &c);
+// cos and sin of m * f turns, two of them.  The product's upper word, a turn's fraction, becomes a float by its upper 23 bits, rounded
+// (a conversion would take the unit that the cosines need); the fast functions are off by 2^-21 for arguments in [-pi, pi].
+// Together 2^-20 at most.
+__device__ __forceinline__ float turn_bits(unsigned m, unsigned long long f) {      // 1.5 + the fraction's distance from whole turns
+  const unsigned t = __umulhi(m, (unsigned)f) + (m * (unsigned)(f >> 32) + 0x80000100u);      // half a turn on, and half a step
+  return __uint_as_float((t >> 9) | 0x3f800000u);
 }
+__device__ __forceinline__ void turn_cos_sin(unsigned m, unsigned long long f0, unsigned long long f1, float2& c, float2& s) {
+  const float2 x = __fmul2_rn(__fadd2_rn(make_float2(turn_bits(m, f0), turn_bits(m, f1)), make_float2(-1.5f, -1.5f)), make_float2(6.2831853f, 6.2831853f));
+  c = make_float2(__cosf(x.x), __cosf(x.y));
+  s = make_float2(__sinf(x.x), __sinf(x.y));
+}
+__device__ __forceinline__ unsigned magnitude(int pos) { return pos < 0 ? 0u - (unsigned)pos : (unsigned)pos; }
+
+// Which elements are a pair: i and i + d / 2, i and i + rot / 2, or 2 i and 2 i + 1.
+enum { kHalves, kPart, kAdjacent };
 
 // What a lane holds of a row: chunks c0 and c1 (of 8 elements), and the pair of its j-th (a, b).
-template <int D, bool ADJ>
+template <int D, int LAY>
 struct LanePart {
   int c0, c1;
   __device__ __forceinline__ LanePart(int rot, int l) {
     const int n = rot / 16;
-    if (ADJ || n == D / 16) {
-      c0 = l;
-      c1 = l + D / 16;
-    } else if (l < n) {
-      c0 = l;
+    c0 = l;
+    c1 = l + D / 16;
+    if (LAY == kPart && l < n) {
       c1 = l + n;
-    } else {
+    } else if (LAY == kPart) {
       c0 = 2 * l;
       c1 = c0 + 1;
     }
   }
-  __device__ __forceinline__ int pair(int j) const { return ADJ ? (j < 4 ? 4 * c0 + j : 4 * c1 + j - 4) : 8 * c0 + j; }
+  // c1's distance, in chunks
+  __device__ __forceinline__ int apart() const { return LAY == kPart ? c1 - c0 : D / 16; }
+  __device__ __forceinline__ int pair(int j) const { return LAY == kAdjacent ? (j < 4 ? 4 * c0 + j : 4 * c1 + j - 4) : 8 * c0 + j; }
   // (the pair's number is past the rotated ones where the elements do not turn)
-  __device__ __forceinline__ bool turns(int j, int rot) const { return ADJ ? pair(j) < rot / 2 : c0 < rot / 16; }
+  __device__ __forceinline__ bool turns(int j, int rot) const { return LAY == kHalves || (LAY == kAdjacent ? pair(j) < rot / 2 : c0 < rot / 16); }
 };
 
 __device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
@@ -47,237 +60,609 @@ __device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
   return r;
 }
 
-// (a[j], b[j]) of two chunks, and back
-template <bool ADJ, typename T>
-__device__ __forceinline__ void to_pairs(const T (&x)[16], T (&a)[8], T (&b)[8]) {
+// A lane's pairs (a, b), two at a time: u = (a[2i], a[2i + 1]), v = (b[2i], b[2i + 1]).
+struct Pairs {
+  float2 u[4], v[4];
+};
+// ... of the elements x of its two chunks, and back
+template <int LAY>
+__device__ __forceinline__ Pairs to_pairs(const float (&x)[16]) {
+  constexpr bool ADJ = LAY == kAdjacent;
+  Pairs p;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    a[j] = ADJ ? x[2 * j] : x[j];
-    b[j] = ADJ ? x[2 * j + 1] : x[8 + j];
+  for (int i = 0; i < 4; ++i) {
+    p.u[i] = ADJ ? make_float2(x[4 * i], x[4 * i + 2]) : make_float2(x[2 * i], x[2 * i + 1]);
+    p.v[i] = ADJ ? make_float2(x[4 * i + 1], x[4 * i + 3]) : make_float2(x[8 + 2 * i], x[9 + 2 * i]);
   }
+  return p;
 }
-template <bool ADJ, typename T>
-__device__ __forceinline__ void from_pairs(const T (&a)[8], const T (&b)[8], T (&x)[16]) {
+template <int LAY>
+__device__ __forceinline__ void from_pairs(const Pairs& p, float (&x)[16]) {
+  constexpr bool ADJ = LAY == kAdjacent;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    x[ADJ ? 2 * j : j] = a[j];
-    x[ADJ ? 2 * j + 1 : 8 + j] = b[j];
+  for (int i = 0; i < 4; ++i) {
+    x[ADJ ? 4 * i : 2 * i] = p.u[i].x;
+    x[ADJ ? 4 * i + 2 : 2 * i + 1] = p.u[i].y;
+    x[ADJ ? 4 * i + 1 : 8 + 2 * i] = p.v[i].x;
+    x[ADJ ? 4 * i + 3 : 9 + 2 * i] = p.v[i].y;
   }
 }
 
-__device__ __forceinline__ void unpack_bf16(const uint4& x0, const uint4& x1, float (&x)[16]) {
-  const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+struct Raw {
+  uint4 c0, c1;
+};
+__device__ __forceinline__ void unpack_bf16(const Raw& r, float (&x)[16]) {
+  const uint32_t w[8] = {r.c0.x, r.c0.y, r.c0.z, r.c0.w, r.c1.x, r.c1.y, r.c1.z, r.c1.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     x[2 * i] = bf16_lo(w[i]);
     x[2 * i + 1] = bf16_hi(w[i]);
   }
 }
-__device__ __forceinline__ void pack_bf16(const float (&x)[16], uint4& x0, uint4& x1) {
+__device__ __forceinline__ Raw pack_bf16(const float (&x)[16]) {
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = f32x2_to_bf16x2(x[2 * i], x[2 * i + 1]);
-  x0 = make_uint4(w[0], w[1], w[2], w[3]);
-  x1 = make_uint4(w[4], w[5], w[6], w[7]);
+  return {make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])};
 }
 __device__ __forceinline__ uint2 pack_e4m3(const float* x) {
   return make_uint2(f32x2_to_e4m3x2(x[0], x[1]) | (f32x2_to_e4m3x2(x[2], x[3]) << 16),
                     f32x2_to_e4m3x2(x[4], x[5]) | (f32x2_to_e4m3x2(x[6], x[7]) << 16));
 }
 
-constexpr int kRopeThreads = 256;
 enum { kDense, kPoolBf16, kPoolFp8 };
 
-// One warp turns one token's heads (or a part of them: `parts` warps share a token), 32 / (d / 16) heads at a time.
-template <int D, bool ADJ, int DST>
-__global__ void __launch_bounds__(kRopeThreads)
-    rope_rows_kernel(const __grid_constant__ RopeDims rd, const __grid_constant__ RopeRows a, int parts) {
-  constexpr int LPH = D / 16, HPW = 32 / LPH;
-  const int lane = threadIdx.x & 31, sub = lane / LPH, l = lane % LPH;
-  const LanePart<D, ADJ> at(rd.rot, l);
-  unsigned long long freq[8];
-  int axis[8];
+// What a warp does with rows of d elements, 32 / (d / 16) heads (a step) at a time.
+template <int D, int LAY>
+struct RowWarp {
+  static constexpr int LPH = D / 16, HPW = 32 / LPH, NP = D / 64;
+  const int lane, sub;
+  const LanePart<D, LAY> at;
+  const int rot;
+  const float rot_scale, eps;
+  // (a, b) -> (a cw + b sw, b dw + a ew): the rotation and the norm's weights
+  float2 cw[4], sw[4], dw[4], ew[4];
+
+  __device__ __forceinline__ RowWarp(const RopeDims& rd)
+      : lane(threadIdx.x & 31), sub((threadIdx.x & 31) / LPH), at(rd.rot, (threadIdx.x & 31) % LPH), rot(rd.rot), rot_scale(rd.rot_scale), eps(rd.eps) {}
+
+  // cos and sin of every pair of the row, by all lanes, to shared memory
+  __device__ __forceinline__ void turns(const int (&pos)[NP], const unsigned long long (&freq)[NP], float2* turn) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const bool live = at.turns(j, rd.rot);
-    freq[j] = live ? rd.freq[at.pair(j)] : 0ull;      // (an angle of 0: cos 1, sin 0)
-    axis[j] = live ? rd.axis[at.pair(j)] : 0;
+    for (int j = 0; j < NP; ++j) {
+      const float x = (turn_bits(magnitude(pos[j]), freq[j]) - 1.5f) * 6.2831853f;
+      const float scale = lane + 32 * j < rot / 2 ? rot_scale : 1.f;
+      turn[lane + 32 * j] = make_float2(__cosf(x) * scale, __sinf(x) * (pos[j] < 0 ? -scale : scale));
+    }
+    __syncwarp();
   }
-  const float scale0 = at.turns(0, rd.rot) ? rd.rot_scale : 1.f, scale1 = at.turns(7, rd.rot) ? rd.rot_scale : 1.f;
+  struct Weights {
+    float4 y[4];
+  };
+  __device__ __forceinline__ Weights weights(const float* norm) const {
+    Weights w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w.y[j] = norm ? __ldg(reinterpret_cast<const float4*>(norm) + (j < 2 ? 2 * at.c0 + j : 2 * at.c1 + j - 2)) : make_float4(1.f, 1.f, 1.f, 1.f);
+    return w;
+  }
+  __device__ __forceinline__ void factors(const Weights& y, const float2* turn) {
+    float x[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[4 * j] = y.y[j].x;
+      x[4 * j + 1] = y.y[j].y;
+      x[4 * j + 2] = y.y[j].z;
+      x[4 * j + 3] = y.y[j].w;
+    }
+    const Pairs w = to_pairs<LAY>(x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // the rotated pairs' numbers, or any unrotated pair's (there are as many pairs as elements that do not turn)
+      const int n = LAY != kPart || at.turns(0, rot) ? at.pair(2 * i) : rot / 2;
+      const float4 t = *reinterpret_cast<const float4*>(turn + n);      // cos, sin, cos, sin
+      cw[i] = make_float2(t.x * w.u[i].x, t.z * w.u[i].y);
+      sw[i] = make_float2(-t.y * w.v[i].x, -t.w * w.v[i].y);
+      dw[i] = make_float2(t.x * w.v[i].x, t.z * w.v[i].y);
+      ew[i] = make_float2(t.y * w.u[i].x, t.w * w.u[i].y);
+    }
+  }
+  // the lane's part of a row, normed (if `norm`) and turned
+  __device__ __forceinline__ void row(const Raw& r, bool norm, float (&x)[16]) const {
+    unpack_bf16(r, x);
+    Pairs p = to_pairs<LAY>(x);
+    if (norm) {
+      float2 sum = __ffma2_rn(p.v[0], p.v[0], __fmul2_rn(p.u[0], p.u[0]));
+#pragma unroll
+      for (int i = 1; i < 4; ++i) sum = __ffma2_rn(p.v[i], p.v[i], __ffma2_rn(p.u[i], p.u[i], sum));
+      float s = sum.x + sum.y;
+#pragma unroll
+      for (int o = LPH / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const float inv = rsqrtf(s * (1.f / D) + eps);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p.u[i] = __fmul2_rn(p.u[i], make_float2(inv, inv));
+        p.v[i] = __fmul2_rn(p.v[i], make_float2(inv, inv));
+      }
+    }
+    Pairs y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y.u[i] = __ffma2_rn(p.v[i], sw[i], __fmul2_rn(p.u[i], cw[i]));
+      y.v[i] = __ffma2_rn(p.u[i], ew[i], __fmul2_rn(p.v[i], dw[i]));
+    }
+    if (LAY != kHalves && rot != D) {       // an element that does not turn owes nothing to its partner, which may be infinite
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!at.turns(2 * i, rot)) {
+          y.u[i] = __fmul2_rn(p.u[i], cw[i]);
+          y.v[i] = __fmul2_rn(p.v[i], dw[i]);
+        }
+    }
+    from_pairs<LAY>(y, x);
+  }
+  __device__ __forceinline__ void store_bf16(void* to, const Raw& r) const {
+    reinterpret_cast<uint4*>(to)[at.c0] = r.c0;
+    reinterpret_cast<uint4*>(to)[at.c1] = r.c1;
+  }
+  __device__ __forceinline__ void store_e4m3(void* to, float (&x)[16], float scale) const {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] = __fdiv_rn(x[j], scale);
+    reinterpret_cast<uint2*>(to)[at.c0] = pack_e4m3(x);
+    reinterpret_cast<uint2*>(to)[at.c1] = pack_e4m3(x + 8);
+  }
+  __device__ __forceinline__ static const uint4* from(const RopeHeads& g, int tok, int h) {
+    return reinterpret_cast<const uint4*>(g.src + tok * g.src_tok + h * g.src_head);
+  }
+  __device__ __forceinline__ static void* dense(const RopeHeads& g, int tok, int h) { return g.dst + tok * g.dst_tok + h * g.dst_head; }
+};
+
+// Where a token's K/V rows go: its row in head 0 of its slot.
+struct PlaceRow {
+  size_t row;
+  bool there;
+};
+__device__ __forceinline__ PlaceRow place_row(const RopeRows& a, long long place) {
+  PlaceRow p;
+  p.there = place >= 0 && place < ((long long)a.n_slots << a.log2bs);
+  if (place >= 0 && !p.there) set_error(a.err, KVS_ERR_BAD_INDEX);
+  p.row = (size_t)(place >> a.log2bs) * a.k.n * a.bs + (place & (a.bs - 1));
+  return p;
+}
+
+// Few tokens: a warp per step, everything it needs on its way at once.  One token of 32 + 2 x 8 heads: 1.7 us (3.3 with a loop over
+// the steps of a token).  From about 20 steps for each SM on the other kernel's sharing of a token's angles and its deeper queue win: at
+// 256 tokens (3072 steps) 4.3 us here and 4.5 there, at 512 7.9 and 5.1; of 3 steps each, at 1024 tokens 3.1 and 3.3, at 2048 4.9 and 4.1.
+constexpr int kFewThreads = 128;
+constexpr int kFewSteps = 20;      // steps for each SM, at most
+
+template <int D, int LAY, int DST>
+__global__ void __launch_bounds__(kFewThreads)
+    rope_few_kernel(const __grid_constant__ RopeDims rd, const __grid_constant__ RopeRows a, int iq, int ik, int steps) {
+  using W = RowWarp<D, LAY>;
+  __shared__ __align__(16) float2 cos_sin[kFewThreads / 32][D / 2];
+  W w(rd);
+  float2* turn = cos_sin[threadIdx.x >> 5];
+  unsigned long long freq[W::NP];
+  int pos[W::NP];
+#pragma unroll
+  for (int j = 0; j < W::NP; ++j) {
+    freq[j] = rd.freq[w.lane + 32 * j];      // (past the rotated pairs: an angle of 0)
+    pos[j] = rd.axis[w.lane + 32 * j];
+  }
+  const long long item = (long long)blockIdx.x * (kFewThreads / 32) + (threadIdx.x >> 5);
+  const int tok = (int)(item / steps), it = (int)(item - (long long)tok * steps);
   kvs_pdl_entry();
-  const int iq = (a.q.n + HPW - 1) / HPW, ik = (a.k.n + HPW - 1) / HPW, steps = iq + ik + (DST == kDense ? 0 : ik);
-  const int per = (steps + parts - 1) / parts;
-  const long long items = (long long)a.n_tok * parts, n_warps = (long long)gridDim.x * (kRopeThreads / 32);
-  for (long long item = (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); item < items; item += n_warps) {
-    const int tok = (int)(item / parts), first = (int)(item - (long long)tok * parts) * per, last = min(steps, first + per);
-    float cs[8], sn[8];
-    if (first < iq + ik) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        turn_cos_sin(a.pos[axis[j] * a.pos_stride + tok], freq[j], cs[j], sn[j]);
-        const float sc = j < 4 ? scale0 : scale1;
-        cs[j] *= sc;
-        sn[j] *= sc;
-      }
-    }
-    size_t row = 0;        // the token's row in head 0 of its slot
-    bool stored = true;
-    if (DST != kDense && last > iq) {
-      const long long p = a.place[tok];
-      stored = p >= 0 && p < ((long long)a.n_slots << a.log2bs);
-      if (p >= 0 && !stored) set_error(a.err, KVS_ERR_BAD_INDEX);
-      row = (size_t)(p >> a.log2bs) * a.k.n * a.bs + (p & (a.bs - 1));
-    }
-    for (int it = first; it < last; ++it) {
-      const bool is_q = it < iq, is_v = it >= iq + ik;
-      const RopeHeads& g = is_q ? a.q : is_v ? a.v : a.k;
-      const int h = (it - (is_q ? 0 : is_v ? iq + ik : iq)) * HPW + sub;
-      const bool there = h < g.n;
-      uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-      if (there) {
-        const __nv_bfloat16* src = g.src + tok * g.src_tok + h * g.src_head;
-        x0 = __ldcs(reinterpret_cast<const uint4*>(src) + at.c0);
-        x1 = __ldcs(reinterpret_cast<const uint4*>(src) + at.c1);
-      }
+  if (tok >= a.n_tok) return;
+  const bool is_q = it < iq, is_v = it >= iq + ik;
+  long long place = -1;
+  if (DST != kDense && !is_q) place = a.place[tok];
+  const int h = (is_q ? it : is_v ? it - iq - ik : it - iq) * W::HPW + w.sub;
+  const bool there = h < (is_q ? a.q.n : a.k.n);
+  Raw raw = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  if (there) {
+    const uint4* src = is_q ? W::from(a.q, tok, h) : is_v ? W::from(a.v, tok, h) : W::from(a.k, tok, h);
+    raw.c0 = __ldcs(src + w.at.c0);
+    raw.c1 = __ldcs(src + w.at.c1);
+  }
+  if (DST != kDense && is_v) {
+    const PlaceRow p = place_row(a, place);
+    if (!there || !p.there) return;
+    unsigned char* to = a.vpool + (p.row + (size_t)h * a.bs) * (DST == kPoolFp8 ? D : 2 * D);
+    if (DST == kPoolFp8) {
       float x[16];
-      if (!is_v || DST == kPoolFp8) unpack_bf16(x0, x1, x);
-      if (!is_v) {
-        if (g.norm) {
-          float sum = 0.f;
+      unpack_bf16(raw, x);
+      w.store_e4m3(to, x, a.v_scale);
+    } else {
+      w.store_bf16(to, raw);
+    }
+    return;
+  }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) sum = fmaf(x[j], x[j], sum);
+  for (int j = 0; j < W::NP; ++j) pos[j] = a.pos[pos[j] * a.pos_stride + tok];
+  const float* norm = is_q ? a.q.norm : a.k.norm;
+  const typename W::Weights weights = w.weights(norm);
+  w.turns(pos, freq, turn);
+  w.factors(weights, turn);
+  float x[16];
+  w.row(raw, norm != nullptr, x);
+  if (DST == kDense || is_q) {
+    if (there) w.store_bf16(is_q ? W::dense(a.q, tok, h) : W::dense(a.k, tok, h), pack_bf16(x));
+    return;
+  }
+  const PlaceRow p = place_row(a, place);
+  if (!there || !p.there) return;
+  unsigned char* to = a.kpool + (p.row + (size_t)h * a.bs) * (DST == kPoolFp8 ? D : 2 * D);
+  if (DST == kPoolFp8) w.store_e4m3(to, x, a.k_scale);
+  else w.store_bf16(to, pack_bf16(x));
+}
+
+// Many tokens: the warps take whole tokens in turn, then equal runs of the steps left over.  The steps' rows come through a ring in
+// shared memory, kStages - 1 steps ahead, in which every lane reads what it has copied itself.
+//
+// Bound by the rows' bytes, 3 KB on their way a warp; the norm's weights and the rotation are one set of factors, made once for a token's
+// queries and once for its keys, so that a row costs 8 multiplications and 16 fused ones for 16 elements (in pairs).
+// 16384 tokens of 32 + 2 x 8 heads of 128 into a bf16 pool: 66 us, 6.1 TB/s (59.3 at the rate of a copy).  Rows loaded into registers a
+// step ahead took 83 us, three steps ahead 70; every warp at a run of its own (far from its neighbours') 70; 3 CTAs an SM with
+// 80 registers 75.  11308 tokens of 28 + 4 heads, no norm: 31 us (27.3).
+constexpr int kRopeThreads = 256;
+constexpr int kStages = 4;
+constexpr int kRopeCtas = 2;       // of an SM
+
+__device__ __forceinline__ void cp_async16_at(uint32_t smem, const void* gmem, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;\n" ::"r"(smem), "l"(gmem), "l"(policy) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int D, int LAY, int DST>
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
+    rope_rows_kernel(const __grid_constant__ RopeDims rd, const __grid_constant__ RopeRows a, int iq, int ik, int steps) {
+  using W = RowWarp<D, LAY>;
+  constexpr int NW = kRopeThreads / 32;
+  __shared__ __align__(16) float2 cos_sin[NW][D / 2];
+  extern __shared__ __align__(16) uint4 ring_all[];     // [warps][kStages][2][32]
+  W w(rd);
+  float2* turn = cos_sin[threadIdx.x >> 5];
+  const uint32_t ring_base = smem_u32(ring_all + (threadIdx.x >> 5) * (kStages * 64) + w.lane);
+  unsigned long long freq[W::NP];
+  int axis[W::NP];
 #pragma unroll
-          for (int o = LPH / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          const float inv = rsqrtf(sum * (1.f / D) + rd.eps);
-          const float4* w = reinterpret_cast<const float4*>(g.norm);
+  for (int j = 0; j < W::NP; ++j) {
+    freq[j] = rd.freq[w.lane + 32 * j];      // (past the rotated pairs: an angle of 0)
+    axis[j] = rd.axis[w.lane + 32 * j];
+  }
+  const int ir = iq + ik;
+  // The warp's tokens: every n_warps-th one, so that all warps are at neighbours, then an equal run of the steps of those left over.
+  const int n_warps = gridDim.x * NW, me = blockIdx.x * NW + (threadIdx.x >> 5);
+  int rounds = a.n_tok / n_warps;
+  const long long rest = (long long)(a.n_tok - rounds * n_warps) * steps;
+  const int s0 = (int)(rest * me / n_warps), s1 = (int)(rest * (me + 1) / n_warps);
+  const int rest_tok = rounds * n_warps + s0 / steps, rest_it = s0 % steps;
+  int left = rounds * steps + s1 - s0, tok = rounds ? me : rest_tok, it = rounds ? 0 : rest_it;
+  auto go_on = [&](int& tok, int& it, int& rounds) {      // from a token's last step to the next token's first one
+    it = rounds == 1 ? rest_it : 0;
+    tok = rounds > 1 ? tok + n_warps : rounds == 1 ? rest_tok : tok + 1;
+    rounds = max(0, rounds - 1);
+  };
+  kvs_pdl_entry();
+  if (left == 0) return;
+  // Fetching: the next step's rows into the ring (past the run's end: nothing, an empty group).  ahead_src: the lane's row of the next
+  // step, ahead_h: its head, of ahead_n heads of queries, keys or values.
+  int ahead = left, ahead_tok = tok, ahead_it = it, ahead_rounds = rounds, ahead_h = 0, ahead_n = 0;
+  const uint4* ahead_src = nullptr;
+  long long ahead_step = 0;
+  auto aim = [&]() {      // at the heads of step ahead_it
+    if (ahead_it < iq) {
+      ahead_h = ahead_it * W::HPW + w.sub;
+      ahead_n = a.q.n;
+      ahead_src = W::from(a.q, ahead_tok, ahead_h);
+      ahead_step = a.q.src_head * W::HPW / 8;
+    } else if (ahead_it < ir) {
+      ahead_h = (ahead_it - iq) * W::HPW + w.sub;
+      ahead_n = a.k.n;
+      ahead_src = W::from(a.k, ahead_tok, ahead_h);
+      ahead_step = a.k.src_head * W::HPW / 8;
+    } else {
+      ahead_h = (ahead_it - ir) * W::HPW + w.sub;
+      ahead_n = a.k.n;
+      ahead_src = W::from(a.v, ahead_tok, ahead_h);
+      ahead_step = a.v.src_head * W::HPW / 8;
+    }
+    ahead_src += w.at.c0;
+  };
+  aim();
+  uint64_t once;      // rows are read once: what is written stays in L2 instead, for the attention
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+  auto fetch = [&](uint32_t to) {
+    if (ahead > 0) {
+      if (ahead_h < ahead_n) {
+        cp_async16_at(to, ahead_src, once);
+        cp_async16_at(to + 512, ahead_src + w.at.apart(), once);
+      }
+      --ahead;
+      ++ahead_it;
+      ahead_h += W::HPW;
+      ahead_src += ahead_step;
+      if (ahead_it == iq || ahead_it >= ir) {      // other heads, or the next token's
+        const bool through = ahead_it == steps;
+        if (through) go_on(ahead_tok, ahead_it, ahead_rounds);
+        if (ahead > 0 && (through || ahead_it == iq || ahead_it == ir)) aim();
+      }
+    }
+    cp_async_commit();
+  };
+  int pos[W::NP];
+  long long place = -1;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 y = __ldg(w + (j < 2 ? 2 * at.c0 + j : 2 * at.c1 + j - 2));
-            x[4 * j] *= inv * y.x;
-            x[4 * j + 1] *= inv * y.y;
-            x[4 * j + 2] *= inv * y.z;
-            x[4 * j + 3] *= inv * y.w;
+  for (int j = 0; j < W::NP; ++j) pos[j] = a.pos[axis[j] * a.pos_stride + tok];
+  if (DST != kDense) place = a.place[tok];
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(ring_base + i * 1024);
+  uint32_t slot = 0;
+  // the next step's rows, out of the ring, and another fetch into the slot before it
+  auto arrive = [&]() {
+    cp_async_wait<kStages - 2>();
+    const Raw raw = {ld_shared16(ring_base + slot), ld_shared16(ring_base + slot + 512)};
+    fetch(ring_base + ((slot + (kStages - 1) * 1024) & (kStages * 1024 - 1)));
+    slot = (slot + 1024) & (kStages * 1024 - 1);
+    return raw;
+  };
+  while (true) {
+    const int last = min(steps, it + left);
+    left -= last - it;
+    // the next token's positions come while this one's rows are turned
+    int next = tok, next_it = 0;
+    if (left) go_on(next, next_it, rounds);
+    int next_pos[W::NP];
+    long long next_place = -1;
+#pragma unroll
+    for (int j = 0; j < W::NP; ++j) next_pos[j] = a.pos[axis[j] * a.pos_stride + next];
+    if (DST != kDense) next_place = a.place[next];
+    if (it < ir) {
+      __syncwarp();       // (the last token's factors are read)
+      w.turns(pos, freq, turn);
+    }
+    if (it < iq) {
+      w.factors(w.weights(a.q.norm), turn);
+      int h = it * W::HPW + w.sub;
+      __nv_bfloat16* to = a.q.dst + tok * a.q.dst_tok + h * a.q.dst_head;
+      for (const int end = min(last, iq); it < end; ++it, h += W::HPW, to += a.q.dst_head * W::HPW) {
+        float x[16];
+        w.row(arrive(), a.q.norm != nullptr, x);
+        if (h < a.q.n) w.store_bf16(to, pack_bf16(x));
+      }
+    }
+    if (it < last) {
+      PlaceRow pl = {0, false};
+      if (DST != kDense) pl = place_row(a, place);
+      constexpr int ROW = DST == kPoolFp8 ? D : 2 * D;       // bytes of a row in the pool
+      if (it < ir) {
+        w.factors(w.weights(a.k.norm), turn);
+        int h = (it - iq) * W::HPW + w.sub;
+        __nv_bfloat16* to = a.k.dst + tok * a.k.dst_tok + h * a.k.dst_head;
+        unsigned char* in_pool = a.kpool + (pl.row + (size_t)h * a.bs) * ROW;
+        for (const int end = min(last, ir); it < end; ++it, h += W::HPW, to += a.k.dst_head * W::HPW, in_pool += W::HPW * a.bs * ROW) {
+          float x[16];
+          w.row(arrive(), a.k.norm != nullptr, x);
+          if (DST == kDense) {
+            if (h < a.k.n) w.store_bf16(to, pack_bf16(x));
+          } else if (h < a.k.n && pl.there) {
+            if (DST == kPoolFp8) w.store_e4m3(in_pool, x, a.k_scale);
+            else w.store_bf16(in_pool, pack_bf16(x));
           }
         }
-        float u[8], v[8], p[8], r[8];
-        to_pairs<ADJ>(x, u, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          p[j] = u[j] * cs[j] - v[j] * sn[j];
-          r[j] = v[j] * cs[j] + u[j] * sn[j];
-        }
-        from_pairs<ADJ>(p, r, x);
-        if (is_q || DST != kPoolFp8) pack_bf16(x, x0, x1);
       }
-      if (DST == kDense || is_q) {
-        if (there) {
-          uint4* dst = reinterpret_cast<uint4*>(g.dst + tok * g.dst_tok + h * g.dst_head);
-          dst[at.c0] = x0;
-          dst[at.c1] = x1;
-        }
-      } else if (there && stored) {
-        unsigned char* dst = (is_v ? a.vpool : a.kpool) + (row + (size_t)h * a.bs) * (DST == kPoolFp8 ? D : 2 * D);
-        if (DST == kPoolBf16) {
-          reinterpret_cast<uint4*>(dst)[at.c0] = x0;
-          reinterpret_cast<uint4*>(dst)[at.c1] = x1;
-        } else {
-          const float scale = is_v ? a.v_scale : a.k_scale;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) x[j] = __fdiv_rn(x[j], scale);
-          reinterpret_cast<uint2*>(dst)[at.c0] = pack_e4m3(x);
-          reinterpret_cast<uint2*>(dst)[at.c1] = pack_e4m3(x + 8);
+      if (DST != kDense) {
+        int h = (it - ir) * W::HPW + w.sub;
+        unsigned char* in_pool = a.vpool + (pl.row + (size_t)h * a.bs) * ROW;
+        for (; it < last; ++it, h += W::HPW, in_pool += W::HPW * a.bs * ROW) {
+          const Raw raw = arrive();
+          if (h < a.k.n && pl.there) {
+            if (DST == kPoolFp8) {
+              float x[16];
+              unpack_bf16(raw, x);
+              w.store_e4m3(in_pool, x, a.v_scale);
+            } else {
+              w.store_bf16(in_pool, raw);
+            }
+          }
         }
       }
     }
+    if (!left) break;
+    it = next_it;
+    tok = next;
+    place = next_place;
+#pragma unroll
+    for (int j = 0; j < W::NP; ++j) pos[j] = next_pos[j];
   }
 }
 
-// One warp turns 32 / (d / 16) kept keys of a (request, kv head) at a time, in place, each by its own angles.
+// A warp turns 32 / (d / 16) kept keys of a (request, kv head) a step, in place, each by its own angles, and goes on to the next ones,
+// `run` steps in all.  Rows come through a ring as above, their old positions and slots a step before them.
+//
+// Every key has angles of its own: 16 cosines and sines a lane and step, at 16 a clock of an SM 32 clocks, beside which some 190
+// instructions a step take 48 of each scheduler's: more than an 8-bit row's bytes (a step's 1 KB: 44 clocks at the rate of a copy).
+// 32 x 8 heads x 4096 keys of 128, E4M3: 64.0 us (40.2 for the bytes); one step a warp took 132, four at once and no ring 74.
+// 8 x 8 x 2048, bf16, half of them in L2: 6.9 us.
 constexpr int kRepThreads = 128;
+constexpr int kRepStages = 4;
+constexpr int kRepRun = 16;        // steps of a warp, at most
 
-template <int D, bool ADJ, bool FP8>
-__global__ void __launch_bounds__(kRepThreads)
+__device__ __forceinline__ void cp_async8_at(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(smem), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void cp_async16_at(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ uint2 ld_shared8(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+// Two E4M3 codes as fp32 (exact)
+__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint16_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
+template <int D, int LAY, bool FP8>
+__global__ void __launch_bounds__(kRepThreads, 6)
     pool_reposition_kernel(PoolDims d, const __grid_constant__ RopeDims rd, unsigned char* kpool, const int* __restrict__ kept,
-                           const int* __restrict__ n_kept, const int* __restrict__ table, int keep, unsigned* err) {
-  constexpr int LPH = D / 16, HPW = 32 / LPH;
+                           const int* __restrict__ n_kept, const int* __restrict__ table, int keep, int run, unsigned* err) {
+  constexpr int LPH = D / 16, HPW = 32 / LPH, ROW = FP8 ? D : 2 * D, CH = FP8 ? 8 : 16, S = kRepStages;      // CH: bytes of a chunk
+  __shared__ __align__(16) unsigned char ring_all[kRepThreads / 32][S][2][32 * CH];
+  __shared__ int2 what_all[kRepThreads / 32][S][32];      // positions to turn by, and the row's number in the layer
   const int lane = threadIdx.x & 31, sub = lane / LPH, l = lane % LPH;
-  const LanePart<D, ADJ> at(rd.rot, l);
+  const LanePart<D, LAY> at(rd.rot, l);
+  const uint32_t ring = smem_u32(&ring_all[threadIdx.x >> 5][0][0][lane * CH]);
+  int2* what = &what_all[threadIdx.x >> 5][0][lane];
   unsigned long long freq[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) freq[j] = at.turns(j, rd.rot) ? rd.freq[at.pair(j)] : 0ull;
-  kvs_pdl_entry();
+  for (int j = 0; j < 8; ++j) {
+    freq[j] = at.turns(j, rd.rot) ? rd.freq[at.pair(j)] : 0ull;
+    asm volatile("" : "+l"(freq[j]));      // (kept, not read from the parameters again each step)
+  }
   const int u = blockIdx.y, r = u / d.Hkv, h = u - r * d.Hkv;
+  const int first = (blockIdx.x * (kRepThreads / 32) + (threadIdx.x >> 5)) * run * HPW;
+  kept += (size_t)u * keep;
+  table += (size_t)r * d.nb_max;
+  unsigned char* const pool = kpool + at.c0 * CH;
+  kvs_pdl_entry();
   const int n = n_kept[r];
   if (n < 0 || n > keep) {
     if (threadIdx.x == 0) set_error(err, KVS_ERR_BAD_INDEX);
     return;
   }
-  const int i = (blockIdx.x * (kRepThreads / 32) + (threadIdx.x >> 5)) * HPW + sub;
-  if (i >= n) return;
-  const int by = (int)((unsigned)i - (unsigned)kept[(size_t)u * keep + i]);
-  if (by == 0) return;
-  const int slot = table[(size_t)r * d.nb_max + (i >> d.log2bs)];
-  if (slot < 0 || slot >= d.n_slots) {
-    set_error(err, KVS_ERR_BAD_INDEX);
-    return;
-  }
-  unsigned char* row = kpool + (((size_t)slot * d.Hkv + h) * d.bs + (i & (d.bs - 1))) * (FP8 ? D : 2 * D);
-  float x[16];
-  if (FP8) {
-    const uint2 a = reinterpret_cast<const uint2*>(row)[at.c0], b = reinterpret_cast<const uint2*>(row)[at.c1];
-    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+  const int end = min(n, first + run * HPW);
+  if (first >= end) return;
+  const int steps = (end - first + HPW - 1) / HPW;
+  // a step's old positions and slots come one step before its rows
+  int by = 0, slot = 0, i = first + sub;
+  auto find = [&]() {
+    by = 0;
+    if (i < end) {
+      by = i - kept[i];
+      slot = table[i >> d.log2bs];
+    }
+  };
+  find();
+  auto fetch = [&](int to) {
+    int2 w = make_int2(by, -1);
+    if (by != 0) {
+      if ((unsigned)slot < (unsigned)d.n_slots) {
+        w.y = (slot * d.Hkv + h) * d.bs + (i & (d.bs - 1));
+        const unsigned char* p = pool + (size_t)(unsigned)w.y * ROW;
+        if (FP8) {
+          cp_async8_at(ring + to * (64 * CH), p);
+          cp_async8_at(ring + to * (64 * CH) + 32 * CH, p + at.apart() * CH);
+        } else {
+          cp_async16_at(ring + to * (64 * CH), p);
+          cp_async16_at(ring + to * (64 * CH) + 32 * CH, p + at.apart() * CH);
+        }
+      } else {
+        set_error(err, KVS_ERR_BAD_INDEX);
+      }
+    }
+    what[to * 32] = w;
+    i += HPW;
+    find();
+    cp_async_commit();
+  };
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = e4m3_to_f32((w[j >> 2] >> ((j & 3) * 8)) & 255u);
-  } else {
-    unpack_bf16(reinterpret_cast<const uint4*>(row)[at.c0], reinterpret_cast<const uint4*>(row)[at.c1], x);
-  }
-  float p[8], q[8];
-  to_pairs<ADJ>(x, p, q);
+  for (int j = 0; j < S - 1; ++j) fetch(j);
+  int at_slot = 0;
+  for (int it = 0; it < steps; ++it) {
+    cp_async_wait<S - 2>();
+    const int2 w = what[at_slot * 32];
+    float x[16];
+    if (FP8) {
+      const uint2 a = ld_shared8(ring + at_slot * (64 * CH)), b = ld_shared8(ring + at_slot * (64 * CH) + 32 * CH);
+      const uint32_t c[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float c, s;
-    turn_cos_sin(by, freq[j], c, s);
-    const float y = p[j] * c - q[j] * s;
-    q[j] = q[j] * c + p[j] * s;
-    p[j] = y;
+      for (int k = 0; k < 8; ++k) {
+        const float2 y = e4m3x2_to_f32x2((uint16_t)(c[k >> 1] >> ((k & 1) * 16)));
+        x[2 * k] = y.x;
+        x[2 * k + 1] = y.y;
+      }
+    } else {
+      unpack_bf16({ld_shared16(ring + at_slot * (64 * CH)), ld_shared16(ring + at_slot * (64 * CH) + 32 * CH)}, x);
+    }
+    fetch((at_slot + S - 1) % S);
+    at_slot = (at_slot + 1) % S;
+    const Pairs p = to_pairs<LAY>(x);
+    Pairs y;
+    const unsigned m = magnitude(w.x);
+    const float sign = w.x < 0 ? -1.f : 1.f;      // (of the sines)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float2 c, s;
+      turn_cos_sin(m, freq[2 * k], freq[2 * k + 1], c, s);
+      y.u[k] = __ffma2_rn(__fmul2_rn(p.v[k], make_float2(-sign, -sign)), s, __fmul2_rn(p.u[k], c));
+      y.v[k] = __ffma2_rn(__fmul2_rn(p.u[k], make_float2(sign, sign)), s, __fmul2_rn(p.v[k], c));
+      if (LAY != kHalves && !at.turns(2 * k, rd.rot)) {      // (owes nothing to its partner, which may be infinite)
+        y.u[k] = p.u[k];
+        y.v[k] = p.v[k];
+      }
+    }
+    from_pairs<LAY>(y, x);
+    if (w.y >= 0) {
+      unsigned char* to = pool + (size_t)(unsigned)w.y * ROW;
+      if (FP8) {
+        *reinterpret_cast<uint2*>(to) = pack_e4m3(x);
+        *reinterpret_cast<uint2*>(to + at.apart() * CH) = pack_e4m3(x + 8);
+      } else {
+        const Raw z = pack_bf16(x);
+        *reinterpret_cast<uint4*>(to) = z.c0;
+        *reinterpret_cast<uint4*>(to + at.apart() * CH) = z.c1;
+      }
+    }
   }
-  from_pairs<ADJ>(p, q, x);
-  if (FP8) {
-    reinterpret_cast<uint2*>(row)[at.c0] = pack_e4m3(x);
-    reinterpret_cast<uint2*>(row)[at.c1] = pack_e4m3(x + 8);
-  } else {
-    uint4 a, b;
-    pack_bf16(x, a, b);
-    reinterpret_cast<uint4*>(row)[at.c0] = a;
-    reinterpret_cast<uint4*>(row)[at.c1] = b;
+}
+
+template <int D, int LAY, int DST>
+cudaError_t launch_rows(const RopeDims& rd, const RopeRows& a, cudaStream_t s) {
+  constexpr int HPW = 32 / (D / 16);
+  const int sms = device_sm_count();
+  const int iq = (a.q.n + HPW - 1) / HPW, ik = (a.k.n + HPW - 1) / HPW, steps = iq + ik * (DST == kDense ? 1 : 2);
+  const long long warps = (long long)a.n_tok * steps;
+  if (warps <= (long long)sms * kFewSteps) {
+    const int grid = (int)((warps + kFewThreads / 32 - 1) / (kFewThreads / 32));
+    launch_pdl(rope_few_kernel<D, LAY, DST>, dim3(grid), dim3(kFewThreads), 0, s, rd, a, iq, ik, steps);
+    return cudaGetLastError();
   }
+  constexpr int NW = kRopeThreads / 32;
+  const int grid = std::min((int)std::min<long long>((warps + NW - 1) / NW, 1 << 20), sms * kRopeCtas), smem = kRopeThreads * kStages * 32;
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(rope_rows_kernel<D, LAY, DST>), smem);
+  if (e != cudaSuccess) return e;
+  launch_pdl(rope_rows_kernel<D, LAY, DST>, dim3(grid), dim3(kRopeThreads), (size_t)smem, s, rd, a, iq, ik, steps);
+  return cudaGetLastError();
 }
 
 template <int D, int DST>
 cudaError_t launch_rows(const RopeDims& rd, const RopeRows& a, cudaStream_t s) {
-  constexpr int HPW = 32 / (D / 16), NW = kRopeThreads / 32;
-  const int steps = (a.q.n + HPW - 1) / HPW + (a.k.n + HPW - 1) / HPW * (DST == kDense ? 1 : 2);
-  const int sms = device_sm_count();
-  const long long want = (long long)sms * NW * 3;
-  const int parts = (int)std::max(1ll, std::min<long long>(steps, want / a.n_tok));
-  const long long ctas = ((long long)a.n_tok * parts + NW - 1) / NW;
-  const int grid = (int)std::min<long long>(ctas, (long long)sms * 8);
-  if (rd.adjacent)
-    launch_pdl(rope_rows_kernel<D, true, DST>, dim3(grid), dim3(kRopeThreads), 0, s, rd, a, parts);
-  else
-    launch_pdl(rope_rows_kernel<D, false, DST>, dim3(grid), dim3(kRopeThreads), 0, s, rd, a, parts);
-  return cudaGetLastError();
+  if (rd.adjacent) return launch_rows<D, kAdjacent, DST>(rd, a, s);
+  return rd.rot == D ? launch_rows<D, kHalves, DST>(rd, a, s) : launch_rows<D, kPart, DST>(rd, a, s);
 }
 
 template <int D, bool FP8>
 cudaError_t launch_reposition(const PoolDims& d, const RopeDims& rd, unsigned char* k, const int* kept, const int* n_kept, const int* table,
                               int n_req, int keep, unsigned* err, cudaStream_t s) {
-  constexpr int SPAN = kRepThreads / 32 * (32 / (D / 16));
-  const dim3 grid((keep + SPAN - 1) / SPAN, n_req * d.Hkv);
-  if (rd.adjacent)
-    launch_pdl(pool_reposition_kernel<D, true, FP8>, grid, dim3(kRepThreads), 0, s, d, rd, k, kept, n_kept, table, keep, err);
-  else
-    launch_pdl(pool_reposition_kernel<D, false, FP8>, grid, dim3(kRepThreads), 0, s, d, rd, k, kept, n_kept, table, keep, err);
+  constexpr int HPW = 32 / (D / 16), NW = kRepThreads / 32;
+  // steps of a warp: all of them, if one wave of warps does it, in runs that still even out over several waves if not
+  const long long steps = (long long)n_req * d.Hkv * ((keep + HPW - 1) / HPW);
+  const int run = (int)std::max(1ll, std::min<long long>(kRepRun, steps / (device_sm_count() * 32ll)));
+  const dim3 grid((keep + NW * HPW * run - 1) / (NW * HPW * run), n_req * d.Hkv);
+  auto go = [&](auto kernel) { launch_pdl(kernel, grid, dim3(kRepThreads), 0, s, d, rd, k, kept, n_kept, table, keep, run, err); };
+  if (rd.adjacent) go(pool_reposition_kernel<D, kAdjacent, FP8>);
+  else if (rd.rot == D) go(pool_reposition_kernel<D, kHalves, FP8>);
+  else go(pool_reposition_kernel<D, kPart, FP8>);
   return cudaGetLastError();
 }
 

@@ -59,6 +59,9 @@ class Case:
 
     def rotate(self, **kw):
         qo, ko = torch.full_like(self.q, 7.0), torch.full_like(self.k, 7.0)
+        if self.hk == 0:
+            self.rope.rotate(self.q, self.pos, qo, q_norm=self.wq, **kw)
+            return qo, ko
         self.rope.rotate(self.q, self.pos, qo, self.k, ko, q_norm=self.wq, k_norm=self.wk, **kw)
         return qo, ko
 
@@ -69,7 +72,7 @@ class Case:
 
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("adjacent", [False, True])
-@pytest.mark.parametrize("n,hq,hk", [(1, 32, 8), (5, 7, 1), (77, 1, 1), (300, 12, 3), (6000, 3, 2)])
+@pytest.mark.parametrize("n,hq,hk", [(1, 32, 8), (5, 7, 1), (77, 1, 1), (300, 12, 3), (6000, 3, 2), (1701, 11, 5), (20001, 0, 3), (4567, 17, 0)])
 def test_dense(d, adjacent, n, hq, hk):
     c = Case(n + d, n, hq, hk, d, adjacent=adjacent)
     c.check(*c.rotate())
@@ -174,6 +177,18 @@ def test_rows_of_zeros_infinities_and_nan_stay_by_themselves():
     check(qo[:2], *(a[:2] for a in c.ref(c.q, c.wq)))
 
 
+@pytest.mark.parametrize("n", [20, 9000])
+@pytest.mark.parametrize("adjacent", [False, True])
+def test_elements_that_do_not_turn_stay_by_themselves(n, adjacent):
+    c = Case(15, n, 3, 1, 128, rot=32, norm=False, adjacent=adjacent)
+    for i, x in ((40, float("inf")), (41, float("nan")), (127, -float("inf")), (96, float("nan"))):
+        c.q[i % n, 1, i] = x
+    qo, _ = c.rotate()
+    assert torch.equal(qo[..., 32:].view(torch.int16)[torch.isfinite(c.q[..., 32:])], c.q[..., 32:].view(torch.int16)[torch.isfinite(c.q[..., 32:])])
+    assert torch.equal(torch.isnan(qo), torch.isnan(c.q)) and torch.equal(torch.isinf(qo), torch.isinf(c.q))
+    check(qo[..., :32], *(a[..., :32] for a in c.ref(c.q, None)))
+
+
 def test_no_tokens_and_no_keys():
     c = Case(10, 4, 4, 2, 64)
     e = c.q[:0]
@@ -246,7 +261,7 @@ class PoolRows(Case):
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 @pytest.mark.parametrize("d,adjacent,rot,sections", [(128, False, None, None), (64, True, None, None), (128, False, 96, [16, 16, 16]), (64, False, 16, None),
                                                      (128, True, 32, [8, 8])])
-@pytest.mark.parametrize("n,hq,hk,bs", [(1, 32, 8, 16), (33, 7, 7, 128), (500, 9, 3, 32), (5000, 4, 2, 64)])
+@pytest.mark.parametrize("n,hq,hk,bs", [(1, 32, 8, 16), (33, 7, 7, 128), (500, 9, 3, 32), (5000, 4, 2, 64), (1301, 15, 5, 16)])
 def test_append(kv, d, adjacent, rot, sections, n, hq, hk, bs):
     c = PoolRows(n + d, n, hq, hk, d, bs, kv, adjacent=adjacent, rot=rot, sections=sections)
     if n > 2:
