@@ -9,6 +9,10 @@
 // requests are written past what they hold, tables of shrinking ones are only read, and the blocks that are given back and
 // taken in the same call are handed over by the thread that gives them.  The lengths held and the ring's state are written
 // by the CTA that is the last to have read them.
+//
+// Bound by latencies: the launch, one read of the lengths, the scan, a table entry, 3.0 us of which the launch is half (64 requests, a
+// token each).  24 prompts of 494000 tokens in all: 6 us, four consecutive tokens a thread (6 MB of places and positions,
+// 0.9 us at the rate of a copy); without the ring's state to write last, as a launch of its own for the tokens, 11 us.
 #include <algorithm>
 
 #include "kvs_rope.cuh"
@@ -17,7 +21,8 @@ namespace kvs {
 
 namespace {
 
-constexpr int kTabThreads = 512;
+constexpr int kTabThreads = 256;
+constexpr int kTabDeep = 4;                  // moves of a thread on their way at once
 constexpr unsigned kTabMany = 1u << 30;      // sums stop here (no pool has as many slots)
 
 __device__ __forceinline__ unsigned add_sat(unsigned a, unsigned b) { return min(a + b, kTabMany); }
@@ -32,6 +37,7 @@ __device__ __forceinline__ int last_at(const int* x, int n, int v) {
   return lo;
 }
 
+template <int PER>      // consecutive tokens a thread places at a time
 __global__ void __launch_bounds__(kTabThreads)
     pool_tables_kernel(PoolDims d, PoolTables t, unsigned* ticket, unsigned* err) {
   extern __shared__ int dyn[];
@@ -42,8 +48,8 @@ __global__ void __launch_bounds__(kTabThreads)
   int* need = held + n;          // [n] and after it
   int* takes = need + n;         // [n + 1] blocks taken by the requests before
   int* gives = takes + n + 1;    // [n + 1]
+  int* delta = gives + n + 1;    // [n]
   __shared__ unsigned warp_take[kTabThreads / 32], warp_give[kTabThreads / 32];
-  __shared__ int is_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   kvs_pdl_entry();
   const bool alloc = t.ring != nullptr;
@@ -56,23 +62,35 @@ __global__ void __launch_bounds__(kTabThreads)
   // each thread counts a run of requests
   const int per = (n + kTabThreads - 1) / kTabThreads, r0 = min(n, tid * per), r1 = min(n, r0 + per);
   unsigned take = 0, give = 0;
-  for (int r = r0; r < r1; ++r) {
-    int len = t.ctx_len[r];
-    const bool ok_len = len >= 0 && len <= d.max_ctx;
-    const int blocks = ok_len ? (len + d.bs - 1) >> d.log2bs : 0;
-    int had = alloc ? t.n_held[r] : blocks;
-    const bool ok = ok_len && had >= 0 && had <= d.nb_max;
-    bad |= !ok;
-    if (!ok) had = 0;
-    const int want = ok ? blocks : 0;
-    ctx[r] = ok ? len : -1;
-    held[r] = had;
-    need[r] = want;
-    take = add_sat(take, max(0, want - had));
-    give = add_sat(give, max(0, had - want));
+  for (int r = r0; r < r1; r += 2) {      // (two requests' loads at once)
+    int len[2], had[2], by[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (r + k < r1) {
+        len[k] = __ldg(t.ctx_len + r + k);
+        had[k] = alloc ? t.n_held[r + k] : 0;
+        by[k] = t.pos_delta ? __ldg(t.pos_delta + r + k) : 0;
+      }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (r + k < r1) {
+        const bool ok_len = len[k] >= 0 && len[k] <= d.max_ctx;
+        const int blocks = ok_len ? (len[k] + d.bs - 1) >> d.log2bs : 0;
+        if (!alloc) had[k] = blocks;
+        const bool ok = ok_len && had[k] >= 0 && had[k] <= d.nb_max;
+        bad |= !ok;
+        if (!ok) had[k] = 0;
+        const int want = ok ? blocks : 0;
+        ctx[r + k] = ok ? len[k] : -1;
+        held[r + k] = had[k];
+        need[r + k] = want;
+        delta[r + k] = by[k];
+        take = add_sat(take, max(0, want - had[k]));
+        give = add_sat(give, max(0, had[k] - want));
+      }
   }
   if (t.cu_q)
-    for (int r = tid; r <= n; r += kTabThreads) cu[r] = t.cu_q[r];
+    for (int r = tid; r <= n; r += kTabThreads) cu[r] = __ldg(t.cu_q + r);
   unsigned in_take = take, in_give = give;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -88,8 +106,8 @@ __global__ void __launch_bounds__(kTabThreads)
   }
   __syncthreads();
   unsigned before_take = 0, before_give = 0, all_take = 0, all_give = 0;
-#pragma unroll
-  for (int w = 0; w < kTabThreads / 32; ++w) {
+  const int busy = per ? (n + 32 * per - 1) / (32 * per) : 0;      // warps with requests
+  for (int w = 0; w < busy; ++w) {
     if (w == warp) {
       before_take = all_take;
       before_give = all_give;
@@ -97,7 +115,7 @@ __global__ void __launch_bounds__(kTabThreads)
     all_take = add_sat(all_take, warp_take[w]);
     all_give = add_sat(all_give, warp_give[w]);
   }
-  // (sums that stopped are never used: such calls change nothing)
+  // (sums that stopped are never used, nor those of warps without requests)
   before_take = add_sat(before_take, in_take - take);
   before_give = add_sat(before_give, in_give - give);
   for (int r = r0; r < r1; ++r) {
@@ -120,20 +138,13 @@ __global__ void __launch_bounds__(kTabThreads)
   const bool change = alloc && ok_state && !lacking;
   bad |= !ok_state;
   if (bad) set_error(err, KVS_ERR_BAD_INDEX);
-  if (alloc) {
-    if (tid == 0) {
-      is_last = 1;
-      if (gridDim.x > 1) {
-        __threadfence();
-        is_last = atomicAdd(ticket, 1u) == gridDim.x - 1;
-        __threadfence();
-        if (is_last) *ticket = 0;
-      }
-    }
-    __syncthreads();
-    if (is_last) {
-      if (tid == 0 && ok_state) {
-        t.state[2] = lacking ? (int)(all_take - have) : 0;
+  if (alloc && warp == kTabThreads / 32 - 1) {      // (the warp that has the least of the rest to do)
+    unsigned before = gridDim.x - 1;
+    if (lane == 0 && gridDim.x > 1) asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(ticket) : "memory");
+    if (__shfl_sync(0xffffffffu, before, 0) == gridDim.x - 1) {
+      if (lane == 0) {
+        *ticket = 0;
+        if (ok_state) t.state[2] = lacking ? (int)(all_take - have) : 0;
         if (change) {
           const int at = head + (int)all_take;        // all_take <= have <= n_slots
           t.state[0] = at < d.n_slots ? at : at - d.n_slots;
@@ -142,7 +153,7 @@ __global__ void __launch_bounds__(kTabThreads)
         if (lacking) set_error(err, KVS_ERR_CAPACITY);
       }
       if (change)
-        for (int r = tid; r < n; r += kTabThreads)
+        for (int r = lane; r < n; r += 32)
           if (ctx[r] >= 0) t.n_held[r] = need[r];
     }
   }
@@ -153,68 +164,122 @@ __global__ void __launch_bounds__(kTabThreads)
   };
   if (change) {
     const int taken = (int)min(all_take, (unsigned)n_free);
-    for (int i = first; i < taken; i += stride) {
-      const int r = last_at(takes, n, i);
-      t.table[(size_t)r * d.nb_max + held[r] + (i - takes[r])] = *ring_at(i);
+    for (int i0 = first; i0 < taken; i0 += stride * kTabDeep) {
+      int slot[kTabDeep];
+#pragma unroll
+      for (int k = 0; k < kTabDeep; ++k) slot[k] = i0 + k * stride < taken ? *ring_at(i0 + k * stride) : 0;
+#pragma unroll
+      for (int k = 0; k < kTabDeep; ++k) {
+        const int i = i0 + k * stride;
+        if (i >= taken) break;
+        const int r = last_at(takes, n, i);
+        t.table[(size_t)r * d.nb_max + held[r] + (i - takes[r])] = slot[k];
+      }
     }
-    for (int j = first; j < (int)all_give; j += stride) {
-      const int r = last_at(gives, n, j);
-      const int slot = t.table[(size_t)r * d.nb_max + need[r] + (j - gives[r])];
-      *ring_at(n_free + j) = slot;
-      const int i = n_free + j;
-      if (i < (int)all_take) {
-        const int to = last_at(takes, n, i);
-        t.table[(size_t)to * d.nb_max + held[to] + (i - takes[to])] = slot;
+    for (int j0 = first; j0 < (int)all_give; j0 += stride * kTabDeep) {
+      int slot[kTabDeep];
+#pragma unroll
+      for (int k = 0; k < kTabDeep; ++k) {
+        const int j = j0 + k * stride;
+        if (j < (int)all_give) {
+          const int r = last_at(gives, n, j);
+          slot[k] = t.table[(size_t)r * d.nb_max + need[r] + (j - gives[r])];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kTabDeep; ++k) {
+        const int j = j0 + k * stride, i = n_free + j;
+        if (j >= (int)all_give) break;
+        *ring_at(i) = slot[k];
+        if (i < (int)all_take) {
+          const int to = last_at(takes, n, i);
+          t.table[(size_t)to * d.nb_max + held[to] + (i - takes[to])] = slot[k];
+        }
       }
     }
   }
   if (!t.cu_q) return;
-  for (int tok = first; tok < t.n_tok; tok += stride) {
-    long long place = -1;
-    int pos = 0;
-    const int r = last_at(cu, n, tok);
-    const int a = cu[r], b = cu[r + 1];
-    // (offsets that cannot be, and requests of a bad length, are reported above: their tokens have no place)
-    if (a >= 0 && b <= t.n_tok && tok >= a && tok < b && ctx[r] >= 0) {
-      const int p = ctx[r] - (b - tok);
-      pos = (int)((unsigned)p + (unsigned)(t.pos_delta ? t.pos_delta[r] : 0));
-      if (p >= 0) {
-        const int block = p >> d.log2bs;
-        int slot = -1;
-        bool known = true;
-        if (block < held[r]) {
-          slot = t.table[(size_t)r * d.nb_max + block];
-        } else if (change) {
-          const int i = takes[r] + (block - held[r]);
-          if (i < n_free) {
-            slot = *ring_at(i);
-          } else {
-            const int from = last_at(gives, n, i - n_free);
-            slot = t.table[(size_t)from * d.nb_max + need[from] + (i - n_free - gives[from])];
+  // the slot of a request's block, or -1 where it has none
+  auto slot_of = [&](int r, int block) {
+    int slot = -1;
+    if (block < held[r]) {
+      slot = t.table[(size_t)r * d.nb_max + block];
+    } else if (change) {
+      const int i = takes[r] + (block - held[r]);
+      if (i < n_free) {
+        slot = *ring_at(i);
+      } else {
+        const int from = last_at(gives, n, i - n_free);
+        slot = t.table[(size_t)from * d.nb_max + need[from] + (i - n_free - gives[from])];
+      }
+    } else {
+      return -1;      // the block was lacking
+    }
+    if (slot >= 0 && slot < d.n_slots) return slot;
+    set_error(err, KVS_ERR_BAD_INDEX);
+    return -1;
+  };
+  const bool wide = PER == 4 && ((reinterpret_cast<uintptr_t>(t.place) | reinterpret_cast<uintptr_t>(t.pos)) & 15) == 0;
+  for (long long t0 = (long long)first * PER; t0 < t.n_tok; t0 += (long long)stride * PER) {
+    long long place[PER];
+    int pos[PER];
+    int r = last_at(cu, n, (int)t0), at_block = -1, slot = -1;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int tok = min((int)t0 + j, t.n_tok - 1);
+      while (r + 1 < n && cu[r + 1] <= tok) {      // (offsets that descend end here as well: r grows)
+        ++r;
+        at_block = -1;
+      }
+      place[j] = -1;
+      pos[j] = 0;
+      const int a = cu[r], b = cu[r + 1];
+      // (offsets that cannot be, and requests of a bad length, are reported above: their tokens have no place)
+      if (a >= 0 && b <= t.n_tok && tok >= a && tok < b && ctx[r] >= 0) {
+        const int p = ctx[r] - (b - tok);
+        pos[j] = (int)((unsigned)p + (unsigned)delta[r]);
+        if (p >= 0) {
+          if (p >> d.log2bs != at_block) {
+            at_block = p >> d.log2bs;
+            slot = slot_of(r, at_block);
           }
-        } else {
-          known = false;      // the block was lacking
+          if (slot >= 0) place[j] = ((long long)slot << d.log2bs) + (p & (d.bs - 1));
         }
-        if (slot >= 0 && slot < d.n_slots) place = ((long long)slot << d.log2bs) + (p & (d.bs - 1));
-        else if (known) set_error(err, KVS_ERR_BAD_INDEX);
       }
     }
-    t.place[tok] = place;
-    if (t.pos) t.pos[tok] = pos;
+    if (wide && t0 + PER <= t.n_tok) {
+      longlong2* to = reinterpret_cast<longlong2*>(t.place + t0);
+      to[0] = make_longlong2(place[0], place[1 % PER]);
+      to[1] = make_longlong2(place[2 % PER], place[3 % PER]);
+      if (t.pos) *reinterpret_cast<int4*>(t.pos + t0) = make_int4(pos[0], pos[1 % PER], pos[2 % PER], pos[3 % PER]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        if (t0 + j < t.n_tok) {
+          t.place[t0 + j] = place[j];
+          if (t.pos) t.pos[t0 + j] = pos[j];
+        }
+    }
   }
 }
 
 }  // namespace
 
 cudaError_t launch_pool_tables(const PoolDims& d, const PoolTables& t, unsigned* ticket, unsigned* err, cudaStream_t s) {
-  const long long blocks = t.ring ? (long long)t.n_req * d.nb_max : 0;
-  const long long work = std::max<long long>(t.n_tok, blocks / 16);
-  const int grid = (int)std::max(1ll, std::min<long long>((work + kTabThreads - 1) / kTabThreads, device_sm_count()));
-  const int smem = (6 * t.n_req + 3) * 4;
-  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(pool_tables_kernel), (6 * kPoolMaxReq + 3) * 4);
-  if (e != cudaSuccess) return e;
-  launch_pdl(pool_tables_kernel, dim3(grid), dim3(kTabThreads), (size_t)smem, s, d, t, ticket, err);
-  return cudaGetLastError();
+  // A thread places one token (a batch's next tokens), or four where there are two for every thread of the GPU; a call without tokens
+  // may move as many blocks as the tables hold, and mostly moves few: 64 CTAs for large tables (500 requests that give 190 blocks
+  // back: 4.1 us with 1 to 64 CTAs, 4.4 with 244; 24 that give back 7700: 13 us with 1, 4 with 12).
+  const int sms = device_sm_count(), smem = (7 * t.n_req + 3) * 4;
+  const bool many = t.n_tok > sms * kTabThreads * 2;
+  const long long work = t.cu_q ? t.n_tok / (many ? 4 : 1) : (long long)t.n_req * d.nb_max / 4;
+  const int grid = (int)std::max(1ll, std::min<long long>((work + kTabThreads - 1) / kTabThreads, t.cu_q ? sms * 4 : 64));
+  auto go = [&](auto kernel) {
+    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), (7 * kPoolMaxReq + 3) * 4);
+    if (e != cudaSuccess) return e;
+    launch_pdl(kernel, dim3(grid), dim3(kTabThreads), (size_t)smem, s, d, t, ticket, err);
+    return cudaGetLastError();
+  };
+  return many ? go(pool_tables_kernel<4>) : go(pool_tables_kernel<1>);
 }
 
 }  // namespace kvs
