@@ -129,6 +129,41 @@ def lib():
     return _lib
 
 
+BINDING_PATH = os.path.join(_HERE, "_build", "kvs_binding.so")
+_binding = None
+
+
+def binding():
+    """The compiled part of the binding (csrc/binding.cpp): what the calls of a decoding loop check and pass on."""
+    global _binding
+    if _binding is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries, which the module links to)
+        lib()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"kvs_binding.so is not built ({BINDING_PATH}); run __graft_entry__.build()")
+        loader = importlib.machinery.ExtensionFileLoader("kvs_binding", BINDING_PATH)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("kvs_binding", loader))
+        loader.exec_module(m)
+        _binding = m
+    return _binding
+
+
+class _Calls:
+    """The C ABI's functions: those of the compiled binding where it has them, else through ctypes."""
+
+    def __getattr__(self, name):
+        f = getattr(binding(), name, None) if name in _SIGS else None
+        f = f or getattr(lib(), name)
+        setattr(self, name, f)
+        return f
+
+
+calls = _Calls()
+
+
 def _check(status: int, where: str) -> None:
     if status != 0:
         raise KvsError(status, where)

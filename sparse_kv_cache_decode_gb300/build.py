@@ -1,13 +1,17 @@
-"""Build libkvs.so in-tree: each CUDA source compiled for sm_103a in parallel, then linked."""
+"""Build libkvs.so in-tree: each CUDA source compiled for sm_103a in parallel, then linked; and kvs_binding.so, the compiled part of the
+Python binding, against torch's headers."""
 import concurrent.futures as cf
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libkvs.so")
+BINDING = os.path.join(OUT_DIR, "kvs_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
@@ -31,6 +35,32 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_binding():
+    src, obj = os.path.join(CSRC, "binding.cpp"), os.path.join(OUT_DIR, "binding.o")
+    if _stale(obj, [src] + headers()):
+        torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+        cuda = os.path.dirname(os.path.dirname(NVCC))
+        inc = [f"-I{torch}/include", f"-I{torch}/include/torch/csrc/api/include", f"-I{cuda}/include", f"-I{sysconfig.get_paths()['include']}"]
+        _run(["g++", "-O2", "-std=c++17", "-fPIC"] + inc + ["-c", src, "-o", obj + ".tmp"], src)
+        os.replace(obj + ".tmp", obj)
+    return obj
+
+
+def _link_binding(obj):
+    if _stale(BINDING, [obj]):
+        tmp = BINDING + f".tmp{os.getpid()}"
+        torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+        _run(["g++", "-shared", "-o", tmp, obj, f"-L{OUT_DIR}", "-lkvs", "-Wl,-rpath,$ORIGIN", f"-L{torch}/lib", "-ltorch_python", "-ltorch_cpu",
+              "-lc10", "-lc10_cuda"], BINDING)
+        os.replace(tmp, BINDING)
+
+
 def _compile(src):
     obj = os.path.join(OUT_DIR, os.path.basename(src)[:-3] + ".o")
     if _stale(obj, [src] + headers()):
@@ -48,8 +78,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if force:
         for f in os.listdir(OUT_DIR):
             os.remove(os.path.join(OUT_DIR, f))
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, srcs))
+        binding = binding.result()
     if _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [NVCC] + ARCH + ["-shared", "-o", tmp] + objs
@@ -57,6 +89,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    _link_binding(binding)
     if verbose:
         print(LIB)
     return LIB

@@ -15,14 +15,16 @@ what the tensors are (ValueError) and forward to the C ABI (KvsError).  Tensors:
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
-from . import KV_DTYPE, KvsError, KvsPoolConfig, _check, lib
+from . import KV_DTYPE, KvsError, KvsPoolConfig, _check, binding, calls
 from .rope import Rope, _norm, _positions
 
 _BF16 = (torch.bfloat16, torch.int16)
 _FP8 = (torch.float8_e4m3fn, torch.uint8)
+_fast = binding()
 _I32, _I64, _F32 = (torch.int32,), (torch.int64,), (torch.float32,)
 
 
@@ -52,7 +54,7 @@ class Pool:
     def __init__(self, cfg: KvsPoolConfig, k: torch.Tensor, v: torch.Tensor):
         self.h = None
         self.cfg = cfg
-        self.L = lib()
+        self.L = calls
         nbytes = self.L.kvs_pool_workspace_bytes(ctypes.byref(cfg))
         if nbytes == 0:
             raise KvsError(1, "kvs_pool_workspace_bytes")
@@ -88,8 +90,9 @@ class Pool:
     # ------------------------------------------------------------------ checks (every call: kept short)
     def _whole(self, t, name, dtypes, shape):
         """Pointer of a contiguous tensor of this device."""
-        if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == self.index:
-            return t.data_ptr()
+        p = _fast.whole(t, dtypes, shape, self.index)
+        if p is not None:
+            return p
         if t.dtype not in dtypes:
             raise ValueError(f"{name}: dtype {t.dtype}, expected {dtypes[0]}")
         if t.shape != shape:
@@ -101,6 +104,9 @@ class Pool:
     def _tokens(self, t, name, heads):
         """Rows [n_tok][heads][d] of bf16, contiguous within a token: (pointer, token stride, tokens)."""
         d = self.cfg.head_dim
+        x = _fast.rows(t, _BF16, heads, d, self.index)
+        if x is not None and (x[2] == d or heads == 1) and x[1] >= heads * d:
+            return x[0], x[1], x[3]
         if t.dtype not in _BF16:
             raise ValueError(f"{name}: dtype {t.dtype}, expected {_BF16[0]}")
         if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
@@ -125,13 +131,13 @@ class Pool:
 
     def _stream(self, stream):
         if stream is None:
-            return torch.cuda.current_stream(self.index).cuda_stream
+            return _fast.stream(self.index)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
     def _call(self, fn, where, *args):
         if self.h is None:
             raise ValueError("Pool: closed")
-        if torch.cuda.current_device() == self.index:
+        if self.index < 0 or _fast.device() == self.index:
             status = fn(self.h, *args)
         else:
             with torch.cuda.device(self.index):
@@ -211,19 +217,26 @@ class Pool:
     def rotate_append(self, layer, rope, q, k, v, pos, place, q_out, q_norm=None, k_norm=None, stream=None):
         """kvs_pool_rotate_append: q [n_tok][H_q][d] normed and rotated into q_out; k and v [n_tok][H_kv][d] to their places, k normed and
         rotated as well."""
-        c = self.cfg
-        qp, qs, n_tok = self._tokens(q, "q", c.n_q_head)
-        kp, ks, n_k = self._tokens(k, "k", c.n_kv_head)
-        vp, vs, n_v = self._tokens(v, "v", c.n_kv_head)
-        op, os, n_o = self._tokens(q_out, "q_out", c.n_q_head)
-        if n_k != n_tok or n_v != n_tok or n_o != n_tok or ks != vs:
+        hq, hk, d = self._heads
+        i, rows = self.index, _fast.rows
+        a, b, c, o = rows(q, _BF16, hq, d, i), rows(k, _BF16, hk, d, i), rows(v, _BF16, hk, d, i), rows(q_out, _BF16, hq, d, i)
+        if a is None or b is None or c is None or o is None or a[2] != d or b[2] != d or c[2] != d or o[2] != d:
+            for t, name, heads in ((q, "q", hq), (k, "k", hk), (v, "v", hk), (q_out, "q_out", hq)):
+                self._tokens(t, name, heads)
+        n_tok = a[3]
+        if b[3] != n_tok or c[3] != n_tok or o[3] != n_tok or b[1] != c[1]:
             raise ValueError("q, k, v and q_out: different numbers of tokens, or k and v of different strides")
         h = self._rope(rope)
-        pp, ps = _positions(pos, rope.n_axis, n_tok, self.index)
+        pp, ps = _positions(pos, rope.n_axis, n_tok, i)
         pl = self._whole(place, "place", _I64, (n_tok,))
-        qn, kn = _norm(q_norm, "q_norm", c.head_dim, self.index), _norm(k_norm, "k_norm", c.head_dim, self.index)
-        self._call(self.L.kvs_pool_rotate_append, "kvs_pool_rotate_append", h, _int(layer, "layer"), qp, qs, kp, vp, ks, qn, kn, pp, ps, pl,
-                   n_tok, op, os, self._stream(stream))
+        qn, kn = _norm(q_norm, "q_norm", d, i), _norm(k_norm, "k_norm", d, i)
+        self._call(self.L.kvs_pool_rotate_append, "kvs_pool_rotate_append", h, _int(layer, "layer"), a[0], a[1], b[0], c[0], b[1], qn, kn, pp, ps, pl,
+                   n_tok, o[0], o[1], _fast.stream(i) if stream is None else self._stream(stream))
+
+    @functools.cached_property
+    def _heads(self):
+        """(H_q, H_kv, head_dim)"""
+        return self.cfg.n_q_head, self.cfg.n_kv_head, self.cfg.head_dim
 
     def reposition(self, layer, rope, kept, n_kept, block2slot, stream=None):
         """kvs_pool_reposition: the keys that `evict` kept (its kept, n_kept and dst2slot), rotated to their new positions."""

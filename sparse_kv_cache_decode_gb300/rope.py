@@ -13,9 +13,11 @@ import ctypes
 
 import torch
 
-from . import KvsRopeConfig, KvsError, _check, lib
+from . import KvsError, KvsRopeConfig, _check, binding, calls
 
 _BF16 = (torch.bfloat16, torch.int16)
+_I32, _F32 = (torch.int32,), (torch.float32,)
+_fast = binding()
 
 
 def rope_axes(sections, cycle: bool = False) -> list:
@@ -56,35 +58,35 @@ def make_rope_config(head_dim: int, rot_dim: int | None = None, theta: float = 1
 
 def _rows(t, name, d, index):
     """Rows [n_tok][heads][d] of bf16: (pointer, token stride, head stride, tokens, heads)."""
+    x = _fast.rows(t, _BF16, -1, d, index)
+    if x is not None:
+        return x
     if t.dtype not in _BF16:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {_BF16[0]}")
     if t.dim() != 3 or t.shape[2] != d:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (n_tok, heads, {d})")
-    n, h, _ = t.shape
-    s0, s1, s2 = t.stride()
-    if s2 != 1:
+    if t.stride(2) != 1:
         raise ValueError(f"{name}: a head's elements must be contiguous")
-    if t.get_device() != index:
-        raise ValueError(f"{name}: on {t.device}")
-    if h <= 1:
-        s1 = d
-    if n <= 1:
-        s0 = h * s1
-    return t.data_ptr(), s0, s1, n, h
+    raise ValueError(f"{name}: on {t.device}")
 
 
 def _norm(t, name, d, index):
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != d or t.stride(0) != 1:
-        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected contiguous torch.float32 ({d},)")
-    if t.get_device() != index:
-        raise ValueError(f"{name}: on {t.device}")
-    return t.data_ptr()
+    p = _fast.whole(t, _F32, (d,), index)
+    if p is None:
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected contiguous torch.float32 ({d},)")
+    return p
 
 
 def _positions(t, n_axis, n, index):
     """(pointer, elements between axes) of positions [n_axis][n] or [n]."""
+    p = _fast.whole(t, _I32, (n,), index)
+    if p is not None:
+        return p, 0
+    p = _fast.whole(t, _I32, (n_axis, n), index)
+    if p is not None:
+        return p, n if n_axis > 1 else 0
     if t.dtype != torch.int32:
         raise ValueError(f"pos: dtype {t.dtype}, expected torch.int32")
     shape, stride = t.shape, t.stride()
@@ -102,7 +104,7 @@ class Rope:
         self.h = None
         self.cfg = cfg
         self.d, self.n_axis = cfg.head_dim, cfg.n_axis
-        self.L = lib()
+        self.L = calls
         h = ctypes.c_void_p()
         _check(self.L.kvs_rope_create(ctypes.byref(cfg), ctypes.byref(h)), "kvs_rope_create")
         self.h = h
@@ -140,11 +142,11 @@ class Rope:
         pp, ps = _positions(pos, self.n_axis, n, index)
         qn, kn = _norm(q_norm, "q_norm", d, index), _norm(k_norm, "k_norm", d, index)
         if stream is None:
-            stream = torch.cuda.current_stream(index).cuda_stream
+            stream = _fast.stream(index)
         elif not isinstance(stream, int):
             stream = stream.cuda_stream
         args = (self.h, qp, qs, qh, hq, qn, op, os, oh, kp, ks, kh, hk, kn, kop, kos, koh, pp, ps, n, stream)
-        if torch.cuda.current_device() == index:
+        if _fast.device() == index:
             status = self.L.kvs_rotate(*args)
         else:
             with torch.cuda.device(index):
