@@ -15,15 +15,16 @@ namespace kvs {
 
 namespace {
 
-// cos and sin of m * f turns, two of them.  The product's upper word, a turn's fraction, becomes a float by its upper 23 bits, rounded
-// (a conversion would take the unit that the cosines need); the fast functions are off by 2^-21 for arguments in [-pi, pi].
-// Together 2^-20 at most.
+// cos and sin of m * f turns, two of them.  The product's upper word, a turn's fraction, becomes a float in [1, 2) by its upper 23
+// bits, rounded (a conversion would take the unit that the cosines need); the fast functions are off by 2^-21 for arguments in
+// [-pi, pi].  Together 2^-20 at most.
+constexpr float kTwoPi = 6.2831853f;
 __device__ __forceinline__ float turn_bits(unsigned m, unsigned long long f) {      // 1.5 + the fraction's distance from whole turns
   const unsigned t = __umulhi(m, (unsigned)f) + (m * (unsigned)(f >> 32) + 0x80000100u);      // half a turn on, and half a step
   return __uint_as_float((t >> 9) | 0x3f800000u);
 }
 __device__ __forceinline__ void turn_cos_sin(unsigned m, unsigned long long f0, unsigned long long f1, float2& c, float2& s) {
-  const float2 x = __fmul2_rn(__fadd2_rn(make_float2(turn_bits(m, f0), turn_bits(m, f1)), make_float2(-1.5f, -1.5f)), make_float2(6.2831853f, 6.2831853f));
+  const float2 x = __fmul2_rn(__fadd2_rn(make_float2(turn_bits(m, f0), turn_bits(m, f1)), make_float2(-1.5f, -1.5f)), make_float2(kTwoPi, kTwoPi));
   c = make_float2(__cosf(x.x), __cosf(x.y));
   s = make_float2(__sinf(x.x), __sinf(x.y));
 }
@@ -105,10 +106,14 @@ __device__ __forceinline__ Raw pack_bf16(const float (&x)[16]) {
   for (int i = 0; i < 8; ++i) w[i] = f32x2_to_bf16x2(x[2 * i], x[2 * i + 1]);
   return {make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])};
 }
-__device__ __forceinline__ uint2 pack_e4m3(const float* x) {
-  return make_uint2(f32x2_to_e4m3x2(x[0], x[1]) | (f32x2_to_e4m3x2(x[2], x[3]) << 16),
-                    f32x2_to_e4m3x2(x[4], x[5]) | (f32x2_to_e4m3x2(x[6], x[7]) << 16));
+// Four E4M3 codes, rounded to nearest even, saturating
+__device__ __forceinline__ uint32_t pack_e4m3x4(const float* x) {
+  uint32_t r;
+  asm("{.reg .b16 lo, hi;\n cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n mov.b32 %0, {lo, hi};}"
+      : "=r"(r) : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
+  return r;
 }
+__device__ __forceinline__ uint2 pack_e4m3(const float* x) { return make_uint2(pack_e4m3x4(x), pack_e4m3x4(x + 4)); }
 
 enum { kDense, kPoolBf16, kPoolFp8 };
 
@@ -130,7 +135,7 @@ struct RowWarp {
   __device__ __forceinline__ void turns(const int (&pos)[NP], const unsigned long long (&freq)[NP], float2* turn) {
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-      const float x = (turn_bits(magnitude(pos[j]), freq[j]) - 1.5f) * 6.2831853f;
+      const float x = (turn_bits(magnitude(pos[j]), freq[j]) - 1.5f) * kTwoPi;
       const float scale = lane + 32 * j < rot / 2 ? rot_scale : 1.f;
       turn[lane + 32 * j] = make_float2(__cosf(x) * scale, __sinf(x) * (pos[j] < 0 ? -scale : scale));
     }
@@ -505,11 +510,16 @@ __device__ __forceinline__ uint2 ld_shared8(uint32_t addr) {
   return v;
 }
 
-// Two E4M3 codes as fp32 (exact)
-__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint16_t codes) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
-  return __half22float2(*reinterpret_cast<__half2*>(&h));
+// Four E4M3 codes as fp32 (exact)
+__device__ __forceinline__ void unpack_e4m3(uint32_t codes, float* x) {
+  uint32_t h[2];
+  asm("{.reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n cvt.rn.f16x2.e4m3x2 %1, hi;}" : "=r"(h[0]), "=r"(h[1]) : "r"(codes));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 y = __half22float2(*reinterpret_cast<__half2*>(&h[i]));
+    x[2 * i] = y.x;
+    x[2 * i + 1] = y.y;
+  }
 }
 
 template <int D, int LAY, bool FP8>
@@ -584,13 +594,10 @@ __global__ void __launch_bounds__(kRepThreads, 6)
     float x[16];
     if (FP8) {
       const uint2 a = ld_shared8(ring + at_slot * (64 * CH)), b = ld_shared8(ring + at_slot * (64 * CH) + 32 * CH);
-      const uint32_t c[4] = {a.x, a.y, b.x, b.y};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float2 y = e4m3x2_to_f32x2((uint16_t)(c[k >> 1] >> ((k & 1) * 16)));
-        x[2 * k] = y.x;
-        x[2 * k + 1] = y.y;
-      }
+      unpack_e4m3(a.x, x);
+      unpack_e4m3(a.y, x + 4);
+      unpack_e4m3(b.x, x + 8);
+      unpack_e4m3(b.y, x + 12);
     } else {
       unpack_bf16({ld_shared16(ring + at_slot * (64 * CH)), ld_shared16(ring + at_slot * (64 * CH) + 32 * CH)}, x);
     }
