@@ -109,6 +109,167 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return call_as<FN>(FN, args, n);
 }
 
+// ------------------------------------------------------------------ whole calls: tensors checked and passed on
+// Each returns the call's status, or None where a tensor is not what it should be, the device not the current one, or an integer too
+// large: the Python side then goes through the same checks one by one and says which.
+struct Rows {
+  void* p = nullptr;
+  long long tok = 0, head = 0, n = 0, heads = 0;
+};
+struct Parser {
+  long index;      // the device
+  bool ok = true;
+
+  const at::Tensor* take(PyObject* o, at::ScalarType a, at::ScalarType b) {
+    const at::Tensor* t = tensor(o);
+    if (t && (t->scalar_type() == a || t->scalar_type() == b) && t->get_device() == index) return t;
+    ok = false;
+    return nullptr;
+  }
+  Rows rows(PyObject* o, long long heads, long long d) {
+    Rows r;
+    const at::Tensor* t = take(o, at::kBFloat16, at::kShort);
+    if (!t) return r;
+    if (t->dim() != 3 || t->size(2) != d || (heads >= 0 && t->size(1) != heads) || (t->numel() && t->stride(2) != 1)) {
+      ok = false;
+      return r;
+    }
+    r.p = t->data_ptr();
+    r.n = t->size(0);
+    r.heads = t->size(1);
+    r.head = r.heads <= 1 ? d : t->stride(1);
+    r.tok = r.n <= 1 || !t->numel() ? r.heads * r.head : t->stride(0);
+    return r;
+  }
+  // rows whose heads lie together
+  Rows tokens(PyObject* o, long long heads, long long d) {
+    const Rows r = rows(o, heads, d);
+    ok = ok && r.head == d && r.tok >= heads * d;
+    return r;
+  }
+  // a contiguous tensor of n (or a x b) elements; None: a null pointer where it may be left out
+  template <typename T>
+  T* vec(PyObject* o, at::ScalarType type, long long n, bool optional = false) {
+    if (optional && o == Py_None) return nullptr;
+    const at::Tensor* t = take(o, type, type);
+    if (!t) return nullptr;
+    if (t->dim() != 1 || t->size(0) != n || !t->is_contiguous()) ok = false;
+    return static_cast<T*>(t->data_ptr());
+  }
+  const int* positions(PyObject* o, long long n_axis, long long n, long long* stride) {
+    const at::Tensor* t = take(o, at::kInt, at::kInt);
+    if (!t) return nullptr;
+    const bool one = t->dim() == 1;
+    if (!t->is_contiguous() || t->size(-1) != n || !(one || (t->dim() == 2 && t->size(0) == n_axis))) ok = false;
+    *stride = one || n_axis == 1 ? 0 : n;
+    return static_cast<const int*>(t->data_ptr());
+  }
+  template <typename T>
+  T number(PyObject* o) {
+    T v{};
+    if (ok && !get(o, &v)) {
+      PyErr_Clear();
+      ok = false;
+    }
+    return v;
+  }
+  kvs_stream_t stream(PyObject* o) {
+    ok = ok && index >= 0;
+    if (!ok) return nullptr;
+    if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream();
+    PyObject* v = PyLong_Check(o) ? (Py_INCREF(o), o) : PyObject_GetAttrString(o, "cuda_stream");
+    const kvs_stream_t s = v ? static_cast<kvs_stream_t>(PyLong_AsVoidPtr(v)) : nullptr;
+    Py_XDECREF(v);
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      ok = false;
+    }
+    return s;
+  }
+  bool here() const { return ok && index >= 0 && c10::cuda::current_device() == index; }
+};
+template <typename F>
+PyObject* go(const Parser& p, F f) {
+  if (!p.here()) Py_RETURN_NONE;
+  kvs_status status;
+  Py_BEGIN_ALLOW_THREADS
+  status = f();
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(status);
+}
+constexpr long long kInt = 0x7fffffff;
+
+// rotate(handle, d, n_axis, q, pos, q_out, k, k_out, q_norm, k_norm, stream)
+PyObject* rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (wrong_args(n, 11)) return nullptr;
+  const at::Tensor* t = tensor(a[3]);
+  Parser p{t ? (long)t->get_device() : -1};
+  const auto* h = p.number<const kvs_rope*>(a[0]);
+  const int d = p.number<int>(a[1]), n_axis = p.number<int>(a[2]);
+  const Rows q = p.rows(a[3], -1, d), qo = p.rows(a[5], q.heads, d);
+  Rows k, ko;
+  if ((a[6] == Py_None) != (a[7] == Py_None)) Py_RETURN_NONE;
+  if (a[6] != Py_None) {
+    k = p.rows(a[6], -1, d);
+    ko = p.rows(a[7], k.heads, d);
+  }
+  if (!p.ok || qo.n != q.n || (a[6] != Py_None && (k.n != q.n || ko.n != q.n)) || q.n > kInt || q.heads > kInt || k.heads > kInt) Py_RETURN_NONE;
+  long long ps = 0;
+  const int* pos = p.positions(a[4], n_axis, q.n, &ps);
+  const auto *qn = p.vec<const float>(a[8], at::kFloat, d, true), *kn = p.vec<const float>(a[9], at::kFloat, d, true);
+  const kvs_stream_t s = p.stream(a[10]);
+  return go(p, [&] {
+    return kvs_rotate(h, q.p, q.tok, q.head, (int)q.heads, qn, qo.p, qo.tok, qo.head, k.p, k.tok, k.head, (int)k.heads, kn, ko.p, ko.tok, ko.head,
+                      pos, ps, (int)q.n, s);
+  });
+}
+
+// rotate_append(pool, rope, index, H_q, H_kv, d, n_axis, layer, q, k, v, pos, place, q_out, q_norm, k_norm, stream)
+PyObject* rotate_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (wrong_args(n, 17)) return nullptr;
+  Parser p{-1};
+  p.index = p.number<int>(a[2]);
+  auto* h = p.number<kvs_pool*>(a[0]);
+  const auto* rope = p.number<const kvs_rope*>(a[1]);
+  const int hq = p.number<int>(a[3]), hk = p.number<int>(a[4]), d = p.number<int>(a[5]), n_axis = p.number<int>(a[6]), layer = p.number<int>(a[7]);
+  if (!p.ok) Py_RETURN_NONE;
+  const Rows q = p.tokens(a[8], hq, d), k = p.tokens(a[9], hk, d), v = p.tokens(a[10], hk, d), qo = p.tokens(a[13], hq, d);
+  if (!p.ok || k.n != q.n || v.n != q.n || qo.n != q.n || k.tok != v.tok || q.n > kInt) Py_RETURN_NONE;
+  long long ps = 0;
+  const int* pos = p.positions(a[11], n_axis, q.n, &ps);
+  const auto* place = p.vec<const long long>(a[12], at::kLong, q.n);
+  const auto *qn = p.vec<const float>(a[14], at::kFloat, d, true), *kn = p.vec<const float>(a[15], at::kFloat, d, true);
+  const kvs_stream_t s = p.stream(a[16]);
+  return go(p, [&] { return kvs_pool_rotate_append(h, rope, layer, q.p, q.tok, k.p, v.p, k.tok, qn, kn, pos, ps, place, (int)q.n, qo.p, qo.tok, s); });
+}
+
+// reserve(pool, index, n_req, held, table, ring, state, ctx_len, cu_q, place, pos, pos_delta, stream)
+PyObject* reserve(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (wrong_args(n, 13)) return nullptr;
+  Parser p{-1};
+  p.index = p.number<int>(a[1]);
+  auto* h = p.number<kvs_pool*>(a[0]);
+  const int n_req = p.number<int>(a[2]);
+  auto *held = p.number<int*>(a[3]), *table = p.number<int*>(a[4]), *ring = p.number<int*>(a[5]), *state = p.number<int*>(a[6]);
+  const int* ctx = p.vec<const int>(a[7], at::kInt, n_req);
+  const int *cu = nullptr, *delta = nullptr;
+  long long* place = nullptr;
+  int* pos = nullptr;
+  long long n_tok = 0;
+  if (a[8] != Py_None) {
+    const at::Tensor* t = tensor(a[9]);
+    if (!t || t->dim() != 1 || (n_tok = t->size(0)) > kInt) Py_RETURN_NONE;
+    cu = p.vec<const int>(a[8], at::kInt, n_req + 1ll);
+    place = p.vec<long long>(a[9], at::kLong, n_tok);
+    pos = p.vec<int>(a[10], at::kInt, n_tok, true);
+    delta = p.vec<const int>(a[11], at::kInt, n_req, true);
+  } else if (a[9] != Py_None || a[10] != Py_None || a[11] != Py_None) {
+    Py_RETURN_NONE;
+  }
+  const kvs_stream_t s = p.stream(a[12]);
+  return go(p, [&] { return kvs_pool_reserve(h, ctx, held, table, ring, state, n_req, cu, delta, (int)n_tok, place, pos, s); });
+}
+
 // A C++ exception (a tensor without storage, no device) ends here.
 template <auto FN, typename... A>
 PyObject* guarded(A... a) {
@@ -129,6 +290,9 @@ PyObject* plain(PyObject* m, PyObject* o) { return guarded<FN>(m, o); }
 PyMethodDef methods[] = {
     {"whole", KVS_FAST(whole), METH_FASTCALL, nullptr},
     {"rows", KVS_FAST(rows), METH_FASTCALL, nullptr},
+    {"rotate", KVS_FAST(rotate), METH_FASTCALL, nullptr},
+    {"rotate_append", KVS_FAST(rotate_append), METH_FASTCALL, nullptr},
+    {"reserve", KVS_FAST(reserve), METH_FASTCALL, nullptr},
     {"device", &plain<&device>, METH_NOARGS, nullptr},
     {"stream", &plain<&stream>, METH_O, nullptr},
     KVS_CALL(kvs_pool_append),

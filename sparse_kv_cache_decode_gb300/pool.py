@@ -218,6 +218,13 @@ class Pool:
         """kvs_pool_rotate_append: q [n_tok][H_q][d] normed and rotated into q_out; k and v [n_tok][H_kv][d] to their places, k normed and
         rotated as well."""
         hq, hk, d = self._heads
+        if self.L is calls and self.h is not None and rope.h is not None:
+            status = _fast.rotate_append(self.h, rope.h, self.index, hq, hk, d, rope.n_axis, layer, q, k, v, pos, place, q_out, q_norm, k_norm, stream)
+            if status == 0:
+                return
+            if status is not None:
+                raise KvsError(status, "kvs_pool_rotate_append")
+        # another device than the current one, or something to complain of
         i, rows = self.index, _fast.rows
         a, b, c, o = rows(q, _BF16, hq, d, i), rows(k, _BF16, hk, d, i), rows(v, _BF16, hk, d, i), rows(q_out, _BF16, hq, d, i)
         if a is None or b is None or c is None or o is None or a[2] != d or b[2] != d or c[2] != d or o[2] != d:
@@ -281,6 +288,13 @@ class BlockTables:
         """kvs_pool_reserve: every row gets the blocks of its new length, or gives back those past it; with cu_q and place also where the
         call's tokens go, and their positions."""
         p, n_req = self.pool, self.n_req
+        if p.L is calls and p.h is not None:
+            status = _fast.reserve(p.h, p.index, n_req, *self._ptrs, ctx_len, cu_q, place, pos, pos_delta, stream)
+            if status == 0:
+                return
+            if status is not None:
+                raise KvsError(status, "kvs_pool_reserve")
+        # another device than the current one, or something to complain of
         ctx = p._whole(ctx_len, "ctx_len", _I32, (n_req,))
         cu = pl = po = de = None
         n_tok = 0

@@ -124,6 +124,11 @@ class Rope:
         """kvs_rotate: q [n_tok][H_q][d] into q_out and, if given, k [n_tok][H_k][d] into k_out (in place: the same tensor)."""
         if self.h is None:
             raise ValueError("Rope: closed")
+        status = _fast.rotate(self.h, self.d, self.n_axis, q, pos, q_out, k, k_out, q_norm, k_norm, stream)
+        if status == 0:
+            return
+        if status is not None:
+            raise KvsError(status, "kvs_rotate")
         d, index = self.d, q.get_device()
         if index < 0:
             raise ValueError("q: must be a CUDA tensor")
