@@ -30,6 +30,14 @@ __device__ __forceinline__ void turn_cos_sin(unsigned m, unsigned long long f0, 
 }
 __device__ __forceinline__ unsigned magnitude(int pos) { return pos < 0 ? 0u - (unsigned)pos : (unsigned)pos; }
 
+// The parameters by their address: lanes that read entries of their own take one load, where an indexed read of the constant bank is
+// repeated for every lane (128 tokens of 12 steps 3.0 us that way, 2.45 by address; one token 1.83 and 1.65).
+__device__ __forceinline__ const RopeDims* by_address(const RopeDims& rd) {
+  const RopeDims* p = &rd;
+  asm volatile("" : "+l"(p));
+  return p;
+}
+
 // Which elements are a pair: i and i + d / 2, i and i + rot / 2, or 2 i and 2 i + 1.
 enum { kHalves, kPart, kAdjacent };
 
@@ -235,11 +243,12 @@ __device__ __forceinline__ PlaceRow place_row(const RopeRows& a, long long place
   return p;
 }
 
-// Few tokens: a warp per step, everything it needs on its way at once.  One token of 32 + 2 x 8 heads: 1.7 us (3.3 with a loop over
-// the steps of a token).  From about 20 steps for each SM on the other kernel's sharing of a token's angles and its deeper queue win: at
-// 256 tokens (3072 steps) 4.3 us here and 4.5 there, at 512 7.9 and 5.1; of 3 steps each, at 1024 tokens 3.1 and 3.3, at 2048 4.9 and 4.1.
+// Few tokens: a warp per step, everything it needs on its way at once.  One token of 32 + 2 x 8 heads into a bf16 pool: 1.65 us (3.3 with a
+// loop over the token's steps), about the time of a launch.  From some 16 steps for each SM on, where the other kernel's warps have one
+// each, its sharing of a token's angles wins: 128 tokens (1536 steps) 2.4 us here and 2.8 there, 256 3.7 and 3.15; of 3 steps each,
+// 512 tokens 2.0 and 2.3, 2048 4.1 and 3.6.
 constexpr int kFewThreads = 128;
-constexpr int kFewSteps = 20;      // steps for each SM, at most
+constexpr int kFewSteps = 16;      // steps for each SM, at most
 
 template <int D, int LAY, int DST>
 __global__ void __launch_bounds__(kFewThreads)
@@ -250,10 +259,11 @@ __global__ void __launch_bounds__(kFewThreads)
   float2* turn = cos_sin[threadIdx.x >> 5];
   unsigned long long freq[W::NP];
   int pos[W::NP];
+  const RopeDims* const rp = by_address(rd);
 #pragma unroll
   for (int j = 0; j < W::NP; ++j) {
-    freq[j] = rd.freq[w.lane + 32 * j];      // (past the rotated pairs: an angle of 0)
-    pos[j] = rd.axis[w.lane + 32 * j];
+    freq[j] = rp->freq[w.lane + 32 * j];      // (past the rotated pairs: an angle of 0)
+    pos[j] = rp->axis[w.lane + 32 * j];
   }
   const long long item = (long long)blockIdx.x * (kFewThreads / 32) + (threadIdx.x >> 5);
   const int tok = (int)(item / steps), it = (int)(item - (long long)tok * steps);
@@ -335,10 +345,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
   const uint32_t ring_base = smem_u32(ring_all + (threadIdx.x >> 5) * (kStages * 64) + w.lane);
   unsigned long long freq[W::NP];
   int axis[W::NP];
+  const RopeDims* const rp = by_address(rd);
 #pragma unroll
   for (int j = 0; j < W::NP; ++j) {
-    freq[j] = rd.freq[w.lane + 32 * j];      // (past the rotated pairs: an angle of 0)
-    axis[j] = rd.axis[w.lane + 32 * j];
+    freq[j] = rp->freq[w.lane + 32 * j];      // (past the rotated pairs: an angle of 0)
+    axis[j] = rp->axis[w.lane + 32 * j];
   }
   const int ir = iq + ik;
   // The warp's tokens: every n_warps-th one, so that all warps are at neighbours, then an equal run of the steps of those left over.
@@ -534,9 +545,10 @@ __global__ void __launch_bounds__(kRepThreads, 6)
   const uint32_t ring = smem_u32(&ring_all[threadIdx.x >> 5][0][0][lane * CH]);
   int2* what = &what_all[threadIdx.x >> 5][0][lane];
   unsigned long long freq[8];
+  const RopeDims* const rp = by_address(rd);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    freq[j] = at.turns(j, rd.rot) ? rd.freq[at.pair(j)] : 0ull;
+    freq[j] = at.turns(j, rd.rot) ? rp->freq[at.pair(j)] : 0ull;
     asm volatile("" : "+l"(freq[j]));      // (kept, not read from the parameters again each step)
   }
   const int u = blockIdx.y, r = u / d.Hkv, h = u - r * d.Hkv;
