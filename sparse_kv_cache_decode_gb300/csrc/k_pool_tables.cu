@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kTabThreads)
   for (long long t0 = (long long)first * PER; t0 < t.n_tok; t0 += (long long)stride * PER) {
     long long place[PER];
     int pos[PER];
-    int r = last_at(cu, n, (int)t0), at_block = -1, slot = -1;
+    int r = n ? last_at(cu, n, (int)t0) : 0, at_block = -1, slot = -1;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int tok = min((int)t0 + j, t.n_tok - 1);
@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kTabThreads)
       }
       place[j] = -1;
       pos[j] = 0;
+      if (n == 0) continue;      // nobody's
       const int a = cu[r], b = cu[r + 1];
       // (offsets that cannot be, and requests of a bad length, are reported above: their tokens have no place)
       if (a >= 0 && b <= t.n_tok && tok >= a && tok < b && ctx[r] >= 0) {

@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kRepThreads, 6)
   auto find = [&]() {
     by = 0;
     if (i < end) {
-      by = i - kept[i];
+      by = (int)((unsigned)i - (unsigned)kept[i]);
       slot = table[i >> d.log2bs];
     }
   };

@@ -322,7 +322,7 @@ kvs_status kvs_pool_reserve(kvs_pool* c, const int* d_ctx_len, int* d_n_held, in
                             int n_req, const int* d_cu_q, const int* d_pos_delta, int n_tok, long long* d_place, int* d_pos,
                             kvs_stream_t stream) try {
   if (!call_ok(c, 0, n_req) || n_tok < 0 || n_tok > c->d.max_tokens) return KVS_ERR_INVALID_ARG;
-  if (n_req == 0) return KVS_OK;
+  if (n_req == 0) return n_tok == 0 ? KVS_OK : kvs_pool_places(c, d_cu_q, d_ctx_len, d_block2slot, 0, n_tok, d_pos_delta, d_place, d_pos, stream);
   if (!d_ctx_len || !d_n_held || !d_block2slot || !d_ring || !d_ring_state || d_ctx_len == d_n_held) return KVS_ERR_INVALID_ARG;
   if (n_tok == 0) d_cu_q = nullptr;
   if (n_tok > 0 && (!d_cu_q || !d_place)) return KVS_ERR_INVALID_ARG;
@@ -336,8 +336,8 @@ kvs_status kvs_pool_reserve(kvs_pool* c, const int* d_ctx_len, int* d_n_held, in
 kvs_status kvs_pool_places(kvs_pool* c, const int* d_cu_q, const int* d_ctx_len, const int* d_block2slot, int n_req, int n_tok,
                            const int* d_pos_delta, long long* d_place, int* d_pos, kvs_stream_t stream) try {
   if (!call_ok(c, 0, n_req) || n_tok < 0 || n_tok > c->d.max_tokens) return KVS_ERR_INVALID_ARG;
-  if (n_req == 0 || n_tok == 0) return KVS_OK;
-  if (!d_cu_q || !d_ctx_len || !d_block2slot || !d_place) return KVS_ERR_INVALID_ARG;
+  if (n_tok == 0) return KVS_OK;
+  if (!d_cu_q || !d_place || (n_req > 0 && (!d_ctx_len || !d_block2slot))) return KVS_ERR_INVALID_ARG;      // (no request: nobody's tokens)
   const PoolTables t = {d_ctx_len, nullptr, const_cast<int*>(d_block2slot), nullptr, nullptr, d_cu_q, d_pos_delta, d_place, d_pos, n_req, n_tok};
   c->launches += 1;
   return cuda_status(launch_pool_tables(c->d, t, c->err + kTicketWord, c->err, S(stream)));
@@ -355,7 +355,9 @@ kvs_status kvs_pool_rotate_append(kvs_pool* c, const kvs_rope* rope, int layer, 
   if (n_tok == 0) return KVS_OK;
   if (!d_q || !d_k || !d_v || !d_pos || !d_place || !d_q_out) return KVS_ERR_INVALID_ARG;
   const long long q_row = (long long)d.Hq * d.d, kv_row = (long long)d.Hkv * d.d;
-  if (q_stride % 8 || kv_stride % 8 || q_out_stride % 8 || q_stride < q_row || kv_stride < kv_row || q_out_stride < q_row)
+  constexpr long long most = 1ll << 40;      // (extents stay in 64 bits)
+  if (q_stride % 8 || kv_stride % 8 || q_out_stride % 8 || q_stride < q_row || kv_stride < kv_row || q_out_stride < q_row || q_stride > most ||
+      kv_stride > most || q_out_stride > most)
     return KVS_ERR_INVALID_ARG;
   for (const void* x : {d_q, d_k, d_v, static_cast<const void*>(d_q_out), static_cast<const void*>(d_q_norm), static_cast<const void*>(d_k_norm)})
     if (!aligned16(x)) return KVS_ERR_INVALID_ARG;

@@ -349,6 +349,71 @@ def test_places_outside_the_pool():
     assert c.pool.poll_error() == 0
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_rows_behind_the_fourth_gigabyte(kv):
+    """A pool whose last rows lie past 2^32 bytes: append there, then reposition them."""
+    hk, bs, d = 8, 128, 128
+    n_slots = 18000 if kv == "bf16" else 36000
+    kind = torch.float8_e4m3fn if kv == "fp8" else torch.bfloat16
+    kp, vp = (torch.zeros((1, n_slots, hk, bs, d), dtype=kind, device="cuda") for _ in range(2))
+    assert kp.numel() * kp.element_size() > 1 << 32
+    pool = K.Pool(K.make_pool_config(1, n_slots, hk, hk, d, bs, 3 * bs, 1, 300, kv_dtype=kv), kp, vp)
+    c = Case(30, 300, hk, hk, d)
+    table = torch.tensor([[n_slots - 1, 0, n_slots - 2]], dtype=torch.int32, device="cuda")
+    v = bf16(c.rng, 300, hk, d)
+    place, qo = torch.empty(300, dtype=torch.int64, device="cuda"), torch.empty_like(c.q)
+    cu, ctx = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 300], [300]))
+    pool.places(cu, ctx, table, place)
+    pool.rotate_append(0, c.rope, c.q, c.k, v, c.pos, place, qo, q_norm=c.wq, k_norm=c.wk)
+    rows = lambda p: p[0][table[0].long()].transpose(1, 2).reshape(-1, hk, d)[:300]  # noqa: E731
+    want, mag = c.ref(c.k, c.wk)
+    check(rows(kp).to(torch.bfloat16), want, mag) if kv == "bf16" else check_codes(rows(kp).view(torch.uint8), want, mag, 1.0)
+    assert torch.equal(rows(vp).float(), v.float().clamp(-448, 448).to(kind).float())
+    before = f64(rows(kp).float())
+    kept = torch.arange(300, dtype=torch.int32, device="cuda").add_(7).expand(1, hk, 300).contiguous()
+    pool.reposition(0, c.rope, kept, ctx, table)
+    y, mag = rope_rows(before, np.full((1, 300), -7), c.freqs)
+    half = (2.0 ** -4 * np.abs(y) + 2.0 ** -10) if kv == "fp8" else 2.0 ** -8 * np.abs(y)
+    assert (np.abs(f64(rows(kp).float()) - y) <= half + 2.0 ** -18 * mag).all()
+    assert not kp[0, 1:n_slots - 2].view(torch.uint8).any() and not vp[0, 1:n_slots - 2].view(torch.uint8).any()
+    assert pool.poll_error() == 0
+
+
+def test_a_captured_step():
+    """Tables, rotation and append in one graph, replayed with other lengths and rows, beside the same calls one by one."""
+    n_req, hq, hk, d, bs = 4, 8, 2, 64, 16
+    r = np.random.default_rng(40)
+    sets = []
+    for _ in range(2):
+        kp, vp = (torch.zeros((1, 40, hk, bs, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        pool = K.Pool(K.make_pool_config(1, 40, hq, hk, d, bs, 128, n_req, 8), kp, vp)
+        sets.append((pool, K.BlockTables.empty(pool, n_req), kp, vp, torch.empty(8, dtype=torch.int64, device="cuda"),
+                     torch.empty(8, dtype=torch.int32, device="cuda"), torch.empty((8, hq, d), dtype=torch.bfloat16, device="cuda")))
+    rope = K.Rope(K.make_rope_config(d))
+    x = bf16(r, 8, hq + 2 * hk, d)
+    cu, ctx = (torch.tensor(a, dtype=torch.int32, device="cuda") for a in ([0, 2, 4, 6, 8], [0] * 4))
+
+    def step(pool, tables, kp, vp, place, pos, qo):
+        tables.reserve(ctx, cu, place, pos)
+        pool.rotate_append(0, rope, x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], pos, place, qo)
+
+    ctx.fill_(2)
+    for s in sets:
+        step(*s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(*sets[0])
+    for i in range(9):
+        ctx.add_(2 if i != 4 else -3)
+        x.copy_(bf16(r, 8, hq + 2 * hk, d))
+        g.replay()
+        step(*sets[1])
+        for a, b in zip(sets[0][2:], sets[1][2:]):
+            assert torch.equal(a, b)
+        assert torch.equal(sets[0][1].n_held, sets[1][1].n_held) and torch.equal(sets[0][1].ring_state, sets[1][1].ring_state)
+    assert sets[0][0].poll_error() == 0 and sets[1][0].poll_error() == 0
+
+
 # ------------------------------------------------------------------ kept keys
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 @pytest.mark.parametrize("d,adjacent,rot", [(128, False, 128), (64, True, 64), (64, False, 48), (128, True, 16), (128, False, 0)])
@@ -367,6 +432,8 @@ def test_reposition(kv, d, adjacent, rot, keep, bs, hk):
         for h in range(hk):
             kept[i, h, :m] = np.sort(r.choice(70000, m, replace=False))
     kept[0, 0, 0] = 0                               # stays where it is
+    if keep > 200:                                  # far away, on either side, and where the sums change
+        kept[2, 0, :9] = [(1 << 31) - 1, -(1 << 31) + 9, (1 << 24) + 1, -(1 << 24), (1 << 22) + 3, (1 << 22) + 5, 5 - (1 << 22), 7 - (1 << 22), 1 << 30]
     rope = K.Rope(K.make_rope_config(d, rot, theta=5e5, adjacent=adjacent, rot_scale=1.5))
     before = kp.clone()
     pool.reposition(0, rope, torch.from_numpy(kept).cuda(), torch.tensor(n_kept, dtype=torch.int32, device="cuda"), table)
@@ -377,7 +444,7 @@ def test_reposition(kv, d, adjacent, rot, keep, bs, hk):
         slot = table[i].cpu().numpy()[np.arange(m) // bs]
         for h in range(hk):
             x = want[0, slot, h, np.arange(m) % bs]
-            y, mag = rope_rows(x[:, None], (np.arange(m) - kept[i, h, :m])[:, None], freqs, adjacent=adjacent)
+            y, mag = rope_rows(x[:, None], (np.arange(m) - kept[i, h, :m].astype(np.int64))[:, None], freqs, adjacent=adjacent)
             y, mag = y[:, 0], mag[:, 0]
             if kv == "fp8":
                 y = np.clip(y, -448, 448)

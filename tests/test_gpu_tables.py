@@ -159,6 +159,21 @@ def test_bad_offsets_and_slots():
     assert place.tolist() == [-1, -1] + [int(t.t.block2slot[1, 0]) * 16 + i for i in range(2)] + [-1, -1] and t.pool.poll_error() == 0
 
 
+def test_tokens_of_no_batch():
+    """No requests at all: every token is nobody's."""
+    t = Tables(12, 2, 4, 16, 32, max_tokens=8)
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    place, pos = torch.full((7,), 99, dtype=torch.int64, device="cuda"), i32([99] * 7)
+    t.pool.places(i32([0]), none, t.t.block2slot[:0], place, pos)
+    assert place.tolist() == [-1] * 7 and pos.tolist() == [0] * 7
+    empty = K.BlockTables(t.pool, t.t.block2slot[:0], none, t.t.ring, t.t.ring_state)
+    place.fill_(99)
+    empty.reserve(none, i32([0]), place, pos)
+    empty.reserve(none)
+    assert place.tolist() == [-1] * 7 and t.pool.poll_error() == 0
+    t.check()
+
+
 def test_refusals():
     t = Tables(8, 2, 4, 16, 32, max_tokens=4)
     place = torch.zeros(5, dtype=torch.int64, device="cuda")
