@@ -15,7 +15,7 @@ namespace kvs {
 
 namespace {
 
-// cos and sin of m * f turns, two of them.  The product's upper word, a turn's fraction, becomes a float in [1, 2) by its upper 23
+// cos and sin of m * f turns, two of them (two_pi: its sign is the angle's).  The product's upper word, a turn's fraction, becomes a float in [1, 2) by its upper 23
 // bits, rounded (a conversion would take the unit that the cosines need); the fast functions are off by 2^-21 for arguments in
 // [-pi, pi].  Together 2^-20 at most.
 constexpr float kTwoPi = 6.2831853f;
@@ -23,8 +23,8 @@ __device__ __forceinline__ float turn_bits(unsigned m, unsigned long long f) {  
   const unsigned t = __umulhi(m, (unsigned)f) + (m * (unsigned)(f >> 32) + 0x80000100u);      // half a turn on, and half a step
   return __uint_as_float((t >> 9) | 0x3f800000u);
 }
-__device__ __forceinline__ void turn_cos_sin(unsigned m, unsigned long long f0, unsigned long long f1, float2& c, float2& s) {
-  const float2 x = __fmul2_rn(__fadd2_rn(make_float2(turn_bits(m, f0), turn_bits(m, f1)), make_float2(-1.5f, -1.5f)), make_float2(kTwoPi, kTwoPi));
+__device__ __forceinline__ void turn_cos_sin(unsigned m, float two_pi, unsigned long long f0, unsigned long long f1, float2& c, float2& s) {
+  const float2 x = __fmul2_rn(__fadd2_rn(make_float2(turn_bits(m, f0), turn_bits(m, f1)), make_float2(-1.5f, -1.5f)), make_float2(two_pi, two_pi));
   c = make_float2(__cosf(x.x), __cosf(x.y));
   s = make_float2(__sinf(x.x), __sinf(x.y));
 }
@@ -501,11 +501,14 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
 // A warp turns 32 / (d / 16) kept keys of a (request, kv head) a step, in place, each by its own angles, and goes on to the next ones,
 // `run` steps in all.  Rows come through a ring as above, their old positions and slots a step before them.
 //
-// Every key has angles of its own: 16 cosines and sines a lane and step, at 16 a clock of an SM 32 clocks, beside which some 190
-// instructions a step take 48 of each scheduler's: more than an 8-bit row's bytes (a step's 1 KB: 44 clocks at the rate of a copy).
-// 32 x 8 heads x 4096 keys of 128, E4M3: 64.0 us (40.2 for the bytes); one step a warp took 132, four at once and no ring 74.
-// 8 x 8 x 2048, bf16, half of them in L2: 6.9 us.
+// Every key has angles of its own: 16 cosines and sines a lane and step, at 16 a clock of an SM 32 clocks, beside which some 180
+// instructions a step take 45 of each scheduler's: more than an 8-bit row's bytes (a step's 1 KB: 44 clocks at the rate of a copy).
+// 32 x 8 heads x 4096 keys of 128, E4M3: 62.0 us (40.2 for the bytes), the schedulers 69% busy, the same with 24 to 32 warps an SM and 3
+// or 4 stages; one step a warp took 132, four at once and no ring 74.  Angles by fused fp32 multiplications of a split frequency, fewer
+// instructions than in integers, took 67: packed or not they use the unit that the rotation needs.
+// 8 x 8 x 2048 keys, bf16, half of them in L2: 5.8 us.
 constexpr int kRepThreads = 128;
+
 constexpr int kRepStages = 4;
 constexpr int kRepRun = 16;        // steps of a warp, at most
 
@@ -618,13 +621,13 @@ __global__ void __launch_bounds__(kRepThreads, 6)
     const Pairs p = to_pairs<LAY>(x);
     Pairs y;
     const unsigned m = magnitude(w.x);
-    const float sign = w.x < 0 ? -1.f : 1.f;      // (of the sines)
+    const float two_pi = w.x < 0 ? -kTwoPi : kTwoPi;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       float2 c, s;
-      turn_cos_sin(m, freq[2 * k], freq[2 * k + 1], c, s);
-      y.u[k] = __ffma2_rn(__fmul2_rn(p.v[k], make_float2(-sign, -sign)), s, __fmul2_rn(p.u[k], c));
-      y.v[k] = __ffma2_rn(__fmul2_rn(p.u[k], make_float2(sign, sign)), s, __fmul2_rn(p.v[k], c));
+      turn_cos_sin(m, two_pi, freq[2 * k], freq[2 * k + 1], c, s);
+      y.u[k] = __ffma2_rn(__fmul2_rn(p.v[k], make_float2(-1.f, -1.f)), s, __fmul2_rn(p.u[k], c));
+      y.v[k] = __ffma2_rn(p.u[k], s, __fmul2_rn(p.v[k], c));
       if (LAY != kHalves && !at.turns(2 * k, rd.rot)) {      // (owes nothing to its partner, which may be infinite)
         y.u[k] = p.u[k];
         y.v[k] = p.v[k];
