@@ -2,8 +2,8 @@
 
 Tolerance of a rotated element y of a pair of length M (the oracle's mag): the norm's sum of squares is of 16 products a lane and a few
 sums across lanes, its root and the weight's product take 4 more roundings: 12 * 2^-24 relative at most (the root halves the sum's).  The angle is
-off by 2^-32 turns, a rounding of pi * 2^-24 and the position times 2^-53 (2^-21 at 2^31), its cosine and sine by 2^-20.5 at most; two
-products and a sum: 3 * 2^-24.  Together below 2^-18 M.  Then one rounding: half a step of bf16, 2^-8 |y|, or of E4M3, 2^-4 |y| or 2^-10 of the
+rounded to 2^-24 turns (2^-21.3), its product with 2 pi by pi * 2^-24 (2^-22.3), and off by the position times 2^-53 (2^-22 at 2^31); its cosine and
+sine are off by 2^-21 at most; two products and a sum: 3 * 2^-24.  Together below 2^-18 M.  Then one rounding: half a step of bf16, 2^-8 |y|, or of E4M3, 2^-4 |y| or 2^-10 of the
 code's unit below its normal range."""
 import numpy as np
 import pytest
