@@ -218,9 +218,25 @@ struct RowWarp {
     reinterpret_cast<uint4*>(to)[at.c0] = r.c0;
     reinterpret_cast<uint4*>(to)[at.c1] = r.c1;
   }
-  __device__ __forceinline__ void store_e4m3(void* to, float (&x)[16], float scale) const {
+  // x / scale, rounded as the quantiser's division is.  With the reciprocal's rounding r at hand (0: scale is extreme) the quotient comes
+  // from two corrections of x r by their exact remainders (Markstein, IBM J. Res. Dev. 34, 1990): the first is within a unit in the
+  // last place, the second rounds correctly.  Quotients that saturate or become zero need none: the former may have no finite
+  // remainder, the latter would lose their sign.  (16 divisions took 0.6 us of one token's 2.3.)
+  __device__ __forceinline__ void store_e4m3(void* to, float (&x)[16], float scale, float r) const {
+    if (r != 0.f) {
+      const float2 rr = make_float2(r, r), ss = make_float2(-scale, -scale);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = __fdiv_rn(x[j], scale);
+      for (int j = 0; j < 16; j += 2) {
+        const float2 y = make_float2(x[j], x[j + 1]), q0 = __fmul2_rn(y, rr);
+        const float2 q1 = __ffma2_rn(__ffma2_rn(q0, ss, y), rr, q0);
+        const float2 q2 = __ffma2_rn(__ffma2_rn(q1, ss, y), rr, q1);
+        x[j] = fabsf(q0.x) < 1024.f && fabsf(q0.x) > 0x1p-12f ? q2.x : q0.x;
+        x[j + 1] = fabsf(q0.y) < 1024.f && fabsf(q0.y) > 0x1p-12f ? q2.y : q0.y;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] = __fdiv_rn(x[j], scale);
+    }
     reinterpret_cast<uint2*>(to)[at.c0] = pack_e4m3(x);
     reinterpret_cast<uint2*>(to)[at.c1] = pack_e4m3(x + 8);
   }
@@ -287,7 +303,7 @@ __global__ void __launch_bounds__(kFewThreads)
     if (DST == kPoolFp8) {
       float x[16];
       unpack_bf16(raw, x);
-      w.store_e4m3(to, x, a.v_scale);
+      w.store_e4m3(to, x, a.v_scale, a.v_rcp);
     } else {
       w.store_bf16(to, raw);
     }
@@ -308,7 +324,7 @@ __global__ void __launch_bounds__(kFewThreads)
   const PlaceRow p = place_row(a, place);
   if (!there || !p.there) return;
   unsigned char* to = a.kpool + (p.row + (size_t)h * a.bs) * (DST == kPoolFp8 ? D : 2 * D);
-  if (DST == kPoolFp8) w.store_e4m3(to, x, a.k_scale);
+  if (DST == kPoolFp8) w.store_e4m3(to, x, a.k_scale, a.k_rcp);
   else w.store_bf16(to, pack_bf16(x));
 }
 
@@ -467,7 +483,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
           if (DST == kDense) {
             if (h < a.k.n) w.store_bf16(to, pack_bf16(x));
           } else if (h < a.k.n && pl.there) {
-            if (DST == kPoolFp8) w.store_e4m3(in_pool, x, a.k_scale);
+            if (DST == kPoolFp8) w.store_e4m3(in_pool, x, a.k_scale, a.k_rcp);
             else w.store_bf16(in_pool, pack_bf16(x));
           }
         }
@@ -481,7 +497,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
             if (DST == kPoolFp8) {
               float x[16];
               unpack_bf16(raw, x);
-              w.store_e4m3(in_pool, x, a.v_scale);
+              w.store_e4m3(in_pool, x, a.v_scale, a.v_rcp);
             } else {
               w.store_bf16(in_pool, raw);
             }

@@ -388,6 +388,9 @@ kvs_status kvs_pool_rotate_append(kvs_pool* c, const kvs_rope* rope, int layer, 
   a.fp8 = d.fp8;
   a.k_scale = d.k_scale;
   a.v_scale = d.v_scale;
+  auto rcp = [](float s) { return s >= 0x1p-60f && s <= 0x1p60f ? 1.f / s : 0.f; };
+  a.k_rcp = rcp(d.k_scale);
+  a.v_rcp = rcp(d.v_scale);
   a.err = c->err;
   a.n_tok = n_tok;
   c->launches += 1;

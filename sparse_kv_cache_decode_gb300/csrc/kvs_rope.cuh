@@ -33,6 +33,7 @@ struct RopeRows {
   unsigned char *kpool, *vpool;
   int n_slots, bs, log2bs, fp8;
   float k_scale, v_scale;
+  float k_rcp, v_rcp;           // 1 / scale, rounded; 0 where scale is beyond 2^+-60
   unsigned* err;
   int n_tok;
 };

@@ -304,6 +304,24 @@ def test_append_as_pool_append_does():
         assert torch.equal(got[0][at], c.rows(c.kp)[at]) and torch.equal(got[1][at], c.rows(c.vp)[at])
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.05, 0.0625, 0.3333333, 1.9999999, 1e-3, 7.77e5, 3.0 * 2.0 ** -61, 2.0 ** -60, 2.0 ** 60, 1.5 * 2.0 ** 61, 1e-38, 3e38])
+def test_every_value_is_quantised_as_the_quantiser_does(scale):
+    """All bf16 patterns (infinities and NaN among them) as V rows of an E4M3 pool."""
+    hk, d, bs = 8, 128, 16
+    n = 65536 // (hk * d)
+    kp, vp = (torch.zeros((1, n // bs, hk, bs, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+    pool = K.Pool(K.make_pool_config(1, n // bs, hk, hk, d, bs, n, 1, n, kv_dtype="fp8", k_scale=scale, v_scale=scale), kp, vp)
+    v = torch.arange(-32768, 32768, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.bfloat16).view(n, hk, d)
+    q = torch.zeros_like(v)
+    place = torch.arange(n, device="cuda")
+    pool.rotate_append(0, K.Rope(K.make_rope_config(d, rot_dim=0)), q, v, v.clone(), torch.zeros(n, dtype=torch.int32, device="cuda"), place, q.clone())
+    codes = torch.empty(65536, dtype=torch.uint8, device="cuda")
+    K.quantize_e4m3(v.view(-1), codes, scale)
+    for p in (vp, kp):                              # K, neither normed nor rotated, is the same values
+        got = p[0].transpose(1, 2).reshape(-1)
+        assert torch.equal(got, codes), (got != codes).nonzero()[:5]
+
+
 def test_append_layers_and_strides():
     c = PoolRows(6, 30, 6, 2, 128, n_layer=3, norm=True)
     want = c.go(layer=0)
