@@ -512,7 +512,7 @@ kvs_status kvs_rope_destroy(kvs_rope* rope);
 /* The heads of queries and of keys of n_tok tokens, as above: for kvs_decode_step (its q and k_new), an index of one's own,
  * or the part of a latent row that turns.  Token t's head h is at d_x + t * x_stride + h * x_head_stride (elements: multiples of 8;
  * rows 16-byte aligned, not overlapping); norms [head_dim] fp32, 16-byte aligned, or NULL; n_q_head or n_k_head may be 0 (its pointers
- * are not used), at most 1024.  pos: n_axis rows of [n_tok] int32, pos_stride apart (0: one row for all axes).  Outputs are
+ * are not used), at most 1024.  Launches on the current device.  pos: n_axis rows of [n_tok] int32, pos_stride apart (0: one row for all axes).  Outputs are
  * written in place (the same pointer and strides) or apart from the inputs and from one another. */
 kvs_status kvs_rotate(const kvs_rope* rope, const void* d_q, long long q_stride, long long q_head_stride, int n_q_head,
                       const float* d_q_norm, void* d_q_out, long long q_out_stride, long long q_out_head_stride, const void* d_k,

@@ -151,6 +151,15 @@ def binding():
     return _binding
 
 
+class _Fast:
+    """binding()'s functions, loaded on first use."""
+
+    def __getattr__(self, name):
+        f = getattr(binding(), name)
+        setattr(self, name, f)
+        return f
+
+
 class _Calls:
     """The C ABI's functions: those of the compiled binding where it has them, else through ctypes."""
 
@@ -161,7 +170,7 @@ class _Calls:
         return f
 
 
-calls = _Calls()
+fast, calls = _Fast(), _Calls()
 
 
 def _check(status: int, where: str) -> None:

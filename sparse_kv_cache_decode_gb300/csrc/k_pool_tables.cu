@@ -12,7 +12,7 @@
 //
 // Bound by latencies: the launch, one read of the lengths, the scan, a table entry, 3.0 us of which the launch is half (64 requests, a
 // token each).  24 prompts of 494000 tokens in all: 6 us, four consecutive tokens a thread (6 MB of places and positions,
-// 0.9 us at the rate of a copy); without the ring's state to write last, as a launch of its own for the tokens, 11 us.
+// 0.9 us at the rate of a copy); the blocks and the tokens in a launch each took 4 us more.
 #include <algorithm>
 
 #include "kvs_rope.cuh"
@@ -275,7 +275,8 @@ cudaError_t launch_pool_tables(const PoolDims& d, const PoolTables& t, unsigned*
   const long long work = t.cu_q ? t.n_tok / (many ? 4 : 1) : (long long)t.n_req * d.nb_max / 4;
   const int grid = (int)std::max(1ll, std::min<long long>((work + kTabThreads - 1) / kTabThreads, t.cu_q ? sms * 4 : 64));
   auto go = [&](auto kernel) {
-    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), (7 * kPoolMaxReq + 3) * 4);
+    cudaError_t e = cudaSuccess;      // (up to 47 KB need no asking)
+    if (smem > 47 * 1024) e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), (7 * kPoolMaxReq + 3) * 4);
     if (e != cudaSuccess) return e;
     launch_pdl(kernel, dim3(grid), dim3(kTabThreads), (size_t)smem, s, d, t, ticket, err);
     return cudaGetLastError();

@@ -281,8 +281,7 @@ __global__ void __launch_bounds__(kFewThreads)
     freq[j] = rp->freq[w.lane + 32 * j];      // (past the rotated pairs: an angle of 0)
     pos[j] = rp->axis[w.lane + 32 * j];
   }
-  const long long item = (long long)blockIdx.x * (kFewThreads / 32) + (threadIdx.x >> 5);
-  const int tok = (int)(item / steps), it = (int)(item - (long long)tok * steps);
+  const int item = blockIdx.x * (kFewThreads / 32) + (threadIdx.x >> 5), tok = item / steps, it = item - tok * steps;
   kvs_pdl_entry();
   if (tok >= a.n_tok) return;
   const bool is_q = it < iq, is_v = it >= iq + ik;
@@ -676,9 +675,9 @@ cudaError_t launch_rows(const RopeDims& rd, const RopeRows& a, cudaStream_t s) {
     return cudaGetLastError();
   }
   constexpr int NW = kRopeThreads / 32;
-  const int grid = std::min((int)std::min<long long>((warps + NW - 1) / NW, 1 << 20), sms * kRopeCtas), smem = kRopeThreads * kStages * 32;
-  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(rope_rows_kernel<D, LAY, DST>), smem);
-  if (e != cudaSuccess) return e;
+  constexpr int smem = kRopeThreads * kStages * 32;
+  static_assert(smem + NW * D / 2 * 8 <= 48 * 1024, "what a kernel may use without asking");
+  const int grid = (int)std::min<long long>((warps + NW - 1) / NW, sms * kRopeCtas);
   launch_pdl(rope_rows_kernel<D, LAY, DST>, dim3(grid), dim3(kRopeThreads), (size_t)smem, s, rd, a, iq, ik, steps);
   return cudaGetLastError();
 }

@@ -355,7 +355,7 @@ kvs_status kvs_pool_rotate_append(kvs_pool* c, const kvs_rope* rope, int layer, 
   if (n_tok == 0) return KVS_OK;
   if (!d_q || !d_k || !d_v || !d_pos || !d_place || !d_q_out) return KVS_ERR_INVALID_ARG;
   const long long q_row = (long long)d.Hq * d.d, kv_row = (long long)d.Hkv * d.d;
-  constexpr long long most = 1ll << 40;      // (extents stay in 64 bits)
+  const long long most = (1ll << 40) / n_tok;      // (extents stay in 64 bits, and within any memory)
   if (q_stride % 8 || kv_stride % 8 || q_out_stride % 8 || q_stride < q_row || kv_stride < kv_row || q_out_stride < q_row || q_stride > most ||
       kv_stride > most || q_out_stride > most)
     return KVS_ERR_INVALID_ARG;

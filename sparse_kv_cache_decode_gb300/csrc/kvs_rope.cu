@@ -41,9 +41,10 @@ bool rope_dims(const kvs_rope_config* c, RopeDims* d) {
 // Rows of `n` heads of d elements of n_tok tokens: 16-byte aligned vectors, no two rows sharing an element (a token's heads
 // together, or a head's tokens together).
 bool rows_ok(const void* p, long long tok, long long head, int n, int d, int n_tok) {
-  constexpr long long most = 1ll << 40;      // (the products of strides and counts stay in 64 bits)
-  if (!p || (reinterpret_cast<uintptr_t>(p) & 15u) || tok % 8 || head % 8 || tok > most || head > most) return false;
+  if (!p || (reinterpret_cast<uintptr_t>(p) & 15u) || tok % 8 || head % 8) return false;
   if ((n > 1 && head < d) || (n_tok > 1 && tok < d)) return false;
+  constexpr long long most = 1ll << 40;      // (extents stay in 64 bits, and within any memory)
+  if ((n > 1 && head > most / n) || (n_tok > 1 && tok > most / n_tok)) return false;
   return n == 1 || n_tok <= 1 || tok >= (n - 1) * head + d || head >= (n_tok - 1) * tok + d;
 }
 

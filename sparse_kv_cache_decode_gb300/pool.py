@@ -19,12 +19,12 @@ import functools
 
 import torch
 
-from . import KV_DTYPE, KvsError, KvsPoolConfig, _check, binding, calls
+from . import KV_DTYPE, KvsError, KvsPoolConfig, _check, calls
+from . import fast as _fast
 from .rope import Rope, _norm, _positions
 
 _BF16 = (torch.bfloat16, torch.int16)
 _FP8 = (torch.float8_e4m3fn, torch.uint8)
-_fast = binding()
 _I32, _I64, _F32 = (torch.int32,), (torch.int64,), (torch.float32,)
 
 
@@ -218,7 +218,7 @@ class Pool:
         """kvs_pool_rotate_append: q [n_tok][H_q][d] normed and rotated into q_out; k and v [n_tok][H_kv][d] to their places, k normed and
         rotated as well."""
         hq, hk, d = self._heads
-        if self.L is calls and self.h is not None and rope.h is not None:
+        if self.L is calls and self.h is not None and type(rope) is Rope and rope.h is not None:
             status = _fast.rotate_append(self.h, rope.h, self.index, hq, hk, d, rope.n_axis, layer, q, k, v, pos, place, q_out, q_norm, k_norm, stream)
             if status == 0:
                 return

@@ -13,11 +13,11 @@ import ctypes
 
 import torch
 
-from . import KvsError, KvsRopeConfig, _check, binding, calls
+from . import KvsError, KvsRopeConfig, _check, calls
+from . import fast as _fast
 
 _BF16 = (torch.bfloat16, torch.int16)
 _I32, _F32 = (torch.int32,), (torch.float32,)
-_fast = binding()
 
 
 def rope_axes(sections, cycle: bool = False) -> list:

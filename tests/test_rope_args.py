@@ -66,7 +66,7 @@ def test_rows_that_are_refused(K):
     r = K.Rope(K.make_rope_config(128))
     bad = [dict(q=0), dict(qo=0), dict(k=0), dict(ko=0), dict(pos=0), dict(n=-1), dict(hq=-1), dict(hk=-1), dict(hq=1025), dict(ps=-1),
            dict(q=A + 8), dict(ko=D + 2), dict(qs=260), dict(qoh=132), dict(qh=64), dict(qs=200), dict(kos=120), dict(qn=8), dict(kn=4),
-           dict(qs=128, qh=384), dict(qs=128, qh=504), dict(qs=64, qh=4096), dict(qs=1 << 62), dict(qh=1 << 62),
+           dict(qs=128, qh=384), dict(qs=128, qh=504), dict(qs=64, qh=4096), dict(qs=1 << 62), dict(qh=1 << 62), dict(qs=1 << 39, n=1 << 30),
            # outputs over inputs or each other: shifted by a token or a head, of other strides, over the other's rows
            dict(qo=A + 512), dict(qo=A + 256), dict(qo=A, qos=512), dict(qo=C), dict(ko=A), dict(ko=B), dict(ko=B + 256), dict(ko=C + 256),
            dict(qs=768, qh=384, qo=A + 128, qos=768, qoh=384),          # half a head further
