@@ -32,8 +32,9 @@ __device__ __forceinline__ unsigned magnitude(int pos) { return pos < 0 ? 0u - (
 
 // The parameters by their address: lanes that read entries of their own take one load, where an indexed read of the constant bank is
 // repeated for every lane (128 tokens of 12 steps 3.0 us that way, 2.45 by address; one token 1.83 and 1.65).
-__device__ __forceinline__ const RopeDims* by_address(const RopeDims& rd) {
-  const RopeDims* p = &rd;
+template <typename T>
+__device__ __forceinline__ const T* by_address(const T& rd) {
+  const T* p = &rd;
   asm volatile("" : "+l"(p));
   return p;
 }
@@ -136,7 +137,7 @@ struct RowWarp {
   // (a, b) -> (a cw + b sw, b dw + a ew): the rotation and the norm's weights
   float2 cw[4], sw[4], dw[4], ew[4];
 
-  __device__ __forceinline__ RowWarp(const RopeDims& rd)
+  __device__ __forceinline__ RowWarp(const RopeParams<D / 2>& rd)
       : lane(threadIdx.x & 31), sub((threadIdx.x & 31) / LPH), at(rd.rot, (threadIdx.x & 31) % LPH), rot(rd.rot), rot_scale(rd.rot_scale), eps(rd.eps) {}
 
   // cos and sin of every pair of the row, by all lanes, to shared memory
@@ -268,14 +269,14 @@ constexpr int kFewSteps = 16;      // steps for each SM, at most
 
 template <int D, int LAY, int DST>
 __global__ void __launch_bounds__(kFewThreads)
-    rope_few_kernel(const __grid_constant__ RopeDims rd, const __grid_constant__ RopeRows a, int iq, int ik, int steps) {
+    rope_few_kernel(const __grid_constant__ RopeParams<D / 2> rd, const __grid_constant__ RopeRows a, int iq, int ik, int steps) {
   using W = RowWarp<D, LAY>;
   __shared__ __align__(16) float2 cos_sin[kFewThreads / 32][D / 2];
   W w(rd);
   float2* turn = cos_sin[threadIdx.x >> 5];
   unsigned long long freq[W::NP];
   int pos[W::NP];
-  const RopeDims* const rp = by_address(rd);
+  const auto* const rp = by_address(rd);
 #pragma unroll
   for (int j = 0; j < W::NP; ++j) {
     freq[j] = rp->freq[w.lane + 32 * j];      // (past the rotated pairs: an angle of 0)
@@ -350,7 +351,7 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
 
 template <int D, int LAY, int DST>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
-    rope_rows_kernel(const __grid_constant__ RopeDims rd, const __grid_constant__ RopeRows a, int iq, int ik, int steps) {
+    rope_rows_kernel(const __grid_constant__ RopeParams<D / 2> rd, const __grid_constant__ RopeRows a, int iq, int ik, int steps) {
   using W = RowWarp<D, LAY>;
   constexpr int NW = kRopeThreads / 32;
   __shared__ __align__(16) float2 cos_sin[NW][D / 2];
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
   const uint32_t ring_base = smem_u32(ring_all + (threadIdx.x >> 5) * (kStages * 64) + w.lane);
   unsigned long long freq[W::NP];
   int axis[W::NP];
-  const RopeDims* const rp = by_address(rd);
+  const auto* const rp = by_address(rd);
 #pragma unroll
   for (int j = 0; j < W::NP; ++j) {
     freq[j] = rp->freq[w.lane + 32 * j];      // (past the rotated pairs: an angle of 0)
@@ -553,7 +554,7 @@ __device__ __forceinline__ void unpack_e4m3(uint32_t codes, float* x) {
 
 template <int D, int LAY, bool FP8>
 __global__ void __launch_bounds__(kRepThreads, 6)
-    pool_reposition_kernel(PoolDims d, const __grid_constant__ RopeDims rd, unsigned char* kpool, const int* __restrict__ kept,
+    pool_reposition_kernel(PoolDims d, const __grid_constant__ RopeParams<D / 2> rd, unsigned char* kpool, const int* __restrict__ kept,
                            const int* __restrict__ n_kept, const int* __restrict__ table, int keep, int run, unsigned* err) {
   constexpr int LPH = D / 16, HPW = 32 / LPH, ROW = FP8 ? D : 2 * D, CH = FP8 ? 8 : 16, S = kRepStages;      // CH: bytes of a chunk
   __shared__ __align__(16) unsigned char ring_all[kRepThreads / 32][S][2][32 * CH];
@@ -563,7 +564,7 @@ __global__ void __launch_bounds__(kRepThreads, 6)
   const uint32_t ring = smem_u32(&ring_all[threadIdx.x >> 5][0][0][lane * CH]);
   int2* what = &what_all[threadIdx.x >> 5][0][lane];
   unsigned long long freq[8];
-  const RopeDims* const rp = by_address(rd);
+  const auto* const rp = by_address(rd);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     freq[j] = at.turns(j, rd.rot) ? rp->freq[at.pair(j)] : 0ull;
@@ -663,8 +664,18 @@ __global__ void __launch_bounds__(kRepThreads, 6)
   }
 }
 
+// The pairs that rows of d elements have (a kernel's parameters cost host time by their bytes: 0.15 us for 1.3 KB)
+template <int D>
+RopeParams<D / 2> params_of(const RopeDims& r) {
+  RopeParams<D / 2> p = {r.d, r.rot, r.n_axis, r.adjacent, r.rot_scale, r.eps, {}, {}};
+  std::copy_n(r.freq, D / 2, p.freq);
+  std::copy_n(r.axis, D / 2, p.axis);
+  return p;
+}
+
 template <int D, int LAY, int DST>
-cudaError_t launch_rows(const RopeDims& rd, const RopeRows& a, cudaStream_t s) {
+cudaError_t launch_rows(const RopeDims& rope, const RopeRows& a, cudaStream_t s) {
+  const RopeParams<D / 2> rd = params_of<D>(rope);
   constexpr int HPW = 32 / (D / 16);
   const int sms = device_sm_count();
   const int iq = (a.q.n + HPW - 1) / HPW, ik = (a.k.n + HPW - 1) / HPW, steps = iq + ik * (DST == kDense ? 1 : 2);
@@ -689,8 +700,9 @@ cudaError_t launch_rows(const RopeDims& rd, const RopeRows& a, cudaStream_t s) {
 }
 
 template <int D, bool FP8>
-cudaError_t launch_reposition(const PoolDims& d, const RopeDims& rd, unsigned char* k, const int* kept, const int* n_kept, const int* table,
+cudaError_t launch_reposition(const PoolDims& d, const RopeDims& rope, unsigned char* k, const int* kept, const int* n_kept, const int* table,
                               int n_req, int keep, unsigned* err, cudaStream_t s) {
+  const RopeParams<D / 2> rd = params_of<D>(rope);
   constexpr int HPW = 32 / (D / 16), NW = kRepThreads / 32;
   // steps of a warp: all of them, if one wave of warps does it, in runs that still even out over several waves if not
   const long long steps = (long long)n_req * d.Hkv * ((keep + HPW - 1) / HPW);

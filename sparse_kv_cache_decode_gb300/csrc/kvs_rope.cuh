@@ -7,13 +7,15 @@ namespace kvs {
 constexpr int kRopeMaxPairs = 128;
 constexpr int kRopeMaxAxes = 8;
 
-// What a kvs_rope holds, as the kernels see it (passed by value).
-struct RopeDims {
+// What a kvs_rope holds, for rows of up to PAIRS pairs.
+template <int PAIRS>
+struct RopeParams {
   int d, rot, n_axis, adjacent;
   float rot_scale, eps;
-  unsigned long long freq[kRopeMaxPairs];   // turns per position, mod 1, in units of 2^-64
-  unsigned char axis[kRopeMaxPairs];
+  unsigned long long freq[PAIRS];   // turns per position, mod 1, in units of 2^-64
+  unsigned char axis[PAIRS];
 };
+using RopeDims = RopeParams<kRopeMaxPairs>;
 
 // Heads of all tokens, in and out, strides in elements.
 struct RopeHeads {

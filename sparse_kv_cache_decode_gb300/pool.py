@@ -219,7 +219,7 @@ class Pool:
         rotated as well."""
         hq, hk, d = self._heads
         if self.L is calls and self.h is not None and type(rope) is Rope and rope.h is not None:
-            status = _fast.rotate_append(self.h, rope.h, self.index, hq, hk, d, rope.n_axis, layer, q, k, v, pos, place, q_out, q_norm, k_norm, stream)
+            status = _fast.rotate_append(self._address, rope.address, self.index, hq, hk, d, rope.n_axis, layer, q, k, v, pos, place, q_out, q_norm, k_norm, stream)
             if status == 0:
                 return
             if status is not None:
@@ -239,6 +239,10 @@ class Pool:
         qn, kn = _norm(q_norm, "q_norm", d, i), _norm(k_norm, "k_norm", d, i)
         self._call(self.L.kvs_pool_rotate_append, "kvs_pool_rotate_append", h, _int(layer, "layer"), a[0], a[1], b[0], c[0], b[1], qn, kn, pp, ps, pl,
                    n_tok, o[0], o[1], _fast.stream(i) if stream is None else self._stream(stream))
+
+    @functools.cached_property
+    def _address(self):
+        return self.h.value
 
     @functools.cached_property
     def _heads(self):
@@ -289,7 +293,7 @@ class BlockTables:
         call's tokens go, and their positions."""
         p, n_req = self.pool, self.n_req
         if p.L is calls and p.h is not None:
-            status = _fast.reserve(p.h, p.index, n_req, *self._ptrs, ctx_len, cu_q, place, pos, pos_delta, stream)
+            status = _fast.reserve(p._address, p.index, n_req, *self._ptrs, ctx_len, cu_q, place, pos, pos_delta, stream)
             if status == 0:
                 return
             if status is not None:

@@ -107,12 +107,12 @@ class Rope:
         self.L = calls
         h = ctypes.c_void_p()
         _check(self.L.kvs_rope_create(ctypes.byref(cfg), ctypes.byref(h)), "kvs_rope_create")
-        self.h = h
+        self.h, self.address = h, h.value
 
     def close(self):
         if getattr(self, "h", None):
             self.L.kvs_rope_destroy(self.h)
-            self.h = None
+            self.h = self.address = None
 
     def __del__(self):
         try:
@@ -124,7 +124,7 @@ class Rope:
         """kvs_rotate: q [n_tok][H_q][d] into q_out and, if given, k [n_tok][H_k][d] into k_out (in place: the same tensor)."""
         if self.h is None:
             raise ValueError("Rope: closed")
-        status = _fast.rotate(self.h, self.d, self.n_axis, q, pos, q_out, k, k_out, q_norm, k_norm, stream)
+        status = _fast.rotate(self.address, self.d, self.n_axis, q, pos, q_out, k, k_out, q_norm, k_norm, stream)
         if status == 0:
             return
         if status is not None:
