@@ -490,7 +490,8 @@ kvs_status kvs_pool_places(kvs_pool* pool, const int* d_cu_q, const int* d_ctx_l
  * for the pairs i = 0 .. rot_dim / 2 - 1 of its first rot_dim elements: (a, b) = (2 i, 2 i + 1) if adjacent, else
  * (i, i + rot_dim / 2).  A token has a position on each of n_axis axes (time, height and width of an image's patch, say), and each pair
  * turns by one of them.  Positions are any int32; cosines and sines are good to 2^-20, and the
- * angle to 2^-52 of its size.  The sum of a normed row's squares must be finite in fp32. */
+ * angle to 2^-52 of its size.  The sum of a normed row's squares must be finite in fp32.  A row's result
+ * does not depend on the other rows of a call. */
 typedef struct {
   int head_dim;                 /* 64, 128 or 256 (a pool's own for the calls on a pool) */
   int rot_dim;                  /* a multiple of 16, at most head_dim; 0: no rotation */

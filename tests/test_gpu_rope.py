@@ -78,6 +78,18 @@ def test_dense(d, adjacent, n, hq, hk):
     c.check(*c.rotate())
 
 
+@pytest.mark.parametrize("d,rot,adjacent", [(64, 64, False), (64, 48, True), (128, 128, False), (128, 96, False), (256, 256, True)])
+def test_a_row_does_not_depend_on_the_others(d, rot, adjacent):
+    """A prompt in one call, in chunks and token by token gives the same bits."""
+    c = Case(50, 3001, 9, 3, d, rot=rot, adjacent=adjacent, sections=[rot // 4, rot // 4])
+    whole = c.rotate()
+    qo, ko = torch.zeros_like(c.q), torch.zeros_like(c.k)
+    at = [0, 1, 2, 39, 500, 501, 3001]
+    for a, b in zip(at, at[1:]):
+        c.rope.rotate(c.q[a:b], c.pos[:, a:b].contiguous(), qo[a:b], c.k[a:b], ko[a:b], q_norm=c.wq, k_norm=c.wk)
+    assert torch.equal(qo, whole[0]) and torch.equal(ko, whole[1])
+
+
 @pytest.mark.parametrize("d,rot", [(64, 0), (64, 16), (64, 48), (128, 16), (128, 64), (128, 96), (128, 112), (256, 64), (256, 144)])
 @pytest.mark.parametrize("adjacent", [False, True])
 @pytest.mark.parametrize("norm", [False, True])
