@@ -41,10 +41,18 @@ def _run(cmd, what):
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
+def _torch():
+    """torch's folder; None without torch, where the ctypes binding of the C ABI is all there is."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec else None
+
+
 def _compile_binding():
     src, obj = os.path.join(CSRC, "binding.cpp"), os.path.join(OUT_DIR, "binding.o")
+    torch = _torch()
+    if torch is None:
+        return None
     if _stale(obj, [src] + headers()):
-        torch = importlib.util.find_spec("torch").submodule_search_locations[0]
         cuda = os.path.dirname(os.path.dirname(NVCC))
         inc = [f"-I{torch}/include", f"-I{torch}/include/torch/csrc/api/include", f"-I{cuda}/include", f"-I{sysconfig.get_paths()['include']}"]
         _run(["g++", "-O2", "-std=c++17", "-fPIC"] + inc + ["-c", src, "-o", obj + ".tmp"], src)
@@ -53,9 +61,9 @@ def _compile_binding():
 
 
 def _link_binding(obj):
-    if _stale(BINDING, [obj]):
+    if obj is not None and _stale(BINDING, [obj]):
         tmp = BINDING + f".tmp{os.getpid()}"
-        torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+        torch = _torch()
         _run(["g++", "-shared", "-o", tmp, obj, f"-L{OUT_DIR}", "-lkvs", "-Wl,-rpath,$ORIGIN", f"-L{torch}/lib", "-ltorch_python", "-ltorch_cpu",
               "-lc10", "-lc10_cuda"], BINDING)
         os.replace(tmp, BINDING)

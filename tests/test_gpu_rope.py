@@ -114,6 +114,11 @@ def test_several_axes(sections, cycle, adjacent, n):
     qo, ko = torch.empty_like(c.q), torch.empty_like(c.k)
     c.rope.rotate(c.q, one, qo, c.k, ko, q_norm=c.wq, k_norm=c.wk)
     assert torch.equal(qo, whole[0]) and torch.equal(ko, whole[1])
+    wide = torch.full((c.rope.n_axis, n + 5), 77, dtype=torch.int32, device="cuda")       # a part of longer rows of positions
+    wide[:, 3:n + 3] = c.pos
+    qo.zero_()
+    c.rope.rotate(c.q, wide[:, 3:n + 3], qo, q_norm=c.wq)
+    assert torch.equal(qo, whole[0])
 
 
 @pytest.mark.parametrize("far", [1, 1 << 24, (1 << 31) - 1])

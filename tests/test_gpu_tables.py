@@ -219,6 +219,38 @@ def test_captured_and_replayed():
     assert t.pool.poll_error() == 0
 
 
+def test_two_pools_at_once():
+    """Large calls of two pools (many CTAs, each pool's own workspace) on two streams, in graphs replayed beside each other."""
+    sets = [Tables(60 + i, 300, 40000, 16, 4000, max_tokens=1 << 19) for i in range(2)]
+    r = np.random.default_rng(3)
+    lens = [r.integers(0, 2000, 300).tolist() for _ in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    bufs, graphs = [], []
+    for t, n in zip(sets, lens):
+        cu = i32(np.concatenate([[0], np.cumsum(n)]))
+        bufs.append((i32(n), cu, torch.zeros(sum(n), dtype=torch.int64, device="cuda"), i32([0] * sum(n)), i32([0] * 300)))
+    torch.cuda.synchronize()
+    for t, b, s in zip(sets, bufs, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            t.t.reserve(b[0], b[1], b[2], b[3])
+            t.t.reserve(b[4])
+            t.t.reserve(b[0], b[1], b[2], b[3])
+        graphs.append(g)
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for t, n, b in zip(sets, lens, bufs):
+            assert t.o.reserve(n) and t.o.reserve([0] * 300) and t.o.reserve(n)
+            t.check()
+            assert b[2].tolist() == t.o.places(n, b[1].tolist(), sum(n))[0] and t.pool.poll_error() == 0
+            t.o.reserve([0] * 300)
+            t.t.reserve(b[4])
+            t.check()
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_serving_run(kv):
