@@ -60,18 +60,40 @@ Span span(const void* p, long long tok, long long head, int n, int d, int n_tok)
   if (n_tok == 1) s.tok = (n - 1) * s.head + s.d;
   return s;
 }
-// Whether the two may share a byte: apart as a whole, or columns of rows of the same length that are apart, or
-// interleaved by heads of the same stride that are apart.
+// Whether `at` + i * step lies within (-d, d) for a whole i in [lo, hi] (lo <= 0 <= hi, step >= d).
+bool comes_near(long long at, long long step, int lo, int hi, int d) {
+  if (at > -d && at < d) return true;
+  const long long i = at > 0 ? -(at / step) : -at / step;      // rounded towards `at`'s side; the other neighbour is one further
+  for (const long long k : {i, at > 0 ? i - 1 : i + 1})
+    if (k >= lo && k <= hi && at + k * step > -d && at + k * step < d) return true;
+  return false;
+}
+// Whether the two may share a byte.  Apart are: all of both; columns of rows of the same length; heads of the same stride
+// between one another's; and, found row by row, the rows of two of the same strides or of single tokens.  (A stride that
+// only one of them has, because the other has a single head, is the stride of both.)  Strides that differ otherwise: they may.
 bool may_meet(const Span& a, const Span& b) {
   if (a.end() <= b.p || b.end() <= a.p) return false;
   const Span &x = a.p <= b.p ? a : b, &y = a.p <= b.p ? b : a;
   const long long off = (long long)(y.p - x.p);
+  const int d = x.d, n_tok = x.n_tok;      // (the same of both)
   auto apart = [](long long off, long long period, long long wx, long long wy) {
     const long long o = off % period;
     return o >= wx && o + wy <= period;
   };
-  if (x.tok == y.tok && apart(off, x.tok, (x.n - 1) * x.head + x.d, (y.n - 1) * y.head + y.d)) return false;
-  return !(x.head == y.head && x.tok == y.tok && x.tok % x.head == 0 && apart(off, x.head, x.d, y.d));
+  if (n_tok > 1 && x.tok == y.tok && apart(off, x.tok, (x.n - 1) * x.head + d, (y.n - 1) * y.head + d)) return false;
+  if (x.n == 1 || y.n == 1 || x.head == y.head) {
+    const long long head = x.n > 1 ? x.head : y.head;
+    if ((n_tok == 1 || (x.tok == y.tok && x.tok % head == 0)) && apart(off, head, d, d)) return false;
+    if (n_tok > 1 && x.tok != y.tok) return true;
+    const int ahead = n_tok - 1;
+    for (int j = 1 - x.n; j < y.n; ++j)      // y's head less x's
+      if (comes_near(off + j * head, n_tok > 1 ? x.tok : d, -ahead, ahead, d)) return true;
+    return false;
+  }
+  if (n_tok > 1) return true;
+  for (int j = 0; j < x.n; ++j)
+    if (comes_near(off - j * x.head, y.head, 0, y.n - 1, d)) return true;
+  return false;
 }
 bool same(const Span& a, const Span& b) { return a.p == b.p && a.n == b.n && a.tok == b.tok && a.head == b.head; }
 
@@ -125,7 +147,7 @@ kvs_status kvs_rotate(const kvs_rope* rope, const void* d_q, long long q_stride,
   // rows are written while others are still read: in place, or apart
   for (int o = 0; o < 2; ++o)
     for (int i = 0; i < 2; ++i)
-      if (n[o] && n[i] && ((may_meet(out[o], in[i]) && !(o == i && same(out[o], in[i]))) || (o < i && may_meet(out[o], out[i]))))
+      if (n[o] && n[i] && ((!(o == i && same(out[o], in[i])) && may_meet(out[o], in[i])) || (o < i && may_meet(out[o], out[i]))))
         return KVS_ERR_INVALID_ARG;
   RopeRows a = {};
   a.q = {static_cast<const __nv_bfloat16*>(d_q), static_cast<__nv_bfloat16*>(d_q_out), q_stride, q_head_stride, q_out_stride,
