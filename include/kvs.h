@@ -473,9 +473,11 @@ kvs_status kvs_pool_evict(kvs_pool* pool, int layer, const float* d_weight, cons
  *   place [n_tok] int64   slot * block_size + offset of the token's K/V rows; -1: none (a position p < 0, a token of no
  *                         request, a block that was lacking)
  *   pos [n_tok] int32     p + pos_delta[r] (pos_delta may be NULL: 0); 0 for tokens of no request.  May be NULL
- * These serve every layer of the step.  A length outside [0, max_ctx], a count outside [0, nb_max], a ring state or
- * offsets that cannot be, or a slot outside the pool is reported as KVS_ERR_BAD_INDEX; the row keeps its blocks and its
- * tokens get no place (a ring state that cannot be changes nothing at all).  Buffers must not overlap.
+ * These serve every layer of the step.  A length outside [0, max_ctx], a count outside [0, nb_max], or a ring state or
+ * offsets that cannot be are reported as KVS_ERR_BAD_INDEX; the row keeps its blocks and its tokens get no place (a ring
+ * state that cannot be changes nothing at all).  So is a slot outside the pool that is taken, given back or holds a token
+ * of the call: it is moved as it is, and its tokens get no place.  (Slots of rows that keep their blocks are looked at
+ * where a token lies in them.)  Buffers must not overlap.
  *
  * kvs_pool_places is the second half alone, for tables that are kept in another way. */
 kvs_status kvs_pool_reserve(kvs_pool* pool, const int* d_ctx_len, int* d_n_held, int* d_block2slot, int* d_ring, int* d_ring_state,

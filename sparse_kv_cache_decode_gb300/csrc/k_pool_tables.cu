@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kTabThreads)
     return t.ring + (at < d.n_slots ? at : at - d.n_slots);
   };
   if (change) {
+    bool lost = false;      // a slot outside the pool, in the ring or a row: it is moved as it is
     const int taken = (int)min(all_take, (unsigned)n_free);
     for (int i0 = first; i0 < taken; i0 += stride * kTabDeep) {
       int slot[kTabDeep];
@@ -173,6 +174,7 @@ __global__ void __launch_bounds__(kTabThreads)
         const int i = i0 + k * stride;
         if (i >= taken) break;
         const int r = last_at(takes, n, i);
+        lost |= (unsigned)slot[k] >= (unsigned)d.n_slots;
         t.table[(size_t)r * d.nb_max + held[r] + (i - takes[r])] = slot[k];
       }
     }
@@ -190,6 +192,7 @@ __global__ void __launch_bounds__(kTabThreads)
       for (int k = 0; k < kTabDeep; ++k) {
         const int j = j0 + k * stride, i = n_free + j;
         if (j >= (int)all_give) break;
+        lost |= (unsigned)slot[k] >= (unsigned)d.n_slots;
         *ring_at(i) = slot[k];
         if (i < (int)all_take) {
           const int to = last_at(takes, n, i);
@@ -197,6 +200,7 @@ __global__ void __launch_bounds__(kTabThreads)
         }
       }
     }
+    if (lost) set_error(err, KVS_ERR_BAD_INDEX);
   }
   if (!t.cu_q) return;
   // the slot of a request's block, or -1 where it has none
