@@ -156,12 +156,16 @@ struct Parser {
     if (t->dim() != 1 || t->size(0) != n || !t->is_contiguous()) ok = false;
     return static_cast<T*>(t->data_ptr());
   }
+  // [n], or [n_axis] rows of [n] that may be parts of longer ones
   const int* positions(PyObject* o, long long n_axis, long long n, long long* stride) {
     const at::Tensor* t = take(o, at::kInt, at::kInt);
     if (!t) return nullptr;
-    const bool one = t->dim() == 1;
-    if (!t->is_contiguous() || t->size(-1) != n || !(one || (t->dim() == 2 && t->size(0) == n_axis))) ok = false;
-    *stride = one || n_axis == 1 ? 0 : n;
+    const auto dim = t->dim();
+    if (dim < 1 || dim > 2 || t->size(dim - 1) != n || (dim == 2 && t->size(0) != n_axis) || (n > 1 && t->stride(dim - 1) != 1)) {
+      ok = false;
+      return nullptr;
+    }
+    *stride = dim == 1 || n_axis == 1 ? 0 : t->stride(0);
     return static_cast<const int*>(t->data_ptr());
   }
   template <typename T>
