@@ -141,9 +141,12 @@ def binding():
         import importlib.util
 
         import torch  # noqa: F401  (its libraries, which the module links to)
+
+        from . import build
         lib()
-        if not os.path.exists(BINDING_PATH):
-            raise RuntimeError(f"kvs_binding.so is not built ({BINDING_PATH}); run __graft_entry__.build()")
+        if not os.path.exists(BINDING_PATH) or not build.binding_fits():
+            raise RuntimeError(f"kvs_binding.so is not built for this torch and Python ({BINDING_PATH}); run __graft_entry__.build() (it needs a torch "
+                               "with CUDA and Python's headers)")
         loader = importlib.machinery.ExtensionFileLoader("kvs_binding", BINDING_PATH)
         m = importlib.util.module_from_spec(importlib.util.spec_from_loader("kvs_binding", loader))
         loader.exec_module(m)

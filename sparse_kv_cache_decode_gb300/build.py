@@ -42,9 +42,34 @@ def _run(cmd, what):
 
 
 def _torch():
-    """torch's folder; None without torch, where the ctypes binding of the C ABI is all there is."""
+    """torch's folder; None where the compiled binding has nothing to be built against (no torch with CUDA, no headers of Python): libkvs.so is
+    then all that is built."""
     spec = importlib.util.find_spec("torch")
-    return spec.submodule_search_locations[0] if spec else None
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    torch = spec.submodule_search_locations[0]
+    needed = [os.path.join(torch, "lib", "libc10_cuda.so"), os.path.join(torch, "lib", "libtorch_python.so"),
+              os.path.join(torch, "include", "c10", "cuda", "CUDAFunctions.h"), os.path.join(sysconfig.get_paths()["include"], "Python.h")]
+    return torch if all(os.path.exists(f) for f in needed) else None
+
+
+def _binding_key(torch):
+    """What the binding's layout of tensors and of Python's objects hangs on: this torch and this Python."""
+    version = os.path.join(torch, "version.py")
+    return "\n".join([torch, open(version).read() if os.path.exists(version) else "", str(sysconfig.get_config_var("SOABI"))])
+
+
+def _key_file():
+    return BINDING + ".key"
+
+
+def binding_fits():
+    """Whether kvs_binding.so was built for this torch and this Python."""
+    torch = _torch()
+    if torch is None or not os.path.exists(_key_file()):
+        return False
+    with open(_key_file()) as f:
+        return f.read() == _binding_key(torch)
 
 
 def _compile_binding():
@@ -52,31 +77,35 @@ def _compile_binding():
     torch = _torch()
     if torch is None:
         return None
-    if _stale(obj, [src] + headers()):
+    if _stale(obj, [src] + headers()) or not binding_fits():
         cuda = os.path.dirname(os.path.dirname(NVCC))
         inc = [f"-I{torch}/include", f"-I{torch}/include/torch/csrc/api/include", f"-I{cuda}/include", f"-I{sysconfig.get_paths()['include']}"]
-        _run(["g++", "-O2", "-std=c++17", "-fPIC"] + inc + ["-c", src, "-o", obj + ".tmp"], src)
-        os.replace(obj + ".tmp", obj)
+        tmp = obj + f".tmp{os.getpid()}"
+        _run(["g++", "-O2", "-std=c++17", "-fPIC"] + inc + ["-c", src, "-o", tmp], src)
+        os.replace(tmp, obj)
     return obj
 
 
 def _link_binding(obj):
-    if obj is not None and _stale(BINDING, [obj]):
-        tmp = BINDING + f".tmp{os.getpid()}"
-        torch = _torch()
+    if obj is not None and (_stale(BINDING, [obj]) or not binding_fits()):
+        torch, tmp = _torch(), BINDING + f".tmp{os.getpid()}"
         _run(["g++", "-shared", "-o", tmp, obj, f"-L{OUT_DIR}", "-lkvs", "-Wl,-rpath,$ORIGIN", f"-L{torch}/lib", "-ltorch_python", "-ltorch_cpu",
               "-lc10", "-lc10_cuda"], BINDING)
         os.replace(tmp, BINDING)
+        with open(tmp, "w") as f:
+            f.write(_binding_key(torch))
+        os.replace(tmp, _key_file())
 
 
 def _compile(src):
     obj = os.path.join(OUT_DIR, os.path.basename(src)[:-3] + ".o")
     if _stale(obj, [src] + headers()):
-        cmd = [NVCC] + ARCH + FLAGS + ["-c", src, "-o", obj + ".tmp"]
+        tmp = obj + f".tmp{os.getpid()}"
+        cmd = [NVCC] + ARCH + FLAGS + ["-c", src, "-o", tmp]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
-        os.replace(obj + ".tmp", obj)
+        os.replace(tmp, obj)
     return obj
 
 
