@@ -58,7 +58,11 @@ PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return Py_BuildValue("(NLLLL)", pointer(*t), s0, s1, tok, h);
 }
 
-PyObject* device(PyObject*, PyObject*) { return PyLong_FromLong(c10::cuda::current_device()); }
+// the current device, or -1 without one
+PyObject* device(PyObject*, PyObject*) {
+  c10::DeviceIndex i = -1;
+  return PyLong_FromLong(c10::cuda::GetDevice(&i) == cudaSuccess ? i : -1);
+}
 PyObject* stream(PyObject*, PyObject* index) {
   const long i = PyLong_AsLong(index);
   if (i == -1 && PyErr_Occurred()) return nullptr;

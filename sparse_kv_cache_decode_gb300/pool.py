@@ -50,9 +50,9 @@ def make_pool_config(n_layer: int, n_slots: int, n_q_head: int, n_kv_head: int, 
 class Pool:
     """A kvs_pool over K and V tensors of the caller, with its device workspace (allocated through torch): keep it, and every
     tensor of a call, until the calls on them are through."""
+    h = _address = None       # the handle (None: closed), and its address
 
     def __init__(self, cfg: KvsPoolConfig, k: torch.Tensor, v: torch.Tensor):
-        self.h = None
         self.cfg = cfg
         self.L = calls
         nbytes = self.L.kvs_pool_workspace_bytes(ctypes.byref(cfg))
@@ -74,12 +74,12 @@ class Pool:
             h = ctypes.c_void_p()
             _check(self.L.kvs_pool_create(ctypes.byref(cfg), k.data_ptr(), v.data_ptr(), aligned, nbytes,
                                           ctypes.byref(h)), "kvs_pool_create")
-        self.h = h
+        self.h, self._address = h, h.value
 
     def close(self):
-        if getattr(self, "h", None):
+        if self.h is not None:
             self.L.kvs_pool_destroy(self.h)
-            self.h = None
+            self.h = self._address = None
 
     def __del__(self):
         try:
@@ -137,7 +137,7 @@ class Pool:
     def _call(self, fn, where, *args):
         if self.h is None:
             raise ValueError("Pool: closed")
-        if self.index < 0 or _fast.device() == self.index:
+        if _fast.device() == self.index:
             status = fn(self.h, *args)
         else:
             with torch.cuda.device(self.index):
@@ -218,7 +218,7 @@ class Pool:
         """kvs_pool_rotate_append: q [n_tok][H_q][d] normed and rotated into q_out; k and v [n_tok][H_kv][d] to their places, k normed and
         rotated as well."""
         hq, hk, d = self._heads
-        if self.L is calls and self.h is not None and type(rope) is Rope and rope.h is not None:
+        if self.h is not None and type(rope) is Rope and rope.h is not None:
             status = _fast.rotate_append(self._address, rope.address, self.index, hq, hk, d, rope.n_axis, layer, q, k, v, pos, place, q_out, q_norm, k_norm, stream)
             if status == 0:
                 return
@@ -239,10 +239,6 @@ class Pool:
         qn, kn = _norm(q_norm, "q_norm", d, i), _norm(k_norm, "k_norm", d, i)
         self._call(self.L.kvs_pool_rotate_append, "kvs_pool_rotate_append", h, _int(layer, "layer"), a[0], a[1], b[0], c[0], b[1], qn, kn, pp, ps, pl,
                    n_tok, o[0], o[1], _fast.stream(i) if stream is None else self._stream(stream))
-
-    @functools.cached_property
-    def _address(self):
-        return self.h.value
 
     @functools.cached_property
     def _heads(self):
@@ -292,7 +288,7 @@ class BlockTables:
         """kvs_pool_reserve: every row gets the blocks of its new length, or gives back those past it; with cu_q and place also where the
         call's tokens go, and their positions."""
         p, n_req = self.pool, self.n_req
-        if p.L is calls and p.h is not None:
+        if p.h is not None:
             status = _fast.reserve(p._address, p.index, n_req, *self._ptrs, ctx_len, cu_q, place, pos, pos_delta, stream)
             if status == 0:
                 return
