@@ -397,8 +397,9 @@ typedef struct kvs_pool kvs_pool;
 size_t kvs_pool_workspace_bytes(const kvs_pool_config* cfg);
 
 /* Bind a pool to its K/V memory (256-byte aligned device pointers, apart, both of n_layer * n_slots * H_kv *
- * block_size * head_dim elements; never written but by kvs_pool_append and kvs_pool_evict) and to a
- * workspace (>= kvs_pool_workspace_bytes, 256-byte aligned).  Synchronous; on the current device. */
+ * block_size * head_dim elements; never written but by kvs_pool_append, kvs_pool_rotate_append, kvs_pool_evict and, K
+ * alone, kvs_pool_reposition) and to a workspace (>= kvs_pool_workspace_bytes, 256-byte aligned).  Synchronous; on the
+ * current device. */
 kvs_status kvs_pool_create(const kvs_pool_config* cfg, void* d_k, void* d_v, void* d_workspace,
                            size_t workspace_bytes, kvs_pool** out);
 kvs_status kvs_pool_destroy(kvs_pool* pool);
