@@ -491,10 +491,11 @@ kvs_status kvs_pool_places(kvs_pool* pool, const int* d_cu_q, const int* d_ctx_l
  *   y = x / sqrt(mean(x^2) + norm_eps) * w          (with a norm weight w [head_dim] fp32; else y = x)
  *   (y_a, y_b) -> rot_scale (y_a cos t - y_b sin t, y_b cos t + y_a sin t),   t = pos[axis[i]] * inv_freq[i]
  * for the pairs i = 0 .. rot_dim / 2 - 1 of its first rot_dim elements: (a, b) = (2 i, 2 i + 1) if adjacent, else
- * (i, i + rot_dim / 2).  A token has a position on each of n_axis axes (time, height and width of an image's patch, say), and each pair
- * turns by one of them.  Positions are any int32; cosines and sines are good to 2^-20, and the
- * angle to 2^-52 of its size.  The sum of a normed row's squares must be finite in fp32.  A row's result
- * does not depend on the other rows of a call. */
+ * (i, i + rot_dim / 2).  A token has a position on each of n_axis axes (time, height and width of an image's patch, say),
+ * and each pair turns by one of them.  Positions are any int32.  Angles are off by |pos| (2^-51 |inv_freq| / (2 pi) + 2^-64)
+ * + 2^-32 turns at most (2^-32 turns: 1.5e-9 radians), and their cosines and sines by 2^-20.  The sum of a normed row's
+ * squares must be finite in fp32, and with a norm_eps of 0 not vanish.  A row's result does not depend on the other rows of
+ * a call. */
 typedef struct {
   int head_dim;                 /* 64, 128 or 256 (a pool's own for the calls on a pool) */
   int rot_dim;                  /* a multiple of 16, at most head_dim; 0: no rotation */
@@ -514,21 +515,23 @@ kvs_status kvs_rope_create(const kvs_rope_config* cfg, kvs_rope** out);
 kvs_status kvs_rope_destroy(kvs_rope* rope);
 
 /* The heads of queries and of keys of n_tok tokens, as above: for kvs_decode_step (its q and k_new), an index of one's own,
- * or the part of a latent row that turns.  Token t's head h is at d_x + t * x_stride + h * x_head_stride (elements: multiples of 8;
- * rows 16-byte aligned, not overlapping); norms [head_dim] fp32, 16-byte aligned, or NULL; n_q_head or n_k_head may be 0 (its pointers
- * are not used), at most 1024.  Launches on the current device.  pos: n_axis rows of [n_tok] int32, pos_stride apart (0: one row for all axes).  Outputs are
- * written in place (the same pointer and strides) or apart from the inputs and from one another. */
+ * or the part of a latent row that turns.  Token t's head h is at d_x + t * x_stride + h * x_head_stride (elements:
+ * multiples of 8; rows 16-byte aligned, not overlapping); norms [head_dim] fp32, 16-byte aligned, or NULL; n_q_head or
+ * n_k_head may be 0 (its pointers are not used), at most 1024.  pos: n_axis rows of [n_tok] int32, pos_stride apart (0: one
+ * row for all axes).  Outputs are written in place (the same pointer and strides) or apart from the inputs and from one
+ * another: as a whole, between the rows of one of the same strides, or in other columns of tokens of the same stride.
+ * Launches on the current device. */
 kvs_status kvs_rotate(const kvs_rope* rope, const void* d_q, long long q_stride, long long q_head_stride, int n_q_head,
                       const float* d_q_norm, void* d_q_out, long long q_out_stride, long long q_out_head_stride, const void* d_k,
                       long long k_stride, long long k_head_stride, int n_k_head, const float* d_k_norm, void* d_k_out,
                       long long k_out_stride, long long k_out_head_stride, const int* d_pos, long long pos_stride, int n_tok,
                       kvs_stream_t stream);
 
-/* The same with K and V on their way into a pool, in one pass: d_q [n_tok] tokens of [H_q][d], q_stride elements apart, is normed and
- * rotated into d_q_out (q_out_stride; in place, or apart from q, k and v), d_k and d_v [n_tok] tokens of [H_kv][d],
- * kv_stride apart, go to place[t] (of kvs_pool_reserve, distinct), k normed and rotated, v as it is.  E4M3 pools round k's fp32 values
- * and v's bf16 ones once, by the rule of kvs_quantize_e4m3.  A token without a place (-1) has its q written and its K/V passed
- * over; a place outside the pool is reported as KVS_ERR_BAD_INDEX and passed over. */
+/* The same with K and V on their way into a pool, in one pass: d_q [n_tok] tokens of [H_q][d], q_stride elements apart, is
+ * normed and rotated into d_q_out (q_out_stride; in place, or apart from q, k and v), d_k and d_v [n_tok] tokens of
+ * [H_kv][d], kv_stride apart, go to place[t] (of kvs_pool_reserve, distinct), k normed and rotated, v as it is.  E4M3 pools
+ * round k's fp32 values and v's bf16 ones once, by the rule of kvs_quantize_e4m3.  A token without a place (-1) has its q
+ * written and its K/V passed over; a place outside the pool is reported as KVS_ERR_BAD_INDEX and passed over. */
 kvs_status kvs_pool_rotate_append(kvs_pool* pool, const kvs_rope* rope, int layer, const void* d_q, long long q_stride,
                                   const void* d_k, const void* d_v, long long kv_stride, const float* d_q_norm,
                                   const float* d_k_norm, const int* d_pos, long long pos_stride, const long long* d_place,

@@ -1,9 +1,10 @@
 // Norms and rotation of query and key rows, dense or into a pool, and the repositioning of cached keys.
 //
 // A head's d elements lie in d / 16 lanes, two chunks of 8 elements (16 bytes) each, chosen so that both elements of every
-// rotated pair are in one lane: no exchange but the norm's sum.  Pair i of a row turns by pos * f_i.  The angle is kept in
-// turns, as an integer multiple of 2^-64: pos * f_i wraps around at whole turns by itself, exactly, for any 32-bit position
-// (fp32 products lose the angle beyond some thousand positions); its upper 32 bits are off by less than 2^-32 turns.
+// rotated pair are in one lane: no exchange but the norm's sum.  Pair i of a row turns by pos * f_i.  The frequency is kept in
+// turns, as an integer multiple of 2^-64: its product with any 32-bit position wraps around at whole turns by itself, exactly
+// (fp32 products lose the angle beyond some thousand positions).  What is lost: the frequency's own rounding (2^-51 of it and
+// 2^-64) times the position, and less than 2^-32 turns below the product's upper 32 bits.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -15,9 +16,11 @@ namespace kvs {
 
 namespace {
 
-// cos and sin of m * f turns, two of them (two_pi: its sign is the angle's).  The product's upper word, a turn's fraction, becomes a float in [1, 2) by its upper 23
-// bits, rounded (a conversion would take the unit that the cosines need); the fast functions are off by 2^-21 for arguments in
-// [-pi, pi].  Together 2^-20 at most.
+// cos and sin of m * f turns, two of them (two_pi: its sign is the angle's).  The product's upper word, a turn's fraction,
+// becomes a float in [1, 2) by its upper 23 bits, rounded (a conversion would take the unit that the cosines need): off by
+// 2^-24 turns, 2^-21.3.  The fast functions are off by 2^-21 for arguments in [-pi, pi].  Together 2^-20 at most, beside which the
+// stored types' half steps are 2^-8 and 2^-4: the errors of results are the same as with exact cosines, and at most one E4M3
+// code in 80,000, within 2^-21 of its row's largest value from a tie, is rounded to the other side.
 constexpr float kTwoPi = 6.2831853f;
 __device__ __forceinline__ float turn_bits(unsigned m, unsigned long long f) {      // 1.5 + the fraction's distance from whole turns
   const unsigned t = __umulhi(m, (unsigned)f) + (m * (unsigned)(f >> 32) + 0x80000100u);      // half a turn on, and half a step
@@ -30,8 +33,8 @@ __device__ __forceinline__ void turn_cos_sin(unsigned m, float two_pi, unsigned 
 }
 __device__ __forceinline__ unsigned magnitude(int pos) { return pos < 0 ? 0u - (unsigned)pos : (unsigned)pos; }
 
-// The parameters by their address: lanes that read entries of their own take one load, where an indexed read of the constant bank is
-// repeated for every lane (128 tokens of 12 steps 3.0 us that way, 2.45 by address; one token 1.83 and 1.65).
+// The parameters by their address: lanes that read entries of their own take one load, where an indexed read of the constant
+// bank is repeated for every lane (128 tokens of 12 steps 3.0 us that way, 2.45 by address; one token 1.83 and 1.65).
 template <typename T>
 __device__ __forceinline__ const T* by_address(const T& rd) {
   const T* p = &rd;
@@ -260,10 +263,10 @@ __device__ __forceinline__ PlaceRow place_row(const RopeRows& a, long long place
   return p;
 }
 
-// Few tokens: a warp per step, everything it needs on its way at once.  One token of 32 + 2 x 8 heads into a bf16 pool: 1.65 us (3.3 with a
-// loop over the token's steps), about the time of a launch.  From some 16 steps for each SM on, where the other kernel's warps have one
-// each, its sharing of a token's angles wins: 128 tokens (1536 steps) 2.4 us here and 2.8 there, 256 3.7 and 3.15; of 3 steps each,
-// 512 tokens 2.0 and 2.3, 2048 4.1 and 3.6.
+// Few tokens: a warp per step, everything it needs on its way at once.  One token of 32 + 2 x 8 heads into a bf16 pool: 1.65 us
+// (3.3 with a loop over the token's steps), about the time of a launch.  From some 16 steps for each SM on, where the other
+// kernel's warps have one each, its sharing of a token's angles wins: 128 tokens (1536 steps) 2.4 us here and 2.8 there, 256 3.7
+// and 3.15; of 3 steps each, 512 tokens 2.0 and 2.3, 2048 4.1 and 3.6.
 constexpr int kFewThreads = 128;
 constexpr int kFewSteps = 16;      // steps for each SM, at most
 
@@ -331,11 +334,11 @@ __global__ void __launch_bounds__(kFewThreads)
 // Many tokens: the warps take whole tokens in turn, then equal runs of the steps left over.  The steps' rows come through a ring in
 // shared memory, kStages - 1 steps ahead, in which every lane reads what it has copied itself.
 //
-// Bound by the rows' bytes, 3 KB on their way a warp; the norm's weights and the rotation are one set of factors, made once for a token's
-// queries and once for its keys, so that a row costs 8 multiplications and 16 fused ones for 16 elements (in pairs).
-// 16384 tokens of 32 + 2 x 8 heads of 128 into a bf16 pool: 66 us, 6.1 TB/s (59.3 at the rate of a copy).  Rows loaded into registers a
-// step ahead took 83 us, three steps ahead 70; every warp at a run of its own (far from its neighbours') 70; 3 CTAs an SM with
-// 80 registers 75.  11308 tokens of 28 + 4 heads, no norm: 31 us (27.3).
+// Bound by the rows' bytes, 3 KB on their way a warp; the norm's weights and the rotation are one set of factors, made once for
+// a token's queries and once for its keys, so that a row costs 8 multiplications and 16 fused ones for 16 elements (in pairs).
+// 16384 tokens of 32 + 2 x 8 heads of 128 into a bf16 pool: 66 us, 6.1 TB/s (59.3 at the rate of a copy).  Rows loaded into
+// registers a step ahead took 83 us, three steps ahead 70; every warp at a run of its own (far from its neighbours') 70; 3 CTAs
+// an SM with 80 registers 75.  11308 tokens of 28 + 4 heads, no norm: 31 us (27.3).
 constexpr int kRopeThreads = 256;
 constexpr int kStages = 4;
 constexpr int kRopeCtas = 2;       // of an SM
@@ -519,10 +522,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
 //
 // Every key has angles of its own: 16 cosines and sines a lane and step, at 16 a clock of an SM 32 clocks, beside which some 180
 // instructions a step take 45 of each scheduler's: more than an 8-bit row's bytes (a step's 1 KB: 44 clocks at the rate of a copy).
-// 32 x 8 heads x 4096 keys of 128, E4M3: 62.0 us (40.2 for the bytes), the schedulers 69% busy, the same with 24 to 32 warps an SM and 3
-// or 4 stages; one step a warp took 132, four at once and no ring 74.  Angles by fused fp32 multiplications of a split frequency, fewer
-// instructions than in integers, took 67: packed or not they use the unit that the rotation needs.  Lanes of 32 elements took 70.7 (120
-// registers, 16 warps an SM).
+// 32 x 8 heads x 4096 keys of 128, E4M3: 62.0 us (40.2 for the bytes), the schedulers 69% busy, the same with 24 to 32 warps an
+// SM and 3 or 4 stages; one step a warp took 132, four at once and no ring 74.  Angles by fused fp32 multiplications of a split
+// frequency, fewer instructions than in integers, took 67: packed or not they use the unit that the rotation needs.  Lanes of 32
+// elements took 70.7 (120 registers, 16 warps an SM).
 // 8 x 8 x 2048 keys, bf16, half of them in L2: 5.8 us.
 constexpr int kRepThreads = 128;
 
