@@ -271,13 +271,17 @@ __global__ void __launch_bounds__(kTabThreads)
 }  // namespace
 
 cudaError_t launch_pool_tables(const PoolDims& d, const PoolTables& t, unsigned* ticket, unsigned* err, cudaStream_t s) {
-  // A thread places one token (a batch's next tokens), or four where there are two for every thread of the GPU; a call without tokens
-  // may move as many blocks as the tables hold, and mostly moves few: 64 CTAs for large tables (500 requests that give 190 blocks
-  // back: 4.1 us with 1 to 64 CTAs, 4.4 with 244; 24 that give back 7700: 13 us with 1, 4 with 12).
+  // A thread places one token (a batch's next tokens), or four where there are two for every thread of the GPU.  A call may move
+  // as many blocks as the tables hold, and mostly moves few: up to 64 CTAs for large tables, with tokens or without (500 requests
+  // that give 190 blocks back: 4.1 us with 1 to 64 CTAs, 4.4 with 244; 24 that give 7700: 13 us with 1, 4 with 12; 64 requests
+  // of a token each, of which 8 end and give 16384 back, and the call that takes them again: 39 us with 1, 10.5 with 8, 7.1 with 64,
+  // and 5.9 or 6.0 if none ends).
   const int sms = device_sm_count(), smem = (7 * t.n_req + 3) * 4;
   const bool many = t.n_tok > sms * kTabThreads * 2;
-  const long long work = t.cu_q ? t.n_tok / (many ? 4 : 1) : (long long)t.n_req * d.nb_max / 4;
-  const int grid = (int)std::max(1ll, std::min<long long>((work + kTabThreads - 1) / kTabThreads, t.cu_q ? sms * 4 : 64));
+  auto ctas = [](long long threads, int most) { return (int)std::min<long long>((threads + kTabThreads - 1) / kTabThreads, most); };
+  const int for_tokens = t.cu_q ? ctas(t.n_tok / (many ? 4 : 1), sms * 4) : 0;
+  const int for_blocks = t.ring ? ctas((long long)t.n_req * d.nb_max / 4, 64) : 0;
+  const int grid = std::max({1, for_tokens, for_blocks});
   auto go = [&](auto kernel) {
     cudaError_t e = cudaSuccess;      // (up to 47 KB need no asking)
     if (smem > 47 * 1024) e = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), (7 * kPoolMaxReq + 3) * 4);
