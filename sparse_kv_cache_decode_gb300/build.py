@@ -41,22 +41,26 @@ def _run(cmd, what):
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
+def _torch_folder():
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec is not None and spec.submodule_search_locations else None
+
+
 def _torch():
     """torch's folder; None where the compiled binding has nothing to be built against (no torch with CUDA, no headers of Python): libkvs.so is
     then all that is built."""
-    spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.submodule_search_locations:
+    torch = _torch_folder()
+    if torch is None:
         return None
-    torch = spec.submodule_search_locations[0]
     needed = [os.path.join(torch, "lib", "libc10_cuda.so"), os.path.join(torch, "lib", "libtorch_python.so"),
               os.path.join(torch, "include", "c10", "cuda", "CUDAFunctions.h"), os.path.join(sysconfig.get_paths()["include"], "Python.h")]
     return torch if all(os.path.exists(f) for f in needed) else None
 
 
-def _binding_key(torch):
+def _binding_key():
     """What the binding's layout of tensors and of Python's objects hangs on: this torch and this Python."""
-    version = os.path.join(torch, "version.py")
-    return "\n".join([torch, open(version).read() if os.path.exists(version) else "", str(sysconfig.get_config_var("SOABI"))])
+    version = os.path.join(_torch_folder() or "", "version.py")
+    return "\n".join([open(version).read() if os.path.exists(version) else "", str(sysconfig.get_config_var("SOABI"))])
 
 
 def _key_file():
@@ -65,11 +69,10 @@ def _key_file():
 
 def binding_fits():
     """Whether kvs_binding.so was built for this torch and this Python."""
-    torch = _torch()
-    if torch is None or not os.path.exists(_key_file()):
+    if not os.path.exists(_key_file()):
         return False
     with open(_key_file()) as f:
-        return f.read() == _binding_key(torch)
+        return f.read() == _binding_key()
 
 
 def _compile_binding():
@@ -93,7 +96,7 @@ def _link_binding(obj):
               "-lc10", "-lc10_cuda"], BINDING)
         os.replace(tmp, BINDING)
         with open(tmp, "w") as f:
-            f.write(_binding_key(torch))
+            f.write(_binding_key())
         os.replace(tmp, _key_file())
 
 

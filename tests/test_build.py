@@ -58,21 +58,32 @@ def test_it_is_made_once(world):
     assert sorted(os.listdir(B.OUT_DIR)) == ["binding.o", "kvs_binding.so", "kvs_binding.so.key"]
 
 
-@pytest.mark.parametrize("what", ["version", "folder", "python"])
+@pytest.mark.parametrize("what", ["version", "python"])
 def test_another_torch_or_python_makes_it_again(world, monkeypatch, what):
     make()
     if what == "version":
         with open(os.path.join(world.torch, "version.py"), "w") as f:
             f.write("__version__ = '3.0'")
-    elif what == "folder":
-        os.rename(world.torch, world.torch + "2")
-        world.spec.submodule_search_locations = [world.torch + "2"]
     else:
         get = B.sysconfig.get_config_var
         monkeypatch.setattr(B.sysconfig, "get_config_var", lambda name: "cpython-399" if name == "SOABI" else get(name))
     assert not B.binding_fits()
     make()
     assert len(world.ran) == 4 and B.binding_fits()
+
+
+@pytest.mark.parametrize("gone", ["headers", "folder"])
+def test_a_built_binding_needs_no_headers(world, gone):
+    """A machine that only runs it: without Python's headers, or with the same torch in another place."""
+    make()
+    if gone == "headers":
+        os.remove(os.path.join(world.include, "Python.h"))
+    else:
+        os.rename(world.torch, world.torch + "2")
+        world.spec.submodule_search_locations = [world.torch + "2"]
+    assert B.binding_fits()
+    make()
+    assert len(world.ran) == 2
 
 
 def test_a_build_that_ends_half_way_is_done_again(world, monkeypatch):
